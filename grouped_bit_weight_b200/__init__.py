@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -19,8 +20,9 @@ __all__ = [
     "gnf4_grouped_dgrad", "gmxfp4_grouped_dgrad", "gnf4_grouped_expert_mlp",
     "gmxfp4_grouped_expert_mlp", "gnf4_grouped_expert_mlp_noalloc", "gnf4_dequant",
     "gmxfp4_dequant", "gnf4_quantize",
-    "gmxfp4_quantize", "device_status", "MODE_AUTO", "MODE_GEMM", "MODE_GEMV",
-    "DEVERR_OFFSETS", "DEVERR_TOKEN", "DEVERR_TIMEOUT", "FLAG_OVERLAP_PREV",
+    "gmxfp4_quantize", "Routing", "gmoe_route", "gmoe_route_bwd", "gmoe_combine",
+    "gmoe_combine_bwd", "device_status", "MODE_AUTO", "MODE_GEMM", "MODE_GEMV",
+    "DEVERR_OFFSETS", "DEVERR_TOKEN", "DEVERR_TIMEOUT", "DEVERR_ROUTE", "FLAG_OVERLAP_PREV",
     "EXPORTS",
 ]
 
@@ -36,7 +38,8 @@ lib = C.CDLL(LIB_PATH)
 
 MODE_AUTO, MODE_GEMM, MODE_GEMV = 0, 1, 2
 FLAG_OVERLAP_PREV = 0x100
-DEVERR_OFFSETS, DEVERR_TOKEN, DEVERR_TIMEOUT = 1, 2, 4
+DEVERR_OFFSETS, DEVERR_TOKEN, DEVERR_TIMEOUT, DEVERR_ROUTE = 1, 2, 4, 8
+LOGITS_BF16, LOGITS_FP32 = 0, 1
 _STATUS = {0: "GBW_OK", 1: "GBW_ERR_NULL", 2: "GBW_ERR_SHAPE",
            3: "GBW_ERR_ALIGN", 4: "GBW_ERR_ARCH", 5: "GBW_ERR_LAUNCH",
            6: "GBW_ERR_DEVICE"}
@@ -56,6 +59,11 @@ EXPORTS = {
     "gmxfp4_dequant": (C.c_int, [_P, _P, _I64, _I64, _P, _P]),
     "gnf4_quantize": (C.c_int, [_P, _I64, _I64, _P, _P, _P]),
     "gmxfp4_quantize": (C.c_int, [_P, _I64, _I64, _P, _P, _P]),
+    "gmoe_route": (C.c_int, [_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _I64, _P]),
+    "gmoe_route_workspace": (C.c_int64, [_I64, _I32]),
+    "gmoe_route_bwd": (C.c_int, [_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _P, _P, _P]),
+    "gmoe_combine": (C.c_int, [_P, _I64, _I64, _P, _P, _I64, _I32, _P, _P]),
+    "gmoe_combine_bwd": (C.c_int, [_P, _P, _I64, _I64, _P, _P, _P, _I64, _I32, _P, _P, _P]),
     "gbw_device_status": (C.c_int, [_P, C.POINTER(C.c_int32), _I32]),
     "gbw_status_string": (C.c_char_p, [C.c_int]),
     "gbw_version": (C.c_int32, []),
@@ -387,6 +395,144 @@ def gmxfp4_quantize(w):
         _check(lib.gmxfp4_quantize(_ptr(w), rows, K, _ptr(blocks), _ptr(scales),
                                    _stream(dev)), "gmxfp4_quantize")
     return blocks, scales
+
+
+class Routing(NamedTuple):
+    """What gmoe_route gives: the choice of each token and the expert-sorted
+    plan.  The grouped calls take expert_offsets and row_to_token."""
+    topk_ids: torch.Tensor        # [T, k] int32
+    topk_weights: torch.Tensor    # [T, k] fp32
+    expert_offsets: torch.Tensor  # [E + 1] int32
+    row_to_token: torch.Tensor    # [T * k] int32
+    row_of_slot: torch.Tensor     # [T, k] int32
+    slot_of_row: torch.Tensor     # [T * k] int32
+
+
+_LOGITS = {torch.bfloat16: LOGITS_BF16, torch.float32: LOGITS_FP32}
+
+
+def _logits(t, name, where):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _LOGITS:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    _need(t, name, t.dtype)
+    if t.dim() != 2:
+        raise ValueError(f"{where}: {name} must be [T, E]")
+
+
+def gmoe_route(logits, k, renormalize=True):
+    """Each token's k experts (largest logits, ties to the lowest index; NaN
+    counts as -inf), their softmax weights (over the chosen experts, or over
+    all with renormalize=False) and the plan of the routed rows, sorted by
+    expert: a Routing.  logits [T, E] bf16 or fp32."""
+    where = "gmoe_route"
+    _logits(logits, "logits", where)
+    T, E = logits.shape
+    k = int(k)
+    if not 1 <= k <= min(E, 32):
+        raise ValueError(f"{where}: k={k} must be in 1 .. min(E={E}, 32)")
+    if T * k > 0x7FFFFFFF:
+        raise ValueError(f"{where}: T * k must be below 2^31")
+    dev = _on_device(where, logits=logits)
+    i32 = {"dtype": torch.int32, "device": dev}
+    r = Routing(torch.empty((T, k), **i32), torch.empty((T, k), dtype=torch.float32, device=dev),
+                torch.empty(E + 1, **i32), torch.empty(T * k, **i32), torch.empty((T, k), **i32),
+                torch.empty(T * k, **i32))
+    need = lib.gmoe_route_workspace(T, E)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    with torch.cuda.device(dev):
+        _check(lib.gmoe_route(_ptr(logits), _LOGITS[logits.dtype], T, E, k, int(bool(renormalize)),
+                              *(_ptr(t) for t in r), _ptr(ws), need, _stream(dev)), where)
+    return r
+
+
+def gmoe_route_bwd(logits, topk_ids, topk_weights, dweights, renormalize=True):
+    """dlogits [T, E] (in the logits' type) from dweights [T, k], the gradient
+    of gmoe_route's topk_weights."""
+    where = "gmoe_route_bwd"
+    _logits(logits, "logits", where)
+    _need(topk_ids, "topk_ids", torch.int32)
+    _need(topk_weights, "topk_weights", torch.float32)
+    _need(dweights, "dweights", torch.float32)
+    T, E = logits.shape
+    k = topk_ids.shape[-1] if topk_ids.dim() == 2 else 0
+    for name, t in (("topk_ids", topk_ids), ("topk_weights", topk_weights),
+                    ("dweights", dweights)):
+        if tuple(t.shape) != (T, k) or not 1 <= k <= min(E, 32):
+            raise ValueError(f"{where}: {name} must be [T={T}, k], k in 1 .. min(E, 32)")
+    dev = _on_device(where, logits=logits, topk_ids=topk_ids, topk_weights=topk_weights,
+                     dweights=dweights)
+    out = torch.empty_like(logits)
+    with torch.cuda.device(dev):
+        _check(lib.gmoe_route_bwd(_ptr(logits), _LOGITS[logits.dtype], T, E, k,
+                                  int(bool(renormalize)), _ptr(topk_ids), _ptr(topk_weights),
+                                  _ptr(dweights), _ptr(out), _stream(dev)), where)
+    return out
+
+
+def _slots(where, y, row_of_slot, weights):
+    _need(y, "y", torch.bfloat16)
+    _need(row_of_slot, "row_of_slot", torch.int32)
+    if y.dim() != 2 or row_of_slot.dim() != 2:
+        raise ValueError(f"{where}: y must be [P, H] and row_of_slot [T, k]")
+    P, H = y.shape
+    T, k = row_of_slot.shape
+    if weights is not None:
+        _need(weights, "weights", torch.float32)
+        if tuple(weights.shape) != (T, k):
+            raise ValueError(f"{where}: weights must be [{T}, {k}]")
+    return P, H, T, k
+
+
+def gmoe_combine(y, row_of_slot, weights=None, out=None):
+    """out[t] = sum_s weights[t, s] * y[row_of_slot[t, s]]: the routed rows
+    y [P, H] bf16 of each token back into one [T, H] bf16, summed in fp32 in
+    slot order.  weights [T, k] fp32; None sums them unweighted (the routed
+    rows' dx back into their tokens)."""
+    where = "gmoe_combine"
+    P, H, T, k = _slots(where, y, row_of_slot, weights)
+    if out is not None:
+        _need(out, "out", torch.bfloat16)
+        if tuple(out.shape) != (T, H):
+            raise ValueError(f"{where}: out must be [{T}, {H}]")
+    dev = _on_device(where, y=y, row_of_slot=row_of_slot, weights=weights, out=out)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib.gmoe_combine(_ptr(y), P, H, _ptr(row_of_slot), _ptr(weights), T, k, _ptr(out),
+                                _stream(dev)), where)
+    return out
+
+
+def gmoe_combine_bwd(dout, y, row_of_slot, slot_of_row, weights, dy=None):
+    """(dy [P, H] bf16, dweights [T, k] fp32) of gmoe_combine for its output's
+    gradient dout [T, H] bf16.  slot_of_row [P] int32 is the inverse of
+    row_of_slot (gmoe_route gives both).  Rows that no slot names stay as they
+    are in `dy`; a dy made here has zeros there when P exceeds T * k."""
+    where = "gmoe_combine_bwd"
+    P, H, T, k = _slots(where, y, row_of_slot, weights)
+    if weights is None:
+        raise ValueError(f"{where}: weights are needed")
+    _need(dout, "dout", torch.bfloat16)
+    _need(slot_of_row, "slot_of_row", torch.int32)
+    if tuple(dout.shape) != (T, H):
+        raise ValueError(f"{where}: dout must be [{T}, {H}]")
+    _numel(slot_of_row, "slot_of_row", P, where)
+    if dy is not None:
+        _need(dy, "dy", torch.bfloat16)
+        if tuple(dy.shape) != (P, H):
+            raise ValueError(f"{where}: dy must be [{P}, {H}]")
+    dev = _on_device(where, dout=dout, y=y, row_of_slot=row_of_slot, slot_of_row=slot_of_row,
+                     weights=weights, dy=dy)
+    if dy is None:
+        dy = torch.empty_like(y) if P <= T * k else torch.zeros_like(y)
+    dw = torch.empty((T, k), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib.gmoe_combine_bwd(_ptr(dout), _ptr(y), P, H, _ptr(row_of_slot),
+                                    _ptr(slot_of_row), _ptr(weights), T, k, _ptr(dy), _ptr(dw),
+                                    _stream(dev)), where)
+    return dy, dw
 
 
 def device_status(device=None, clear=True) -> int:

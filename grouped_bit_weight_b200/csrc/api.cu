@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "launch.cuh"
 
 namespace gbw {
 namespace {
@@ -328,6 +329,126 @@ gbw_status gnf4_grouped_expert_mlp_noalloc(const uint16_t* x, int64_t T, int64_t
   // same call, so the array's previous contents never matter
   return expert_mlp(Fmt::NF4, x, T, H, gu_packed, gu_absmax, dn_packed, dn_absmax, E, I,
                     expert_offsets, row_to_token, P, g_noalloc_ptr[dev], out, mode, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Routing and combine
+// ---------------------------------------------------------------------------
+
+static gbw_status route_shape(int32_t type, int64_t T, int32_t E, int32_t k) {
+  if (type != GBW_LOGITS_BF16 && type != GBW_LOGITS_FP32)
+    return fail(GBW_ERR_SHAPE, "unknown type of logits");
+  if (T < 0 || E < 1 || k < 1) return fail(GBW_ERR_SHAPE, "need T >= 0, E >= 1, k >= 1");
+  if (E > kMaxExperts) return fail(GBW_ERR_SHAPE, "at most 1024 experts");
+  if (k > E || k > 32) return fail(GBW_ERR_SHAPE, "need k <= min(E, 32)");
+  if (T > INT32_MAX || T * k > INT32_MAX) return fail(GBW_ERR_SHAPE, "T * k must be below 2^31");
+  return GBW_OK;
+}
+
+int64_t gmoe_route_workspace(int64_t T, int32_t E) {
+  if (T < 0 || E < 1) return 0;
+  const int ctas = route_ctas(T, kMaxRouteCtas);
+  return ctas > 1 ? (int64_t)ctas * E * 4 : 0;
+}
+
+gbw_status gmoe_route(const void* logits, int32_t logits_type, int64_t T, int32_t E, int32_t k,
+                      int32_t renormalize, int32_t* topk_ids, float* topk_weights,
+                      int32_t* expert_offsets, int32_t* row_to_token, int32_t* row_of_slot,
+                      int32_t* slot_of_row, void* workspace, int64_t workspace_bytes,
+                      void* stream) {
+  gbw_status st = route_shape(logits_type, T, E, k);
+  if (st != GBW_OK) return st;
+  if (!expert_offsets) return fail(GBW_ERR_NULL, "NULL expert_offsets");
+  if (T > 0 && (!logits || !topk_ids || !topk_weights || !row_to_token || !row_of_slot ||
+                !slot_of_row))
+    return fail(GBW_ERR_NULL, "NULL logits or output");
+  const int64_t need = gmoe_route_workspace(T, E);
+  if (need > 0 && !workspace) return fail(GBW_ERR_NULL, "NULL workspace");
+  if (workspace_bytes < need) return fail(GBW_ERR_SHAPE, "workspace smaller than gmoe_route_workspace");
+  if ((reinterpret_cast<uintptr_t>(logits) & (logits_type == GBW_LOGITS_FP32 ? 3u : 1u)) ||
+      !aligned4(topk_ids) || !aligned4(topk_weights) || !aligned4(expert_offsets) ||
+      !aligned4(row_to_token) || !aligned4(row_of_slot) || !aligned4(slot_of_row) ||
+      !aligned4(workspace))
+    return fail(GBW_ERR_ALIGN, "logits must be aligned to their type, the rest to 4 bytes");
+  int* err = nullptr;
+  int sms = 0;
+  st = device_state(&err, &sms);
+  if (st != GBW_OK) return st;
+  const RouteProblem p{logits, logits_type == GBW_LOGITS_FP32, T, E, k, renormalize != 0, topk_ids,
+                       topk_weights, expert_offsets, row_to_token, row_of_slot, slot_of_row,
+                       static_cast<int32_t*>(workspace)};
+  const cudaError_t e = launch_route(p, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GBW_OK : launch_error(e);
+}
+
+gbw_status gmoe_route_bwd(const void* logits, int32_t logits_type, int64_t T, int32_t E, int32_t k,
+                          int32_t renormalize, const int32_t* topk_ids, const float* topk_weights,
+                          const float* dweights, void* dlogits, void* stream) {
+  gbw_status st = route_shape(logits_type, T, E, k);
+  if (st != GBW_OK) return st;
+  if (T > 0 && (!topk_ids || !topk_weights || !dweights || !dlogits || (!renormalize && !logits)))
+    return fail(GBW_ERR_NULL, "NULL argument");
+  const uintptr_t mask = logits_type == GBW_LOGITS_FP32 ? 3u : 1u;
+  if (((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dlogits)) & mask) ||
+      !aligned4(topk_ids) || !aligned4(topk_weights) || !aligned4(dweights))
+    return fail(GBW_ERR_ALIGN, "logits must be aligned to their type, the rest to 4 bytes");
+  int* err = nullptr;
+  int sms = 0;
+  st = device_state(&err, &sms);
+  if (st != GBW_OK) return st;
+  const cudaError_t e = launch_route_bwd(logits, logits_type == GBW_LOGITS_FP32, T, E, k,
+                                         renormalize != 0, topk_ids, topk_weights, dweights,
+                                         dlogits, err, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GBW_OK : launch_error(e);
+}
+
+static gbw_status combine_shape(int64_t P, int64_t H, int64_t T, int32_t k) {
+  if (P < 0 || H <= 0 || T < 0 || k < 1 || k > 32)
+    return fail(GBW_ERR_SHAPE, "need P >= 0, H > 0, T >= 0, 1 <= k <= 32");
+  if (H % 8) return fail(GBW_ERR_SHAPE, "H must be a multiple of 8");
+  if (H > (int64_t)1 << 30 || P > INT32_MAX || T > INT32_MAX || T * k > INT32_MAX)
+    return fail(GBW_ERR_SHAPE, "sizes exceed the 32-bit row indices");
+  return GBW_OK;
+}
+
+gbw_status gmoe_combine(const uint16_t* y, int64_t P, int64_t H, const int32_t* row_of_slot,
+                        const float* weights, int64_t T, int32_t k, uint16_t* out, void* stream) {
+  gbw_status st = combine_shape(P, H, T, k);
+  if (st != GBW_OK) return st;
+  if (T > 0 && ((P > 0 && !y) || !row_of_slot || !out)) return fail(GBW_ERR_NULL, "NULL argument");
+  if (!aligned16(y) || !aligned16(out)) return fail(GBW_ERR_ALIGN, "y and out must be 16-byte aligned");
+  if (!aligned4(row_of_slot) || !aligned4(weights))
+    return fail(GBW_ERR_ALIGN, "row_of_slot and weights must be 4-byte aligned");
+  int* err = nullptr;
+  int sms = 0;
+  st = device_state(&err, &sms);
+  if (st != GBW_OK) return st;
+  const cudaError_t e = launch_combine(y, P, H, row_of_slot, weights, T, k, out, err, sms,
+                                       static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GBW_OK : launch_error(e);
+}
+
+gbw_status gmoe_combine_bwd(const uint16_t* dout, const uint16_t* y, int64_t P, int64_t H,
+                            const int32_t* row_of_slot, const int32_t* slot_of_row,
+                            const float* weights, int64_t T, int32_t k, uint16_t* dy,
+                            float* dweights, void* stream) {
+  gbw_status st = combine_shape(P, H, T, k);
+  if (st != GBW_OK) return st;
+  if (T > 0 && (!dout || !row_of_slot || !weights || !dweights ||
+                (P > 0 && (!y || !dy || !slot_of_row))))
+    return fail(GBW_ERR_NULL, "NULL argument");
+  if (!aligned16(dout) || !aligned16(y) || !aligned16(dy))
+    return fail(GBW_ERR_ALIGN, "dout, y and dy must be 16-byte aligned");
+  if (!aligned4(row_of_slot) || !aligned4(slot_of_row) || !aligned4(weights) || !aligned4(dweights))
+    return fail(GBW_ERR_ALIGN, "indices and weights must be 4-byte aligned");
+  int* err = nullptr;
+  int sms = 0;
+  st = device_state(&err, &sms);
+  if (st != GBW_OK) return st;
+  const cudaError_t e = launch_combine_bwd(dout, y, P, H, row_of_slot, slot_of_row, weights, T, k,
+                                           dy, dweights, err, sms,
+                                           static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GBW_OK : launch_error(e);
 }
 
 gbw_status gnf4_dequant(const uint8_t* packed, const float* absmax,

@@ -73,6 +73,13 @@ typedef enum {
 #define GBW_DEVERR_OFFSETS 1 /* expert_offsets not 0 <= ... <= P (clamped) */
 #define GBW_DEVERR_TOKEN 2   /* row_to_token[p] outside [0, T) (clamped) */
 #define GBW_DEVERR_TIMEOUT 4 /* a pipeline wait gave up; output incomplete */
+#define GBW_DEVERR_ROUTE 8   /* an expert id or a routed row out of range, or
+                                slot_of_row not the inverse of row_of_slot
+                                (the slot is left out) */
+
+/* Types of the router logits. */
+#define GBW_LOGITS_BF16 0
+#define GBW_LOGITS_FP32 1
 
 /* Grouped NF4 forward ("grouped-nf4-gemm 0.43.0", "Which entry point?":
  * nf4_grouped.gemm_4bit_grouped; the bandwidth route of the 0.43.0 notes is
@@ -210,6 +217,71 @@ GBW_API gbw_status gnf4_grouped_expert_mlp_noalloc(const uint16_t* x, int64_t T,
                                            int32_t E, int64_t I, const int32_t* expert_offsets,
                                            const int32_t* row_to_token, int64_t P,
                                            uint16_t* out, int32_t mode, void* stream);
+
+/* Routing: each token's k experts, their softmax weights, and the
+ * expert-sorted plan that the grouped calls read.
+ *   logits  [T, E] bf16 (logits_type GBW_LOGITS_BF16) or fp32
+ *           (GBW_LOGITS_FP32), contiguous
+ *   topk_ids      [T, k] int32: the k largest logits in falling order, ties
+ *                 to the lowest index; a NaN counts as -inf
+ *   topk_weights  [T, k] fp32: exp(l - max) over its sum, over the chosen
+ *                 experts (renormalize != 0) or over all E; a row without any
+ *                 logit above -inf gets ids 0 .. k-1 and weights 0; equal
+ *                 infinite maxima share
+ *   expert_offsets [E+1], row_to_token [P], P = T * k: as in
+ *                 gnf4_grouped_gemm; routed rows are sorted by expert, stably
+ *                 (rows of one expert in the order of their tokens)
+ *   row_of_slot   [T, k] int32: routed row of slot s of token t
+ *   slot_of_row   [P] int32: its inverse, t * k + s of each routed row
+ *   workspace     gmoe_route_workspace(T, E) bytes of device memory (may be
+ *                 NULL when that is 0), overwritten; calls that may overlap
+ *                 need one each
+ * Requires 1 <= E <= 1024, 1 <= k <= min(E, 32), T * k < 2^31.  T == 0 writes
+ * expert_offsets (zeros) only.  One launch up to 128 tokens, two above. */
+GBW_API gbw_status gmoe_route(const void* logits, int32_t logits_type, int64_t T, int32_t E,
+                              int32_t k, int32_t renormalize, int32_t* topk_ids,
+                              float* topk_weights, int32_t* expert_offsets,
+                              int32_t* row_to_token, int32_t* row_of_slot, int32_t* slot_of_row,
+                              void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace gmoe_route needs for T tokens and E experts. */
+GBW_API int64_t gmoe_route_workspace(int64_t T, int32_t E);
+
+/* Gradient of gmoe_route's weights:
+ *   dlogits[t, e] = [e = ids[s]] w[s] dw[s] - q[e] * sum_s w[s] dw[s]
+ * with q = w on the chosen experts (renormalize) or the softmax over all.
+ *   logits, topk_ids, topk_weights   as gmoe_route took and gave them (logits
+ *            is not read and may be NULL when renormalize != 0)
+ *   dweights [T, k] fp32; dlogits [T, E], every element written, in the
+ *            logits' type.  A slot of weight 0 passes nothing on. */
+GBW_API gbw_status gmoe_route_bwd(const void* logits, int32_t logits_type, int64_t T, int32_t E,
+                                  int32_t k, int32_t renormalize, const int32_t* topk_ids,
+                                  const float* topk_weights, const float* dweights, void* dlogits,
+                                  void* stream);
+
+/* Combine: out[t, :] = bf16( sum_s w[t, s] * y[row_of_slot[t, s], :] ), summed
+ * in slot order in fp32.
+ *   y [P, H] bf16 (the routed rows, e.g. the down projection's output),
+ *   row_of_slot [T, k] int32, weights [T, k] fp32 or NULL (all 1: with it the
+ *   call sums the routed rows' gradients dx back into their tokens), out
+ *   [T, H] bf16.  A slot of weight 0 adds nothing, whatever its row holds.  A
+ *   row outside [0, P) adds nothing and raises GBW_DEVERR_ROUTE.
+ * Requires H % 8 == 0, 1 <= k <= 32, 16-byte aligned y and out. */
+GBW_API gbw_status gmoe_combine(const uint16_t* y, int64_t P, int64_t H,
+                                const int32_t* row_of_slot, const float* weights, int64_t T,
+                                int32_t k, uint16_t* out, void* stream);
+
+/* Gradient of gmoe_combine: for each slot, with r = row_of_slot[t, s],
+ *   dy[r, :] = bf16( w[t, s] * dout[t, :] ),  dw[t, s] = sum_h y[r, h] dout[t, h]
+ * (fp32).  slot_of_row is gmoe_route's inverse of row_of_slot: a row is
+ * written by the slot it names, so each row once; a slot that is not named by
+ * its row, or whose row is outside [0, P), gets dw = 0 and raises
+ * GBW_DEVERR_ROUTE.  Rows of dy that no slot names are left as they were.
+ * Requires H % 8 == 0, 16-byte aligned dout, y and dy. */
+GBW_API gbw_status gmoe_combine_bwd(const uint16_t* dout, const uint16_t* y, int64_t P, int64_t H,
+                                    const int32_t* row_of_slot, const int32_t* slot_of_row,
+                                    const float* weights, int64_t T, int32_t k, uint16_t* dy,
+                                    float* dweights, void* stream);
 
 /* Decode packed weights to bf16 ("grouped-nf4-gemm 0.43.0", "Try the
  * packers and byte checks on CPU", example 1: dequant_ref).  Bit-exact:
