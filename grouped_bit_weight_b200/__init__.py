@@ -21,7 +21,7 @@ __all__ = [
     "gmxfp4_grouped_expert_mlp", "gnf4_grouped_expert_mlp_noalloc", "gnf4_dequant",
     "gmxfp4_dequant", "gnf4_quantize",
     "gmxfp4_quantize", "Routing", "gmoe_route", "gmoe_route_bwd", "gmoe_combine",
-    "gmoe_combine_bwd", "device_status", "MODE_AUTO", "MODE_GEMM", "MODE_GEMV",
+    "gmoe_combine_bwd", "gmxfp4_quantize_rows", "gmxfp4_grouped_gemm_a4", "device_status", "MODE_AUTO", "MODE_GEMM", "MODE_GEMV",
     "DEVERR_OFFSETS", "DEVERR_TOKEN", "DEVERR_TIMEOUT", "DEVERR_ROUTE", "FLAG_OVERLAP_PREV",
     "EXPORTS",
 ]
@@ -64,6 +64,8 @@ EXPORTS = {
     "gmoe_route_bwd": (C.c_int, [_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _P, _P, _P]),
     "gmoe_combine": (C.c_int, [_P, _I64, _I64, _P, _P, _I64, _I32, _P, _P]),
     "gmoe_combine_bwd": (C.c_int, [_P, _P, _I64, _I64, _P, _P, _P, _I64, _I32, _P, _P, _P]),
+    "gmxfp4_quantize_rows": (C.c_int, [_P, _I64, _I64, _P, _I64, _I32, _P, _P, _P]),
+    "gmxfp4_grouped_gemm_a4": (C.c_int, [_P, _P, _I64, _I64, _P, _P, _I32, _I64, _P, _P, _P]),
     "gbw_device_status": (C.c_int, [_P, C.POINTER(C.c_int32), _I32]),
     "gbw_status_string": (C.c_char_p, [C.c_int]),
     "gbw_version": (C.c_int32, []),
@@ -123,6 +125,24 @@ def _on_device(where, **tensors):
         elif t.device != dev:
             raise ValueError(f"{where}: {name} is on {t.device}, expected {dev}")
     return dev
+
+
+def _call(where, fn, dev, *args):
+    """fn(*args, current stream of dev) with dev current; raises on a status.
+    The decode-sized calls take a few microseconds on the GPU, so the host's
+    part is kept short: the device is switched only when it is not current."""
+    i = dev.index
+    if torch.cuda.current_device() == i:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if st != 0:
+        raise GbwError(st, where)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 _MODES = {"auto": MODE_AUTO, "gemm": MODE_GEMM, "gemv": MODE_GEMV}
@@ -435,15 +455,18 @@ def gmoe_route(logits, k, renormalize=True):
     if T * k > 0x7FFFFFFF:
         raise ValueError(f"{where}: T * k must be below 2^31")
     dev = _on_device(where, logits=logits)
-    i32 = {"dtype": torch.int32, "device": dev}
-    r = Routing(torch.empty((T, k), **i32), torch.empty((T, k), dtype=torch.float32, device=dev),
-                torch.empty(E + 1, **i32), torch.empty(T * k, **i32), torch.empty((T, k), **i32),
-                torch.empty(T * k, **i32))
+    # one allocation for the six results: T * k entries each but the offsets
+    n = T * k
+    buf = torch.empty(5 * n + E + 1, dtype=torch.int32, device=dev)
+    parts = buf.split((n, n, n, n, n, E + 1))
+    r = Routing(parts[0].view(T, k), parts[1].view(torch.float32).view(T, k), parts[5], parts[2],
+                parts[3].view(T, k), parts[4])
     need = lib.gmoe_route_workspace(T, E)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    with torch.cuda.device(dev):
-        _check(lib.gmoe_route(_ptr(logits), _LOGITS[logits.dtype], T, E, k, int(bool(renormalize)),
-                              *(_ptr(t) for t in r), _ptr(ws), need, _stream(dev)), where)
+    at, step = buf.data_ptr(), 4 * n
+    _call(where, lib.gmoe_route, dev, logits.data_ptr(), _LOGITS[logits.dtype], T, E, k,
+          1 if renormalize else 0, at, at + step, at + 5 * step, at + 2 * step, at + 3 * step,
+          at + 4 * step, _at(ws), need)
     return r
 
 
@@ -464,10 +487,9 @@ def gmoe_route_bwd(logits, topk_ids, topk_weights, dweights, renormalize=True):
     dev = _on_device(where, logits=logits, topk_ids=topk_ids, topk_weights=topk_weights,
                      dweights=dweights)
     out = torch.empty_like(logits)
-    with torch.cuda.device(dev):
-        _check(lib.gmoe_route_bwd(_ptr(logits), _LOGITS[logits.dtype], T, E, k,
-                                  int(bool(renormalize)), _ptr(topk_ids), _ptr(topk_weights),
-                                  _ptr(dweights), _ptr(out), _stream(dev)), where)
+    _call(where, lib.gmoe_route_bwd, dev, logits.data_ptr(), _LOGITS[logits.dtype], T, E, k,
+          1 if renormalize else 0, topk_ids.data_ptr(), topk_weights.data_ptr(),
+          dweights.data_ptr(), out.data_ptr())
     return out
 
 
@@ -499,9 +521,8 @@ def gmoe_combine(y, row_of_slot, weights=None, out=None):
     dev = _on_device(where, y=y, row_of_slot=row_of_slot, weights=weights, out=out)
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib.gmoe_combine(_ptr(y), P, H, _ptr(row_of_slot), _ptr(weights), T, k, _ptr(out),
-                                _stream(dev)), where)
+    _call(where, lib.gmoe_combine, dev, y.data_ptr(), P, H, row_of_slot.data_ptr(), _at(weights),
+          T, k, out.data_ptr())
     return out
 
 
@@ -528,11 +549,74 @@ def gmoe_combine_bwd(dout, y, row_of_slot, slot_of_row, weights, dy=None):
     if dy is None:
         dy = torch.empty_like(y) if P <= T * k else torch.zeros_like(y)
     dw = torch.empty((T, k), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib.gmoe_combine_bwd(_ptr(dout), _ptr(y), P, H, _ptr(row_of_slot),
-                                    _ptr(slot_of_row), _ptr(weights), T, k, _ptr(dy), _ptr(dw),
-                                    _stream(dev)), where)
+    _call(where, lib.gmoe_combine_bwd, dev, dout.data_ptr(), y.data_ptr(), P, H,
+          row_of_slot.data_ptr(), slot_of_row.data_ptr(), weights.data_ptr(), T, k, dy.data_ptr(),
+          dw.data_ptr())
     return dy, dw
+
+
+def gmxfp4_quantize_rows(x, row_to_token=None, swiglu=False):
+    """(codes [P, K/32, 16] uint8, scales [P, K/32] uint8 e8m0): bf16 rows in
+    MXFP4, gathered through row_to_token [P] int32 when given.  x [T, K]; with
+    swiglu x is a gate_up output [T, 2K] and silu(gate) * up is packed."""
+    where = "gmxfp4_quantize_rows"
+    _need(x, "x", torch.bfloat16)
+    if x.dim() != 2:
+        raise ValueError(f"{where}: x must be [T, {'2K' if swiglu else 'K'}]")
+    T, K = x.shape
+    if swiglu:
+        if K % 2:
+            raise ValueError(f"{where}: x must be [T, 2K]")
+        K //= 2
+    if K <= 0 or K % 32:
+        raise ValueError(f"{where}: K={K} must be a positive multiple of 32")
+    P = T
+    if row_to_token is not None:
+        _need(row_to_token, "row_to_token", torch.int32)
+        P = row_to_token.numel()
+        if P and not T:
+            raise ValueError(f"{where}: x has no rows")
+    dev = _on_device(where, x=x, row_to_token=row_to_token)
+    codes = torch.empty((P, K // 32, 16), dtype=torch.uint8, device=dev)
+    scales = torch.empty((P, K // 32), dtype=torch.uint8, device=dev)
+    _call(where, lib.gmxfp4_quantize_rows, dev, x.data_ptr(), T, K, _at(row_to_token), P,
+          1 if swiglu else 0, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def gmxfp4_grouped_gemm_a4(x_codes, x_scales, blocks, scales, expert_offsets, out=None):
+    """out[P, N] bf16 = rows @ W_e^T per expert, both in MXFP4: x_codes
+    [P, K/32, 16] (or [P, K/2]) and x_scales [P, K/32] from
+    gmxfp4_quantize_rows, expert-sorted; blocks [E, N, K/32, 16] (or
+    [E, N, K/2]), scales [E, N, K/32]."""
+    where = "gmxfp4_grouped_gemm_a4"
+    _need(x_codes, "x_codes", torch.uint8)
+    _need(x_scales, "x_scales", torch.uint8)
+    _need(blocks, "packed weights", torch.uint8)
+    _need(scales, "scales", torch.uint8)
+    _need(expert_offsets, "expert_offsets", torch.int32)
+    if x_scales.dim() != 2 or blocks.dim() < 3 or x_codes.dim() < 2:
+        raise ValueError(f"{where}: x_codes must be [P, ...], x_scales [P, K/32] and the "
+                         "weights [E, N, ...]")
+    P, K = x_scales.shape[0], x_scales.shape[1] * 32
+    E, N = blocks.shape[0], blocks.shape[1]
+    if K == 0 or x_codes.shape[0] != P:
+        raise ValueError(f"{where}: x_codes must hold the {P} rows of x_scales")
+    _numel(x_codes, "x_codes", P * (K // 2), where)
+    _numel(blocks, "packed weights", E * N * (K // 2), where)
+    _numel(scales, "scales", E * N * (K // 32), where)
+    _numel(expert_offsets, "expert_offsets", E + 1, where)
+    if out is not None:
+        _need(out, "out", torch.bfloat16)
+        if tuple(out.shape) != (P, N):
+            raise ValueError(f"{where}: out must be [{P}, {N}]")
+    dev = _on_device(where, x_codes=x_codes, x_scales=x_scales, blocks=blocks, scales=scales,
+                     expert_offsets=expert_offsets, out=out)
+    if out is None:
+        out = torch.empty((P, N), dtype=torch.bfloat16, device=dev)
+    _call(where, lib.gmxfp4_grouped_gemm_a4, dev, x_codes.data_ptr(), x_scales.data_ptr(), P, K,
+          blocks.data_ptr(), scales.data_ptr(), E, N, expert_offsets.data_ptr(), out.data_ptr())
+    return out
 
 
 def device_status(device=None, clear=True) -> int:

@@ -1,0 +1,551 @@
+// a4.cu -- microscaled 4-bit activations: rows of bf16 to MXFP4, and the
+// grouped product of MXFP4 rows with MXFP4 expert weights on the tensor
+// cores' block-scaled 4-bit path.
+//
+//   quantise  per 32 consecutive values: X = floor(log2 max|v|) - 2 clamped to
+//             [-127, 127], scale byte X + 127, codes = v / 2^X to the nearest
+//             e2m1 (ties to the even code, saturating); v is a row of x, or
+//             silu(gate) * up of a gate_up row, in fp32
+//   product   out[p, n] = sum_k xq[p, k] wq[n, k], both e2m1 * 2^(scale - 127);
+//             the products of 32-blocks and their two scales are exact in the
+//             tensor core, the sum is fp32, one rounding to bf16
+//
+// Quantise is bound by memory: 4 lanes share a 32-block, 16-byte loads.
+//
+// Product, one persistent CTA per SM, 16 warps ("swap AB": MMA M is 128
+// weight rows, MMA N the routed rows of one expert, so few rows give a narrow
+// N instead of a padded M):
+//   warp 0      TMA: packed weights [128 x 128 bytes = 256 k] and the rows'
+//               codes (boxes of 64 rows) into a 3-stage ring, 128B swizzle --
+//               the packed bytes are the MMA's operands as they are
+//   warps 4-11  the scale bytes of 128 weight rows and up to 384 routed rows:
+//               two rows per thread, loaded a stage ahead, written to shared
+//               memory in the 32-lane order that tcgen05.cp copies to TMEM
+//   warp 1      tcgen05.cp of a stage's scales into TMEM (two alternating
+//               sets), then tcgen05.mma.kind::mxf4.block_scale, 64 k each
+//   warps 12-15 epilogue: tcgen05.ld -> bf16 -> out, 64-byte row segments
+// A tile holds up to 384 routed rows: rows past 192 go to the second
+// accumulator half, fed by the same weights; tiles of up to 192 alternate
+// between the halves, so that an epilogue overlaps the next tile's MMAs.
+// Tiles (expert, weight tile, row tile) run with row tiles innermost: an
+// expert's weights come from HBM once.
+#include "common.cuh"
+#include "launch.cuh"
+
+namespace gbw {
+
+cudaError_t make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base,
+                        uint64_t d0, uint64_t d1, uint64_t pitch, uint32_t b0,
+                        uint32_t b1, CUtensorMapSwizzle sw);
+
+namespace {
+
+// ----------------------------------------------------------------------
+// quantise
+// ----------------------------------------------------------------------
+
+// Two values to one byte of e2m1 codes, `lo` in the low nibble.
+__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+  uint32_t d;
+  asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u32.u8 %0, t;\n}\n"
+      : "=r"(d)
+      : "f"(hi), "f"(lo));
+  return d;
+}
+
+__device__ __forceinline__ void unpack8(uint4 q, float (&v)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// A thread quantises 8 values; the 4 lanes of a 32-block share its maximum.
+template <bool kGLU>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(
+    const uint16_t* __restrict__ x, int64_t T, int64_t K, const int32_t* __restrict__ r2t,
+    int64_t n, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int* err) {
+  grid_launch_dependents();
+  const int64_t U = K / 8;
+  // n is a multiple of 4: a quad is in or out of the loop as one
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const unsigned quad = 0xFu << (threadIdx.x & 28);
+    const int64_t p = i / U, c = i - p * U;
+    const int64_t t = token_of_row(r2t, (int32_t)p, T, err);
+    float v[8];
+    if (kGLU) {
+      float u[8];
+      const uint16_t* row = x + t * 2 * K + c * 8;
+      unpack8(__ldg(reinterpret_cast<const uint4*>(row)), v);
+      unpack8(__ldg(reinterpret_cast<const uint4*>(row + K)), u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __fdiv_rn(v[j], 1.0f + expf(-v[j])) * u[j];
+    } else {
+      unpack8(__ldg(reinterpret_cast<const uint4*>(x + t * K + c * 8)), v);
+    }
+    uint32_t m = 0;  // magnitudes order as their bits do, NaN and inf on top
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(quad, m, 1));
+    m = max(m, __shfl_xor_sync(quad, m, 2));
+    const uint32_t ex = m >> 23;
+    uint32_t byte = ex > 2u ? ex - 2u : 0u;
+    uint32_t q = 0;
+    if (ex == 255u) {
+      byte = 255u;  // a value that is not finite: the block is NaN
+    } else if (m) {
+      const float inv = __uint_as_float((254u - byte) << 23);  // 2^-X
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q |= e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv) << (8 * j);
+    }
+    reinterpret_cast<uint32_t*>(codes)[i] = q;
+    if ((c & 3) == 0) scales[i >> 2] = (uint8_t)byte;
+  }
+}
+
+// ----------------------------------------------------------------------
+// product
+// ----------------------------------------------------------------------
+
+constexpr int BM = 128;       // weight rows per tile (MMA M)
+constexpr int BH = 192;       // routed rows per accumulator half (MMA N)
+constexpr int BT = 2 * BH;    // routed rows per tile
+constexpr int BKB = 128;      // bytes of codes per row and stage: 256 k
+constexpr int BOX = 64;       // routed rows per TMA box
+constexpr int ST = 3;         // ring stages
+constexpr int kThreads = 512;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSfCol = BT;      // scale columns: two sets
+constexpr uint32_t kSfSet = 8 + 2 * 16;
+static_assert(kSfCol + 2 * kSfSet <= kTmemCols, "accumulators and scales fit TMEM");
+
+constexpr int kABytes = BM * BKB;                 // 16 KB
+constexpr int kBHalfBytes = BH * BKB;             // 24 KB
+constexpr int kSfBytes = 2 * 512 + 2 * 4 * 512;   // A: 2 k-atoms; B: 2 halves x 2 x 2
+constexpr int kStageBytes = kABytes + 2 * kBHalfBytes + kSfBytes;
+static_assert(kStageBytes % 1024 == 0 && kBHalfBytes % 1024 == 0, "swizzle atoms stay aligned");
+
+struct Smem {
+  static constexpr int bars = ST * kStageBytes;
+  static constexpr int nbars = 2 * ST + 4 + 1;
+  static constexpr int misc = bars + nbars * 8;
+  static constexpr int tables = misc + 16;
+};
+static_assert(1024 + Smem::tables + 8 * (1024 + 1) <= 232448,
+              "shared memory for 1024 experts exceeds the 227 KB a CTA can have");
+
+struct A4Problem {
+  const uint8_t* xs;       // [P, K/32] e8m0
+  const uint8_t* ws;       // [E, N, K/32] e8m0
+  int64_t P, K, N;
+  int32_t E;
+  const int32_t* offsets;  // [E + 1]
+  uint16_t* out;           // [P, N] bf16
+  int* err;
+  int xvec, wvec;          // widest aligned load of a row's scales: 1, 2, 4 or 8 bytes
+};
+
+struct Tile {
+  int32_t e, n0, p0, nv, nh;  // nv routed rows, the first nh of them in the first half
+};
+
+__device__ __forceinline__ int32_t row_tiles(int32_t cnt) { return (cnt + BT - 1) / BT; }
+
+__device__ __forceinline__ Tile tile_info(int64_t t, const int32_t* off, const int32_t* ts,
+                                          int32_t E) {
+  int32_t lo = 0, hi = E - 1;
+  while (lo < hi) {
+    const int32_t mid = (lo + hi + 1) >> 1;
+    if (ts[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  const int32_t cnt = off[lo + 1] - off[lo];
+  const int32_t rt = row_tiles(cnt);
+  const int32_t u = (int32_t)(t - ts[lo]);
+  const int32_t nt = u / rt, r = u - nt * rt;
+  // rows dealt evenly over the expert's row tiles, in sixteens
+  const int32_t per = ((cnt + rt - 1) / rt + 15) & ~15;
+  Tile d;
+  d.e = lo;
+  d.n0 = nt * BM;
+  d.p0 = off[lo] + r * per;
+  d.nv = min(per, cnt - r * per);
+  d.nh = d.nv <= BH ? d.nv : min(d.nv, ((d.nv + 31) / 32) * 16);
+  return d;
+}
+
+// Which accumulator half a tile uses (see the file comment); the MMA thread
+// and the epilogue step identical copies.
+struct AccSched {
+  uint32_t h = 0;
+  uint32_t use0 = 0, use1 = 0;
+  __device__ __forceinline__ uint32_t phase(uint32_t k) const { return (k ? use1 : use0) & 1u; }
+  __device__ __forceinline__ void next(bool wide) {
+    if (wide) {
+      ++use0;
+      ++use1;
+    } else {
+      if (h) ++use1; else ++use0;
+      h ^= 1u;
+    }
+  }
+};
+
+// Instruction descriptor, kind::mxf4: A and B e2m1 (K-major), e8m0 scales,
+// fp32 D; sf: which 16-bit half of a scale word (two 32-blocks) is used.
+__device__ __forceinline__ uint32_t idesc_mxf4(uint32_t N, uint32_t sf) {
+  return (sf << 4)              // B scale id
+         | (1u << 7)            // A format: e2m1
+         | (1u << 10)           // B format: e2m1
+         | ((N >> 3) << 17)     // N / 8
+         | (1u << 23)           // scale format: e8m0
+         | ((uint32_t)(BM >> 4) << 24)  // M / 16
+         | (sf << 29);          // A scale id
+}
+
+// D[tmem] (+)= (A * 2^sfa)[smem] * (B * 2^sfb)[smem]^T over 64 k.
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// 512 bytes (32 lanes x 16) from shared memory to 4 TMEM columns, repeated
+// for the four groups of 32 lanes.
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+               : "memory");
+}
+
+// Unswizzled descriptor of such 512 bytes: 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 16) |
+         ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1u << 46);
+}
+
+// Eight scale bytes at `p`, of which the first `nvalid` exist; the others
+// read as 127 (2^0: their codes are zeros).  vec divides the address and
+// nvalid.
+__device__ __forceinline__ uint2 load_scales(const uint8_t* p, int nvalid, int vec) {
+  uint32_t w[2] = {0x7F7F7F7Fu, 0x7F7F7F7Fu};
+  if (vec == 8) {
+    if (nvalid > 0) return __ldg(reinterpret_cast<const uint2*>(p));
+  } else if (vec == 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (4 * i < nvalid) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+  } else if (vec == 2) {
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      h[i] = 2 * i < nvalid ? (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + i) : 0x7F7Fu;
+    w[0] = h[0] | (h[1] << 16);
+    w[1] = h[2] | (h[3] << 16);
+  } else {
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = i < nvalid ? (uint32_t)__ldg(p + i) : 0x7Fu;
+    w[0] = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
+    w[1] = b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24);
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
+               const __grid_constant__ CUtensorMap tmx) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Smem::bars);
+  uint64_t* full = bars;
+  uint64_t* empty = full + ST;
+  uint64_t* acc_full = empty + ST;     // [2]
+  uint64_t* acc_empty = acc_full + 2;  // [2]
+  uint64_t* mma_done = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Smem::misc);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + Smem::misc + 4);
+  int32_t* off_s = reinterpret_cast<int32_t*>(smem + Smem::tables);
+  int32_t* ts_s = off_s + (pb.E + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t E = pb.E;
+  const int64_t N = pb.N;
+  const int32_t KB = (int32_t)(pb.K / 2);         // bytes of codes per row
+  const int32_t KS = (int32_t)(pb.K / 32);        // scale bytes per row
+  const int NS = (KB + BKB - 1) / BKB;            // stages per tile
+  const int32_t ntn = (int32_t)((N + BM - 1) / BM);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1 + 8); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 4); }
+    mbar_init(mma_done, 1);
+    *abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmw);
+    tma_prefetch_desc(&tmx);
+  }
+  grid_dependency_wait();
+  load_offsets_clamped(pb.offsets, E, pb.P, off_s, pb.err);
+  tile_prefix(off_s, E, BT, ntn, ts_s);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int64_t ntiles = ts_s[E];
+
+  if (warp == 0) {
+    // ---------------- codes: weights and routed rows ----------------
+    if (lane == 0) {
+      uint32_t g = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+        const Tile d = tile_info(t, off_s, ts_s, E);
+        const int b0 = (d.nh + BOX - 1) / BOX, b1 = (d.nv - d.nh + BOX - 1) / BOX;
+        const uint32_t bytes = kABytes + (uint32_t)(b0 + b1) * (BOX * BKB);
+        for (int ks = 0; ks < NS; ++ks, ++g) {
+          const uint32_t s = g % ST;
+          if (!(ok = mbar_wait(&empty[s], ((g / ST) & 1u) ^ 1u, abort, pb.err))) break;
+          uint8_t* st = smem + s * kStageBytes;
+          mbar_arrive_expect_tx(&full[s], bytes);
+          tma_load_2d(st, &tmw, ks * BKB, (int32_t)((int64_t)d.e * N + d.n0), &full[s]);
+          for (int b = 0; b < b0; ++b)
+            tma_load_2d(st + kABytes + b * (BOX * BKB), &tmx, ks * BKB, d.p0 + b * BOX, &full[s]);
+          for (int b = 0; b < b1; ++b)
+            tma_load_2d(st + kABytes + kBHalfBytes + b * (BOX * BKB), &tmx, ks * BKB,
+                        d.p0 + d.nh + b * BOX, &full[s]);
+        }
+      }
+      if (*abort)
+        for (uint32_t i = (g > ST ? g - ST : 0); i < g; ++i) mbar_drain(&full[i % ST], (i / ST) & 1u);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      uint32_t g = 0;
+      bool ok = true;
+      AccSched acc;
+      const uint64_t adesc0 = make_sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t bdesc0 = make_sdesc_sw128(smem_u32(smem + kABytes), 16, 1024);
+      const uint64_t sdesc0 = sdesc_scales(smem_u32(smem + kABytes + 2 * kBHalfBytes));
+      for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+        const Tile d = tile_info(t, off_s, ts_s, E);
+        const bool wide = d.nv > d.nh;
+        const uint32_t h0 = acc.h, h1 = acc.h ^ 1u;
+        const uint32_t n0 = (uint32_t)(d.nh + 15) & ~15u, n1 = (uint32_t)(d.nv - d.nh + 15) & ~15u;
+        if (!(ok = mbar_wait(&acc_empty[h0], acc.phase(h0) ^ 1u, abort, pb.err))) break;
+        tc_fence_after();
+        for (int ks = 0; ks < NS; ++ks, ++g) {
+          const uint32_t s = g % ST;
+          if (!(ok = mbar_wait(&full[s], (g / ST) & 1u, abort, pb.err))) break;
+          tc_fence_after();
+          const uint64_t so = (uint64_t)((s * kStageBytes) >> 4);
+          const uint32_t sf = tmem + kSfCol + (g & 1u) * kSfSet;
+          const int nk = min(4, (KB - ks * BKB + 31) / 32);  // 64-k steps of this stage
+          const int na = (nk + 1) / 2;                       // 128-k scale atoms
+          for (int a = 0; a < na; ++a) {
+            const uint64_t sd = sdesc0 + so;
+            tc_cp_scales(sf + a * 4, sd + a * 32);
+            tc_cp_scales(sf + 8 + a * 8, sd + 64 + a * 64);
+            if (n0 > 128u) tc_cp_scales(sf + 8 + a * 8 + 4, sd + 64 + a * 64 + 32);
+            if (wide) {
+              tc_cp_scales(sf + 24 + a * 8, sd + 192 + a * 64);
+              if (n1 > 128u) tc_cp_scales(sf + 24 + a * 8 + 4, sd + 192 + a * 64 + 32);
+            }
+          }
+          const uint64_t ad = adesc0 + so, bd = bdesc0 + so;
+          for (int kk = 0; kk < nk; ++kk)
+            tc_mma_mxf4(tmem + h0 * BH, ad + 2 * kk, bd + 2 * kk,
+                        idesc_mxf4(n0, (uint32_t)(kk & 1) * 2u), sf + (kk >> 1) * 4,
+                        sf + 8 + (kk >> 1) * 8, (ks | kk) != 0);
+          if (wide) {
+            if (ks == 0) {
+              if (!(ok = mbar_wait(&acc_empty[h1], acc.phase(h1) ^ 1u, abort, pb.err))) break;
+              tc_fence_after();
+            }
+            const uint64_t bd1 = bd + (uint64_t)(kBHalfBytes >> 4);
+            for (int kk = 0; kk < nk; ++kk)
+              tc_mma_mxf4(tmem + h1 * BH, ad + 2 * kk, bd1 + 2 * kk,
+                          idesc_mxf4(n1, (uint32_t)(kk & 1) * 2u), sf + (kk >> 1) * 4,
+                          sf + 24 + (kk >> 1) * 8, (ks | kk) != 0);
+          }
+          tc_commit(&empty[s]);
+        }
+        if (!ok) break;
+        tc_commit(&acc_full[h0]);
+        if (wide) tc_commit(&acc_full[h1]);
+        acc.next(wide);
+      }
+      tc_commit(mma_done);
+      mbar_drain(mma_done, 0);
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // ---------------- scales ----------------
+    // thread i: rows i and i + 256 of (128 weight rows, 192 + 192 routed rows)
+    const int i = (warp - 4) * 32 + lane;
+    // where this thread's rows go in a stage's scale area (first k-atom), and
+    // the distance of the second k-atom
+    auto place_of = [](int r, int& atom) -> int {
+      if (r < BM) {
+        atom = 512;
+        return (r & 31) * 16 + (r >> 5) * 4;
+      }
+      const int j = (r - BM) % BH, h = (r - BM) / BH;
+      atom = 1024;
+      return 1024 + h * 2048 + (j >> 7) * 512 + (j & 31) * 16 + ((j & 127) >> 5) * 4;
+    };
+    int atom0, atom1;
+    const int at0 = place_of(i, atom0), at1 = place_of(i + 256, atom1);
+    struct Src {
+      const uint8_t* p;  // the row's scales, or null
+      int vec;
+    };
+    auto src_of = [&](const Tile& d, int r) -> Src {
+      if (r < BM) {
+        if (d.n0 + r >= N) return {nullptr, 1};
+        return {pb.ws + ((int64_t)d.e * N + d.n0 + r) * KS, pb.wvec};
+      }
+      const int j = (r - BM) % BH, h = (r - BM) / BH;
+      const int row = h ? d.nh + j : j, end = h ? d.nv : d.nh;
+      if (row >= end) return {nullptr, 1};
+      return {pb.xs + (int64_t)(d.p0 + row) * KS, pb.xvec};
+    };
+    const uint2 ones = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    auto get = [&](const Src& s, int ks) -> uint2 {
+      return s.p ? load_scales(s.p + 8 * ks, KS - 8 * ks, s.vec) : ones;
+    };
+    int64_t t = blockIdx.x;
+    int ks = 0;
+    Src s0{nullptr, 1}, s1{nullptr, 1};
+    uint2 v0 = ones, v1 = ones;
+    if (t < ntiles) {
+      const Tile d = tile_info(t, off_s, ts_s, E);
+      s0 = src_of(d, i);
+      s1 = src_of(d, i + 256);
+      v0 = get(s0, 0);
+      v1 = get(s1, 0);
+    }
+    for (uint32_t g = 0; t < ntiles; ++g) {
+      const uint2 c0 = v0, c1 = v1;
+      if (++ks == NS) {
+        ks = 0;
+        t += gridDim.x;
+        if (t < ntiles) {
+          const Tile d = tile_info(t, off_s, ts_s, E);
+          s0 = src_of(d, i);
+          s1 = src_of(d, i + 256);
+        }
+      }
+      if (t < ntiles) {
+        v0 = get(s0, ks);
+        v1 = get(s1, ks);
+      }
+      const uint32_t s = g % ST;
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((g / ST) & 1u) ^ 1u, abort, pb.err))) break;
+      uint8_t* sf = smem + s * kStageBytes + kABytes + 2 * kBHalfBytes;
+      *reinterpret_cast<uint32_t*>(sf + at0) = c0.x;
+      *reinterpret_cast<uint32_t*>(sf + at0 + atom0) = c0.y;
+      *reinterpret_cast<uint32_t*>(sf + at1) = c1.x;
+      *reinterpret_cast<uint32_t*>(sf + at1 + atom1) = c1.y;
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[s]);
+    }
+  } else if (warp >= 12) {
+    // ---------------- epilogue ----------------
+    const uint32_t q = (uint32_t)warp & 3u;
+    AccSched acc;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+      const Tile d = tile_info(t, off_s, ts_s, E);
+      const bool wide = d.nv > d.nh;
+      const int64_t n = d.n0 + (int64_t)(q * 32 + lane);
+      for (int part = 0; part < (wide ? 2 : 1); ++part) {
+        const uint32_t h = part ? acc.h ^ 1u : acc.h;
+        ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[h], acc.phase(h), abort, pb.err));
+        if (!ok) break;
+        tc_fence_after();
+        const int rows = part ? d.nv - d.nh : d.nh;
+        uint16_t* dst = pb.out + (int64_t)(d.p0 + (part ? d.nh : 0)) * N + n;
+        const uint32_t taddr = tmem + ((q * 32u) << 16) + h * BH;
+        for (int c = 0; c < rows; c += 32) {
+          uint32_t r[32];
+          tmem_load_32x32b_x32(taddr + c, r);
+          if (n < N) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j < rows)
+                dst[(int64_t)(c + j) * N] =
+                    __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[j])));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[h]);
+      }
+      acc.next(wide);
+    }
+  }
+
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+// The widest of 8, 4, 2, 1 bytes that a row of `pitch` scale bytes at `base`
+// is aligned to in every row.
+int scale_vec(const void* base, int64_t pitch) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(base) | (uintptr_t)pitch | 8u;
+  return (int)(a & (~a + 1u));
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(const uint16_t* x, int64_t T, int64_t K, const int32_t* r2t,
+                                 int64_t P, bool glu, uint8_t* codes, uint8_t* scales, int* err,
+                                 int num_sms, cudaStream_t s) {
+  const int64_t n = P * (K / 8);
+  if (n == 0) return cudaSuccess;
+  const int64_t need = (n + 255) / 256, most = 64 * (int64_t)num_sms;
+  const int grid = (int)(need < most ? need : most);
+  return glu ? launch_kernel<quantize_rows_kernel<true>>(grid, 256, 0, s, false, x, T, K, r2t, n,
+                                                         codes, scales, err)
+             : launch_kernel<quantize_rows_kernel<false>>(grid, 256, 0, s, false, x, T, K, r2t, n,
+                                                          codes, scales, err);
+}
+
+cudaError_t launch_gemm_a4(const uint8_t* xq, const uint8_t* xs, int64_t P, int64_t K,
+                           const uint8_t* w, const uint8_t* ws, int32_t E, int64_t N,
+                           const int32_t* offsets, uint16_t* out, int* err, int num_sms,
+                           cudaStream_t s) {
+  if (P == 0) return cudaSuccess;
+  CUtensorMap tmw, tmx;
+  cudaError_t e = make_map_2d(&tmw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, (uint64_t)K / 2,
+                              (uint64_t)E * (uint64_t)N, (uint64_t)K / 2, BKB, BM,
+                              CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  e = make_map_2d(&tmx, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, (uint64_t)K / 2, (uint64_t)P,
+                  (uint64_t)K / 2, BKB, BOX, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  const A4Problem pb{xs, ws, P, K, N, E, offsets, out, err, scale_vec(xs, K / 32),
+                     scale_vec(ws, K / 32)};
+  constexpr size_t most = 1024 + Smem::tables + 8 * (1024 + 1);
+  e = opt_in_smem<gemm_a4_kernel>(most);
+  if (e != cudaSuccess) return e;
+  const size_t smem = 1024 + Smem::tables + 8 * (size_t)(E + 1);
+  return launch_kernel<gemm_a4_kernel>(num_sms, kThreads, smem, s, true, pb, tmw, tmx);
+}
+
+}  // namespace gbw

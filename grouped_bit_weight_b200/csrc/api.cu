@@ -451,6 +451,58 @@ gbw_status gmoe_combine_bwd(const uint16_t* dout, const uint16_t* y, int64_t P, 
   return e == cudaSuccess ? GBW_OK : launch_error(e);
 }
 
+// ---------------------------------------------------------------------------
+// MXFP4 activations
+// ---------------------------------------------------------------------------
+
+gbw_status gmxfp4_quantize_rows(const uint16_t* x, int64_t T, int64_t K,
+                                const int32_t* row_to_token, int64_t P, int32_t swiglu,
+                                uint8_t* codes, uint8_t* scales, void* stream) {
+  if (T < 0 || K <= 0 || P < 0) return fail(GBW_ERR_SHAPE, "need T >= 0, K > 0, P >= 0");
+  if (K % 32) return fail(GBW_ERR_SHAPE, "MXFP4 needs K % 32 == 0");
+  if (K > (int64_t)1 << 30 || P > INT32_MAX || T > INT32_MAX)
+    return fail(GBW_ERR_SHAPE, "sizes exceed the 32-bit row indices");
+  if (!row_to_token && T < P) return fail(GBW_ERR_SHAPE, "row_to_token == NULL needs T >= P");
+  if (row_to_token && P > 0 && T < 1) return fail(GBW_ERR_SHAPE, "T must be >= 1");
+  if (P > 0 && (!x || !codes || !scales)) return fail(GBW_ERR_NULL, "NULL x, codes or scales");
+  if (!aligned16(x)) return fail(GBW_ERR_ALIGN, "x must be 16-byte aligned");
+  if (!aligned4(codes) || !aligned4(row_to_token))
+    return fail(GBW_ERR_ALIGN, "codes and row_to_token must be 4-byte aligned");
+  int* err = nullptr;
+  int sms = 0;
+  gbw_status st = device_state(&err, &sms);
+  if (st != GBW_OK) return st;
+  const cudaError_t e = launch_quantize_rows(x, T, K, row_to_token, P, swiglu != 0, codes, scales,
+                                             err, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GBW_OK : launch_error(e);
+}
+
+gbw_status gmxfp4_grouped_gemm_a4(const uint8_t* x_codes, const uint8_t* x_scales, int64_t P,
+                                  int64_t K, const uint8_t* blocks, const uint8_t* scales,
+                                  int32_t E, int64_t N, const int32_t* expert_offsets,
+                                  uint16_t* out, void* stream) {
+  if (P < 0 || K <= 0 || N <= 0 || E < 1)
+    return fail(GBW_ERR_SHAPE, "need P >= 0, K > 0, N > 0, E >= 1");
+  if (K % 32) return fail(GBW_ERR_SHAPE, "MXFP4 needs K % 32 == 0");
+  if (N % 8) return fail(GBW_ERR_SHAPE, "N must be a multiple of 8");
+  if (E > kMaxExperts) return fail(GBW_ERR_SHAPE, "at most 1024 experts");
+  if (K > (int64_t)1 << 30 || N > (int64_t)1 << 30 || P > INT32_MAX || (int64_t)E * N > INT32_MAX)
+    return fail(GBW_ERR_SHAPE, "sizes exceed the 32-bit row indices");
+  if (!blocks || !scales || !expert_offsets) return fail(GBW_ERR_NULL, "NULL weights or offsets");
+  if (P > 0 && (!x_codes || !x_scales || !out)) return fail(GBW_ERR_NULL, "NULL rows or out");
+  if (!aligned16(x_codes) || !aligned16(blocks) || !aligned16(out))
+    return fail(GBW_ERR_ALIGN, "x_codes, blocks and out must be 16-byte aligned");
+  if (!aligned4(expert_offsets)) return fail(GBW_ERR_ALIGN, "offsets must be 4-byte aligned");
+  int* err = nullptr;
+  int sms = 0;
+  gbw_status st = device_state(&err, &sms);
+  if (st != GBW_OK) return st;
+  const cudaError_t e = launch_gemm_a4(x_codes, x_scales, P, K, blocks, scales, E, N,
+                                       expert_offsets, out, err, sms,
+                                       static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GBW_OK : launch_error(e);
+}
+
 gbw_status gnf4_dequant(const uint8_t* packed, const float* absmax,
                         int64_t rows, int64_t K, uint16_t* w_out,
                         void* stream) {

@@ -79,4 +79,14 @@ cudaError_t launch_combine_bwd(const uint16_t* dout, const uint16_t* y, int64_t 
                                const float* weights, int64_t T, int32_t k, uint16_t* dy,
                                float* dweights, int* err, int num_sms, cudaStream_t s);
 
+// bf16 rows (gathered through r2t unless it is null; glu: silu(gate) * up of
+// rows [2K]) to MXFP4, and the grouped product of MXFP4 rows and weights.
+cudaError_t launch_quantize_rows(const uint16_t* x, int64_t T, int64_t K, const int32_t* r2t,
+                                 int64_t P, bool glu, uint8_t* codes, uint8_t* scales, int* err,
+                                 int num_sms, cudaStream_t s);
+cudaError_t launch_gemm_a4(const uint8_t* xq, const uint8_t* xs, int64_t P, int64_t K,
+                           const uint8_t* w, const uint8_t* ws, int32_t E, int64_t N,
+                           const int32_t* offsets, uint16_t* out, int* err, int num_sms,
+                           cudaStream_t s);
+
 }  // namespace gbw

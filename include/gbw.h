@@ -283,6 +283,38 @@ GBW_API gbw_status gmoe_combine_bwd(const uint16_t* dout, const uint16_t* y, int
                                     const float* weights, int64_t T, int32_t k, uint16_t* dy,
                                     float* dweights, void* stream);
 
+/* Activations to MXFP4: routed row p of the output is x row row_to_token[p]
+ * (row p when row_to_token is NULL; T >= P then), packed like the weights.
+ *   swiglu == 0: x [T, K] bf16, v = the row
+ *   swiglu != 0: x [T, 2K] bf16 (a gate_up output, gate columns first),
+ *                v[k] = silu(x[k]) * x[K + k] in fp32, not rounded in between
+ *   codes  [P, K/32, 16] (= [P, K/2]) uint8, low nibble = even k
+ *   scales [P, K/32] uint8 e8m0
+ * Per 32 values: X = floor(log2 max|v|) - 2 clamped to [-127, 127], scale byte
+ * X + 127, codes = nearest e2m1 to v / 2^X (ties to the even code,
+ * saturating, sign kept); an all-zero block gets scale 0 and codes 0, a block
+ * with a value that is not finite scale 255 (NaN) and codes 0.  Token indices
+ * are clamped to [0, T) and recorded as in gmxfp4_grouped_gemm.
+ * Requires K % 32 == 0, 16-byte aligned x and 4-byte aligned codes. */
+GBW_API gbw_status gmxfp4_quantize_rows(const uint16_t* x, int64_t T, int64_t K,
+                                        const int32_t* row_to_token, int64_t P, int32_t swiglu,
+                                        uint8_t* codes, uint8_t* scales, void* stream);
+
+/* Grouped MXFP4 x MXFP4 product (W4A4) on the block-scaled tensor cores:
+ *   out[p, n] = bf16( sum_k xq[p, k] * W_e(p)[n, k] ),  fp32 accumulation
+ *   x_codes [P, K/2] uint8, x_scales [P, K/32] uint8: expert-sorted rows as
+ *           gmxfp4_quantize_rows writes them
+ *   blocks, scales, expert_offsets, out: as in gmxfp4_grouped_gemm (scales
+ *           need no alignment here)
+ * Requires K % 32 == 0, N % 8 == 0, 1 <= E <= 1024, 16-byte aligned x_codes,
+ * blocks and out.  P == 0 is a no-op.  Rows of out past expert_offsets[E] are
+ * not written. */
+GBW_API gbw_status gmxfp4_grouped_gemm_a4(const uint8_t* x_codes, const uint8_t* x_scales,
+                                          int64_t P, int64_t K, const uint8_t* blocks,
+                                          const uint8_t* scales, int32_t E, int64_t N,
+                                          const int32_t* expert_offsets, uint16_t* out,
+                                          void* stream);
+
 /* Decode packed weights to bf16 ("grouped-nf4-gemm 0.43.0", "Try the
  * packers and byte checks on CPU", example 1: dequant_ref).  Bit-exact:
  * w[r, k] = bf16_rn(fp32(NF4[q] * absmax[r, k/64])).  rows counts all

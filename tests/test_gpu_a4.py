@@ -1,0 +1,308 @@
+"""MXFP4 activations: the row quantiser byte for byte against the 64-bit
+definition, and the W4A4 grouped product against the 64-bit sum of the same
+4-bit values."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+import moe_plain as mp
+
+gbw = pytest.importorskip("grouped_bit_weight_b200")
+DEV = "cuda:0"
+
+
+def _bf16(shape, seed, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * std).to(torch.bfloat16)
+
+
+def _codes(t):
+    """codes [P, K/32, 16] uint8 -> [P, K] values 0..15, low nibble first."""
+    c = t.cpu().numpy().reshape(t.shape[0], -1)
+    return np.stack([c & 15, c >> 4], -1).reshape(t.shape[0], -1)
+
+
+def _values(codes, scales):
+    q = codes.astype(np.int64)
+    v = mp.E2M1[q & 7] * np.where(q & 8, -1.0, 1.0)
+    s = scales.astype(np.float64)
+    f = np.where(s == 255, np.nan, 2.0 ** (s - 127))
+    return v * np.repeat(f, 32, axis=-1)
+
+
+def _weights(E, N, K, seed, lo=117, hi=122):
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(0, 256, (E, N, K // 2), dtype=np.uint8)
+    scales = rng.integers(lo, hi, (E, N, K // 32), dtype=np.uint8)
+    nib = np.stack([codes & 15, codes >> 4], -1).reshape(E, N, K)
+    return codes, scales, _values(nib, scales)
+
+
+def _offsets(counts):
+    return np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K", [(1, 32), (3, 96), (64, 512), (7, 2880), (257, 160), (1000, 64)])
+def test_quantize_rows_bytes(T, K):
+    x = _bf16((T, K), T + K) * (2.0 ** torch.arange(-8, 8).repeat((T + 15) // 16)[:T, None])
+    x = x.to(torch.bfloat16)
+    codes, scales = gbw.gmxfp4_quantize_rows(x.to(DEV))
+    c, s, _ = mp.mxfp4(x.double().numpy())
+    assert codes.shape == (T, K // 32, 16) and scales.shape == (T, K // 32)
+    assert (scales.cpu().numpy() == s).all() and (_codes(codes) == c).all()
+    perm = torch.randint(0, T, (2 * T + 1,), generator=torch.Generator().manual_seed(1))
+    codes, scales = gbw.gmxfp4_quantize_rows(x.to(DEV), perm.to(torch.int32).to(DEV))
+    assert (scales.cpu().numpy() == s[perm]).all() and (_codes(codes) == c[perm]).all()
+    assert gbw.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_quantize_rows_special_values():
+    """Halfway values, saturation, zeros of both signs, subnormals, the largest
+    bf16, and blocks that hold NaN or an infinity."""
+    x = torch.zeros((10, 64))
+    x[0, :16] = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, -0.25, -0.75, -1.25,
+                              -1.75, -2.5, -3.5, -5.0, 7.0])
+    x[1, :4] = torch.tensor([7.9, -7.9, 4.0, -0.0])
+    x[2, 32] = -0.0
+    x[3, :3] = torch.tensor([1e-38, -1e-39, 9e-41])
+    x[4, 5] = 3.3e38
+    x[5, 7] = float("nan")
+    x[6, 40] = float("inf")
+    x[7, 1], x[7, 2] = float("-inf"), float("nan")
+    x[8] = 1.1754944e-38 * torch.arange(64)
+    x[9, :2] = torch.tensor([2.0 ** -126, 2.0 ** -133])
+    x = x.to(torch.bfloat16)
+    codes, scales = gbw.gmxfp4_quantize_rows(x.to(DEV))
+    c, s, _ = mp.mxfp4(x.double().numpy())
+    assert (scales.cpu().numpy() == s).all() and (_codes(codes) == c).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K", [(1, 32), (33, 288), (130, 2880)])
+def test_quantize_rows_swiglu(T, K):
+    """silu(gate) * up in fp32 and then rounded to 4 bits: the 64-bit value may
+    lie on the other side of a rounding border only when it is nearer to it
+    than fp32's own error, 8 roundings of 2^-24."""
+    x = _bf16((T, 2 * K), T)
+    x[0, :4] = torch.tensor([100.0, -100.0, 0.0, -3e38])
+    h = mp.silu(x[:, :K].double().numpy()) * x[:, K:].double().numpy()
+    codes, scales = gbw.gmxfp4_quantize_rows(x.to(DEV), swiglu=True)
+    got = _values(_codes(codes), scales.cpu().numpy())
+    lo, hi = (mp.mxfp4(h * (1 + s * 2.0 ** -21))[2] for s in (-1, 1))
+    mid = mp.mxfp4(h)[2]
+    near = (got == lo) | (got == hi) | (got == mid)
+    assert near.all() and (got != mid).mean() < 1e-3
+    perm = torch.randint(0, T, (T + 3,), dtype=torch.int32)
+    c2, s2 = gbw.gmxfp4_quantize_rows(x.to(DEV), perm.to(DEV), swiglu=True)
+    assert torch.equal(c2, codes[perm.long().to(DEV)]) and torch.equal(s2, scales[perm.long().to(DEV)])
+
+
+def _check_product(counts, N, K, seed, rows_pad=0, xstd=None):
+    E, P = len(counts), int(sum(counts))
+    w, ws, wv = _weights(E, N, K, seed)
+    x = _bf16((P + rows_pad, K), seed + 1)
+    if xstd is not None:
+        x = (x.float() * xstd[:, None]).to(torch.bfloat16)
+    xq, xs = gbw.gmxfp4_quantize_rows(x.to(DEV))
+    xv = _values(_codes(xq), xs.cpu().numpy())
+    off = _offsets(counts)
+    t = lambda a: torch.from_numpy(a).to(DEV)
+    out = torch.full((P + rows_pad, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    if rows_pad:
+        off[-1] = P + rows_pad  # the last expert takes the padding too
+    got = gbw.gmxfp4_grouped_gemm_a4(xq, xs, t(w), t(ws), t(off), out=out)
+    assert got is out
+    got = got.cpu().double().numpy()
+    assert gbw.device_status() == 0
+    for e in range(E):
+        a, b = off[e], off[e + 1]
+        if a == b:
+            continue
+        ref = xv[a:b] @ wv[e].T
+        mag = np.abs(xv[a:b]) @ np.abs(wv[e]).T
+        # the products are exact; K of them summed in fp32 may each drop what
+        # lies below 2^-24 of the sum of magnitudes
+        mp.bf16_close(got[a:b], ref, K * 2.0 ** -24 * mag)
+    return got
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts,N,K", [
+    ([16], 128, 256), ([1], 8, 32), ([5, 0, 3], 136, 64), ([17, 31], 200, 96),
+    ([16] * 8, 256, 512), ([0, 0, 40, 0], 264, 352), ([128, 129, 130], 128, 128),
+    ([191, 192, 193], 320, 288), ([383, 384, 385], 128, 544), ([601, 2, 0, 77], 192, 320),
+    ([1000], 72, 1024), ([33], 1000, 2912), ([250, 256, 262, 20], 640, 2880),
+    ([3] * 64, 64, 160), ([2, 1] * 20, 2056, 768)])
+def test_product_matches_plain(counts, N, K):
+    _check_product(counts, N, K, sum(counts) + N + K)
+
+
+@pytest.mark.gpu
+def test_product_scales_over_a_wide_range():
+    """Every row has a magnitude of its own, 2^-60 to 2^60."""
+    P = 300
+    _check_product([100, 200], 136, 416, 5, xstd=2.0 ** torch.linspace(-60, 60, P))
+
+
+@pytest.mark.gpu
+def test_product_scales_at_every_alignment():
+    """Scale arrays that start at odd addresses."""
+    E, N, K, P = 3, 136, 512, 60
+    w, ws, _ = _weights(E, N, K, 3)
+    x = _bf16((P, K), 4).to(DEV)
+    xq, xs = gbw.gmxfp4_quantize_rows(x)
+    off = torch.from_numpy(_offsets([20, 30, 10])).to(DEV)
+    t = lambda a: torch.from_numpy(a).to(DEV)
+    ref = gbw.gmxfp4_grouped_gemm_a4(xq, xs, t(w), t(ws), off)
+
+    def shifted(a, n):
+        b = torch.empty(a.numel() + 16, dtype=torch.uint8, device=DEV)
+        b[n:n + a.numel()] = a.flatten()
+        return b[n:n + a.numel()].view(a.shape)
+
+    for n in (1, 2, 4, 6):
+        got = gbw.gmxfp4_grouped_gemm_a4(xq, shifted(xs, n), t(w), shifted(t(ws), 8 - n), off)
+        assert torch.equal(got, ref)
+    assert gbw.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_product_nan_scale_marks_its_rows_and_columns_only():
+    E, N, K, P = 2, 136, 256, 40
+    w, ws, _ = _weights(E, N, K, 3)
+    ws[0, 9, 3] = 255
+    x = _bf16((P, K), 4)
+    x[7, 100] = float("inf")
+    x[30, 0] = float("nan")
+    off = _offsets([20, 20])
+    t = lambda a: torch.from_numpy(a).to(DEV)
+    xq, xs = gbw.gmxfp4_quantize_rows(x.to(DEV))
+    got = gbw.gmxfp4_grouped_gemm_a4(xq, xs, t(w), t(ws), t(off)).cpu()
+    bad = torch.isnan(got)
+    want = torch.zeros_like(bad)
+    want[7] = want[30] = True
+    want[:20, 9] = True
+    assert torch.equal(bad, want)
+
+
+@pytest.mark.gpu
+def test_product_without_rows_bad_offsets_and_repeats():
+    E, N, K = 3, 64, 128
+    w, ws, _ = _weights(E, N, K, 3)
+    t = lambda a: torch.from_numpy(a).to(DEV)
+    xq, xs = gbw.gmxfp4_quantize_rows(_bf16((0, K), 1).to(DEV))
+    assert gbw.gmxfp4_grouped_gemm_a4(xq, xs, t(w), t(ws), t(_offsets([0, 0, 0]))).shape == (0, N)
+    xq, xs = gbw.gmxfp4_quantize_rows(_bf16((50, K), 1).to(DEV))
+    a = gbw.gmxfp4_grouped_gemm_a4(xq, xs, t(w), t(ws), t(_offsets([20, 0, 30])))
+    b = gbw.gmxfp4_grouped_gemm_a4(xq, xs, t(w), t(ws), t(_offsets([20, 0, 30])))
+    assert torch.equal(a, b) and gbw.device_status() == 0
+    gbw.gmxfp4_grouped_gemm_a4(xq, xs, t(w), t(ws), t(np.array([0, 60, 30, 50], np.int32)))
+    assert gbw.device_status() == gbw.DEVERR_OFFSETS
+    bad = torch.tensor([0, 50, -1], dtype=torch.int32, device=DEV)
+    gbw.gmxfp4_quantize_rows(_bf16((50, K), 1).to(DEV), bad)
+    assert gbw.device_status() == gbw.DEVERR_TOKEN
+
+
+@pytest.mark.gpu
+def test_prompt_layer_in_mxfp4_from_routing_to_combine_in_a_graph():
+    """route -> quantise -> gate_up -> SwiGLU + quantise -> down -> combine, as
+    a prompt runs it, captured and replayed on other inputs, each step against
+    the 64-bit value of what went into it."""
+    T, E, k, H, I = 200, 8, 2, 256, 192
+    gw, gs, gv = _weights(E, 2 * I, H, 1)
+    dw, ds, dv = _weights(E, H, I, 2)
+    d = [torch.from_numpy(a).to(DEV) for a in (gw, gs, dw, ds)]
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn((T, H), generator=g, device=DEV).to(torch.bfloat16)
+    l = torch.randn((T, E), generator=g, device=DEV)
+
+    def layer():
+        r = gbw.gmoe_route(l, k)
+        q = gbw.gmxfp4_quantize_rows(x, r.row_to_token)
+        a = gbw.gmxfp4_grouped_gemm_a4(*q, d[0], d[1], r.expert_offsets)
+        h = gbw.gmxfp4_quantize_rows(a, swiglu=True)
+        y = gbw.gmxfp4_grouped_gemm_a4(*h, d[2], d[3], r.expert_offsets)
+        return r, q, a, h, y, gbw.gmoe_combine(y, r.row_of_slot, r.topk_weights)
+
+    def check(r, q, a, h, y, out):
+        ids, w = mp.route(l.cpu().double().numpy(), k, True)
+        off, r2t, ros, _ = mp.plan(ids, E)
+        assert (r.row_to_token.cpu().numpy() == r2t).all()
+        xv = mp.mxfp4(x.cpu().double().numpy())[2][r2t]
+        hv = _values(_codes(h[0]), h[1].cpu().numpy())
+        a64, y64 = a.cpu().double().numpy(), y.cpu().double().numpy()
+        for e in range(E):
+            s = slice(off[e], off[e + 1])
+            mp.bf16_close(a64[s], xv[s] @ gv[e].T, H * 2.0 ** -24 * (np.abs(xv[s]) @ np.abs(gv[e]).T))
+            mp.bf16_close(y64[s], hv[s] @ dv[e].T, I * 2.0 ** -24 * (np.abs(hv[s]) @ np.abs(dv[e]).T))
+        want = mp.mxfp4(mp.silu(a64[:, :I]) * a64[:, I:])[2]
+        assert (hv != want).mean() < 1e-3
+        mp.bf16_close(out.cpu().double().numpy(), mp.combine(y64, ros, w),
+                      2.0 ** -18 * mp.combine(np.abs(y64), ros, w))
+
+    check(*layer())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = layer()
+    for seed in (5, 6):
+        g.manual_seed(seed)
+        l.copy_(torch.randn((T, E), generator=g, device=DEV))
+        x.copy_(torch.randn((T, H), generator=g, device=DEV).to(torch.bfloat16))
+        graph.replay()
+        torch.cuda.synchronize()
+        check(*got)
+    assert gbw.device_status() == 0
+
+
+# ---------------------------------------------------------------- refusals
+
+
+def test_a4_refusals():
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="x must"):
+        gbw.gmxfp4_quantize_rows(x.float())
+    with pytest.raises(ValueError, match="multiple of 32"):
+        gbw.gmxfp4_quantize_rows(x[:, :48].contiguous())
+    with pytest.raises(ValueError, match="multiple of 32"):
+        gbw.gmxfp4_quantize_rows(x[:, :32].contiguous(), swiglu=True)
+    with pytest.raises(ValueError, match="contiguous"):
+        gbw.gmxfp4_quantize_rows(x[:, ::2])
+    with pytest.raises(ValueError, match="no rows"):
+        gbw.gmxfp4_quantize_rows(x[:0], torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        gbw.gmxfp4_quantize_rows(x)
+    a = dict(x_codes=u8(4, 2, 16), x_scales=u8(4, 2), blocks=u8(3, 8, 2, 16), scales=u8(3, 8, 2),
+             expert_offsets=torch.zeros(4, dtype=torch.int32))
+    for name, bad, text in (("x_codes", u8(4, 3, 16), "x_codes"), ("scales", u8(3, 8, 3), "scales"),
+                            ("blocks", u8(3, 8, 3, 16), "packed weights"),
+                            ("expert_offsets", torch.zeros(3, dtype=torch.int32), "expert_offsets"),
+                            ("x_scales", u8(5, 2), "x_codes")):
+        with pytest.raises(ValueError, match=text):
+            gbw.gmxfp4_grouped_gemm_a4(**{**a, name: bad})
+    with pytest.raises(ValueError, match="out must"):
+        gbw.gmxfp4_grouped_gemm_a4(**a, out=torch.zeros((4, 16), dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        gbw.gmxfp4_grouped_gemm_a4(**a)
+
+
+def test_a4_host_validation():
+    L, p, NULL, SHAPE, ALIGN = gbw.lib, C.c_void_p(16), 1, 2, 3
+
+    def q(x=p, T=4, K=64, r2t=None, P=4, codes=p, scales=p):
+        return L.gmxfp4_quantize_rows(x, T, K, r2t, P, 0, codes, scales, None)
+    assert q(K=48) == SHAPE and q(T=3) == SHAPE and q(P=-1) == SHAPE and q(T=0, r2t=p) == SHAPE
+    assert q(x=None) == NULL and q(scales=None) == NULL
+    assert q(x=C.c_void_p(24)) == ALIGN and q(codes=C.c_void_p(18)) == ALIGN
+
+    def g(xc=p, P=4, K=64, w=p, ws=p, E=2, N=64, off=p, out=p):
+        return L.gmxfp4_grouped_gemm_a4(xc, p, P, K, w, ws, E, N, off, out, None)
+    assert g(K=48) == SHAPE and g(N=60) == SHAPE and g(E=1025) == SHAPE and g(P=-1) == SHAPE
+    assert g(E=1000, N=1 << 24) == SHAPE
+    assert g(w=None) == NULL and g(off=None) == NULL and g(out=None) == NULL
+    assert g(xc=C.c_void_p(24)) == ALIGN and g(w=C.c_void_p(8)) == ALIGN
+    assert g(off=C.c_void_p(18)) == ALIGN
