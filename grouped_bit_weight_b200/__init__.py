@@ -21,7 +21,8 @@ __all__ = [
     "gmxfp4_grouped_expert_mlp", "gnf4_grouped_expert_mlp_noalloc", "gnf4_dequant",
     "gmxfp4_dequant", "gnf4_quantize",
     "gmxfp4_quantize", "Routing", "gmoe_route", "gmoe_route_bwd", "gmoe_combine",
-    "gmoe_combine_bwd", "gmxfp4_quantize_rows", "gmxfp4_grouped_gemm_a4", "device_status", "MODE_AUTO", "MODE_GEMM", "MODE_GEMV",
+    "gmoe_combine_bwd", "gmxfp4_quantize_rows", "gmxfp4_grouped_gemm_a4",
+    "gnf4_moe_layer", "gmxfp4_moe_layer", "device_status", "MODE_AUTO", "MODE_GEMM", "MODE_GEMV",
     "DEVERR_OFFSETS", "DEVERR_TOKEN", "DEVERR_TIMEOUT", "DEVERR_ROUTE", "FLAG_OVERLAP_PREV",
     "EXPORTS",
 ]
@@ -64,6 +65,9 @@ EXPORTS = {
     "gmoe_route_bwd": (C.c_int, [_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _P, _P, _P]),
     "gmoe_combine": (C.c_int, [_P, _I64, _I64, _P, _P, _I64, _I32, _P, _P]),
     "gmoe_combine_bwd": (C.c_int, [_P, _P, _I64, _I64, _P, _P, _P, _I64, _I32, _P, _P, _P]),
+    "gnf4_moe_layer": (C.c_int, [_P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I32, _I64, _I32, _I32, _P, _P, _I64, _P]),
+    "gmxfp4_moe_layer": (C.c_int, [_P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I32, _I64, _I32, _I32, _P, _P, _I64, _P]),
+    "gmoe_layer_workspace": (C.c_int64, [_I64, _I32, _I32, _I64, _I64]),
     "gmxfp4_quantize_rows": (C.c_int, [_P, _I64, _I64, _P, _I64, _I32, _P, _P, _P]),
     "gmxfp4_grouped_gemm_a4": (C.c_int, [_P, _P, _I64, _I64, _P, _P, _I32, _I64, _P, _P, _P]),
     "gbw_device_status": (C.c_int, [_P, C.POINTER(C.c_int32), _I32]),
@@ -553,6 +557,82 @@ def gmoe_combine_bwd(dout, y, row_of_slot, slot_of_row, weights, dy=None):
           row_of_slot.data_ptr(), slot_of_row.data_ptr(), weights.data_ptr(), T, k, dy.data_ptr(),
           dw.data_ptr())
     return dy, dw
+
+
+def _moe_layer(fn, where, x, rw, gu, gu_scale, dn, dn_scale, scale_dtype, sdiv, k, renormalize,
+               rb, out, workspace):
+    _need(x, "x", torch.bfloat16)
+    _need(rw, "router_w", torch.bfloat16)
+    _need(gu, "gate_up weights", torch.uint8)
+    _need(gu_scale, "gate_up scales", scale_dtype)
+    _need(dn, "down weights", torch.uint8)
+    _need(dn_scale, "down scales", scale_dtype)
+    if x.dim() != 2 or rw.dim() != 2 or gu.dim() < 3 or dn.dim() < 3:
+        raise ValueError(f"{where}: x must be [T, H], router_w [E, H] and the weights "
+                         "[E, rows, ...]")
+    T, H = x.shape
+    E, I2 = gu.shape[0], gu.shape[1]
+    I = I2 // 2
+    if T > 32:
+        raise ValueError(f"{where}: T={T}: the whole layer takes at most 32 tokens; use "
+                         "gmoe_route, the fused expert pass and gmoe_combine")
+    if I2 % 2 or dn.shape[0] != E or dn.shape[1] != H:
+        raise ValueError(f"{where}: gate_up must be [E, 2I, ...] and down [E, H={H}, ...]")
+    if tuple(rw.shape) != (E, H):
+        raise ValueError(f"{where}: router_w must be [{E}, {H}]")
+    if not 1 <= k <= min(E, 16):
+        raise ValueError(f"{where}: k={k} must be in 1 .. min(E={E}, 16)")
+    if not H or not I or H % 64 or I % 64:
+        raise ValueError(f"{where}: H={H} and I={I} must be positive multiples of 64")
+    _numel(gu, "gate_up weights", E * I2 * (H // 2), where)
+    _numel(gu_scale, "gate_up scales", E * I2 * (H // sdiv), where)
+    _numel(dn, "down weights", E * H * (I // 2), where)
+    _numel(dn_scale, "down scales", E * H * (I // sdiv), where)
+    if rb is not None:
+        _need(rb, "router_bias", torch.float32)
+        _numel(rb, "router_bias", E, where)
+    if out is not None:
+        _need(out, "out", torch.bfloat16)
+        if tuple(out.shape) != (T, H):
+            raise ValueError(f"{where}: out must be [{T}, {H}]")
+    need = lib.gmoe_layer_workspace(T, E, k, H, I)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8)
+        if workspace.numel() < need:
+            raise ValueError(f"{where}: workspace has {workspace.numel()} bytes, needs {need}")
+    dev = _on_device(where, x=x, router_w=rw, gu=gu, gu_scale=gu_scale, dn=dn, dn_scale=dn_scale,
+                     router_bias=rb, out=out, workspace=workspace)
+    if out is None:
+        out = torch.empty_like(x)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _call(where, fn, dev, x.data_ptr(), T, H, rw.data_ptr(), _at(rb), gu.data_ptr(),
+          gu_scale.data_ptr(), dn.data_ptr(), dn_scale.data_ptr(), E, I, k,
+          1 if renormalize else 0, out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def gnf4_moe_layer(x, router_w, gu_packed, gu_absmax, dn_packed, dn_absmax, k, renormalize=True,
+                   router_bias=None, out=None, workspace=None):
+    """A whole mixture-of-experts layer for up to 32 tokens in two launches:
+    router (x [T, H] @ router_w [E, H]^T + router_bias [E] fp32), the k experts
+    of each token and their softmax weights as gmoe_route chooses them,
+    gate_up [E, 2I, H/2] (gate rows then up rows), SwiGLU, down [E, H, I/2],
+    weighted sum -> [T, H] bf16.  workspace: uint8, at least
+    lib.gmoe_layer_workspace(T, E, k, H, I) bytes, 256-byte aligned; calls that
+    may overlap need one each (allocated here when not given)."""
+    return _moe_layer(lib.gnf4_moe_layer, "gnf4_moe_layer", x, router_w, gu_packed, gu_absmax,
+                      dn_packed, dn_absmax, torch.float32, 64, k, renormalize, router_bias, out,
+                      workspace)
+
+
+def gmxfp4_moe_layer(x, router_w, gu_blocks, gu_scales, dn_blocks, dn_scales, k, renormalize=True,
+                     router_bias=None, out=None, workspace=None):
+    """gnf4_moe_layer on MXFP4 experts (blocks [E, rows, K/32, 16], e8m0 scales
+    [E, rows, K/32])."""
+    return _moe_layer(lib.gmxfp4_moe_layer, "gmxfp4_moe_layer", x, router_w, gu_blocks, gu_scales,
+                      dn_blocks, dn_scales, torch.uint8, 32, k, renormalize, router_bias, out,
+                      workspace)
 
 
 def gmxfp4_quantize_rows(x, row_to_token=None, swiglu=False):

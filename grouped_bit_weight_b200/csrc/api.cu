@@ -452,6 +452,76 @@ gbw_status gmoe_combine_bwd(const uint16_t* dout, const uint16_t* y, int64_t P, 
 }
 
 // ---------------------------------------------------------------------------
+// Whole layer for a few tokens
+// ---------------------------------------------------------------------------
+
+int64_t gmoe_layer_workspace(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I) {
+  if (T <= 0 || T > 32 || E < 1 || E > kMaxExperts || k < 1 || k > 16 || H <= 0 || I <= 0 ||
+      H > (int64_t)1 << 30 || I > (int64_t)1 << 29)
+    return 0;
+  return layer_workspace(T, E, k, H, I);
+}
+
+static gbw_status moe_layer(Fmt f, const uint16_t* x, int64_t T, int64_t H, const uint16_t* router_w,
+                            const float* router_bias, const uint8_t* gu, const void* gu_scale,
+                            const uint8_t* dn, const void* dn_scale, int32_t E, int64_t I, int32_t k,
+                            int32_t renormalize, uint16_t* out, void* workspace,
+                            int64_t workspace_bytes, void* stream) {
+  if (T < 0 || H <= 0 || I <= 0 || E < 1 || k < 1)
+    return fail(GBW_ERR_SHAPE, "need T >= 0, H > 0, I > 0, E >= 1, k >= 1");
+  if (T > 32)
+    return fail(GBW_ERR_SHAPE, "the whole layer takes at most 32 tokens: use gmoe_route, the fused "
+                               "expert pass and gmoe_combine");
+  if (H % 64 || I % 64) return fail(GBW_ERR_SHAPE, "the layer needs H % 64 == 0 and I % 64 == 0");
+  if (E > kMaxExperts) return fail(GBW_ERR_SHAPE, "at most 1024 experts");
+  if (k > E || k > 16) return fail(GBW_ERR_SHAPE, "need k <= min(E, 16)");
+  if (H > (int64_t)1 << 30 || I > (int64_t)1 << 29 || (int64_t)E * 2 * I > INT32_MAX ||
+      (int64_t)E * H > INT32_MAX)
+    return fail(GBW_ERR_SHAPE, "sizes exceed the 32-bit row indices");
+  const int64_t need = gmoe_layer_workspace(T, E, k, H, I);
+  if (T > 0 && (!x || !router_w || !gu || !gu_scale || !dn || !dn_scale || !out || !workspace))
+    return fail(GBW_ERR_NULL, "NULL argument");
+  if (workspace_bytes < need) return fail(GBW_ERR_SHAPE, "workspace smaller than gmoe_layer_workspace");
+  if (!aligned16(x) || !aligned16(router_w) || !aligned16(gu) || !aligned16(dn) || !aligned16(out))
+    return fail(GBW_ERR_ALIGN, "x, router_w, packed weights and out must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(GBW_ERR_ALIGN, "the workspace must be 256-byte aligned");
+  if (f == Fmt::NF4 && (!aligned4(gu_scale) || !aligned4(dn_scale)))
+    return fail(GBW_ERR_ALIGN, "absmax must be 4-byte aligned");
+  if (f == Fmt::MXFP4 &&
+      ((reinterpret_cast<uintptr_t>(gu_scale) | reinterpret_cast<uintptr_t>(dn_scale)) & 1u))
+    return fail(GBW_ERR_ALIGN, "MXFP4 scales must be 2-byte aligned");
+  if (!aligned4(router_bias)) return fail(GBW_ERR_ALIGN, "router_bias must be 4-byte aligned");
+  int* err = nullptr;
+  int sms = 0;
+  gbw_status st = device_state(&err, &sms);
+  if (st != GBW_OK) return st;
+  const LayerProblem p{x, T, H, I, E, k, renormalize != 0, router_w, router_bias, gu, gu_scale, dn,
+                       dn_scale, out, err};
+  const cudaError_t e = launch_layer(f, p, workspace, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GBW_OK : launch_error(e);
+}
+
+gbw_status gnf4_moe_layer(const uint16_t* x, int64_t T, int64_t H, const uint16_t* router_w,
+                          const float* router_bias, const uint8_t* gu_packed,
+                          const float* gu_absmax, const uint8_t* dn_packed, const float* dn_absmax,
+                          int32_t E, int64_t I, int32_t k, int32_t renormalize, uint16_t* out,
+                          void* workspace, int64_t workspace_bytes, void* stream) {
+  return moe_layer(Fmt::NF4, x, T, H, router_w, router_bias, gu_packed, gu_absmax, dn_packed,
+                   dn_absmax, E, I, k, renormalize, out, workspace, workspace_bytes, stream);
+}
+
+gbw_status gmxfp4_moe_layer(const uint16_t* x, int64_t T, int64_t H, const uint16_t* router_w,
+                            const float* router_bias, const uint8_t* gu_blocks,
+                            const uint8_t* gu_scales, const uint8_t* dn_blocks,
+                            const uint8_t* dn_scales, int32_t E, int64_t I, int32_t k,
+                            int32_t renormalize, uint16_t* out, void* workspace,
+                            int64_t workspace_bytes, void* stream) {
+  return moe_layer(Fmt::MXFP4, x, T, H, router_w, router_bias, gu_blocks, gu_scales, dn_blocks,
+                   dn_scales, E, I, k, renormalize, out, workspace, workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------------------
 // MXFP4 activations
 // ---------------------------------------------------------------------------
 

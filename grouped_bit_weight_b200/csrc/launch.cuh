@@ -79,6 +79,25 @@ cudaError_t launch_combine_bwd(const uint16_t* dout, const uint16_t* y, int64_t 
                                const float* weights, int64_t T, int32_t k, uint16_t* dy,
                                float* dweights, int* err, int num_sms, cudaStream_t s);
 
+// A whole layer for a few tokens: x [T, H], router [E, H] (+ bias [E]),
+// packed gate_up [E, 2I, H/2] and down [E, H, I/2] with their scales.
+struct LayerProblem {
+  const uint16_t* x;
+  int64_t T, H, I;
+  int32_t E, k, renorm;
+  const uint16_t* rw;
+  const float* rb;      // or null
+  const uint8_t* gu;
+  const void* gu_scale;
+  const uint8_t* dn;
+  const void* dn_scale;
+  uint16_t* out;        // [T, H]
+  int* err;
+};
+int64_t layer_workspace(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I);
+cudaError_t launch_layer(Fmt f, const LayerProblem& p, void* workspace, int num_sms,
+                         cudaStream_t s);
+
 // bf16 rows (gathered through r2t unless it is null; glu: silu(gate) * up of
 // rows [2K]) to MXFP4, and the grouped product of MXFP4 rows and weights.
 cudaError_t launch_quantize_rows(const uint16_t* x, int64_t T, int64_t K, const int32_t* r2t,

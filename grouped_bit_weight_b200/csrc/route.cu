@@ -20,6 +20,7 @@
 // launched early behind the first.
 #include "common.cuh"
 #include "launch.cuh"
+#include "route.cuh"
 
 namespace gbw {
 namespace {
@@ -29,76 +30,10 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxE = 1024;
 constexpr int64_t kSingleTokens = 128;
 
-__device__ __forceinline__ float bf16_to_f32(uint32_t bits16) {
-  return __uint_as_float(bits16 << 16);
-}
-__device__ __forceinline__ float load_logit(const uint16_t* p) { return bf16_to_f32(__ldg(p)); }
-__device__ __forceinline__ float load_logit(const float* p) { return __ldg(p); }
 __device__ __forceinline__ void store_logit(uint16_t* p, float v) {
   *p = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
-
-__device__ __forceinline__ float no_nan(float v) {
-  return v != v ? __int_as_float(0xFF800000) : v;
-}
-
-// Keys order as the values do, -0 equal to +0; 0 is below every value's key.
-__device__ __forceinline__ uint32_t order_key(float v) {
-  const uint32_t u = __float_as_uint(v == 0.0f ? 0.0f : v);
-  return (u >> 31) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float((k >> 31) ? (k & 0x7FFFFFFFu) : ~k);
-}
-
-// exp(v - m) for v <= m; 1 for v == m also when both are infinite.
-__device__ __forceinline__ float share(float v, float m) { return v == m ? 1.0f : expf(v - m); }
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// The choice of one token: lane s < k gets the s-th expert and its weight.
-template <typename TL, int NPL>
-__device__ __forceinline__ void choose(const TL* row, int E, int k, int renorm, int lane, int& id,
-                                       float& w) {
-  uint32_t key[NPL];
-#pragma unroll
-  for (int j = 0; j < NPL; ++j) {
-    const int e = j * 32 + lane;
-    key[j] = e < E ? order_key(no_nan(load_logit(row + e))) : 0u;
-  }
-  float all = 0.0f, m = 0.0f, v = 0.0f;
-  for (int s = 0; s < k; ++s) {
-    uint32_t lk = 0u;
-    int le = 0;
-#pragma unroll
-    for (int j = 0; j < NPL; ++j)
-      if (key[j] > lk) { lk = key[j]; le = j * 32 + lane; }
-    const uint32_t g = __reduce_max_sync(0xffffffffu, lk);
-    const int e = (int)__reduce_min_sync(0xffffffffu, lk == g ? (unsigned)le : 0xffffffffu);
-    if (s == 0) {
-      m = key_value(g);
-      if (!renorm) {
-        float t = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NPL; ++j)
-          if (key[j]) t += share(key_value(key[j]), m);
-        all = warp_sum(t);
-      }
-    }
-    if (lane == s) { id = e; v = key_value(g); }
-#pragma unroll
-    for (int j = 0; j < NPL; ++j)
-      if (e == j * 32 + lane) key[j] = 0u;
-  }
-  const float p = lane < k ? share(v, m) : 0.0f;
-  const float total = renorm ? warp_sum(p) : all;
-  w = m == __int_as_float(0xFF800000) ? 0.0f : p / total;
-}
 
 // Exclusive scan of v over the block's threads (kThreads of them); `part` has
 // kWarps entries.  Returns the sum over lower threads.

@@ -283,6 +283,46 @@ GBW_API gbw_status gmoe_combine_bwd(const uint16_t* dout, const uint16_t* y, int
                                     const float* weights, int64_t T, int32_t k, uint16_t* dy,
                                     float* dweights, void* stream);
 
+/* A whole mixture-of-experts layer for a few tokens, NF4 experts: router,
+ * choice of experts, gate_up, SwiGLU, down and weighted combine, in two
+ * launches.
+ *   l[t, e] = sum_k x[t, k] router_w[e, k] + router_bias[e], fp32 accumulation;
+ *   topk ids and weights as gmoe_route chooses them from l; for each slot with
+ *   e = ids[t, s]:
+ *     h = silu(x[t] @ Wg_e^T) * (x[t] @ Wu_e^T)   not rounded to bf16
+ *   out[t, :] = bf16( sum_s w[t, s] * (h_s @ Wd_e^T) )
+ *   x            [T, H] bf16; out [T, H] bf16
+ *   router_w     [E, H] bf16; router_bias [E] fp32 or NULL
+ *   gu_packed    [E, 2I, H/2], gu_absmax [E, 2I, H/64]: gate rows, then up rows
+ *   dn_packed    [E, H, I/2], dn_absmax [E, H, I/64]
+ *   workspace    gmoe_layer_workspace(T, E, k, H, I) bytes of 256-byte aligned
+ *                device memory, overwritten; nothing is kept in it between
+ *                calls; calls that may overlap need one each
+ * The codebook enters the sums rounded to bf16, as in the bandwidth GEMV.  A
+ * slot of weight 0 adds nothing, whatever its expert gives.
+ * Requires T <= 32 (larger batches: gmoe_route, gnf4_grouped_expert_mlp,
+ * gmoe_combine), 1 <= E <= 1024, 1 <= k <= min(E, 16), H % 64 == 0,
+ * I % 64 == 0, 16-byte aligned x, router_w, packed weights and out.  T == 0 is
+ * a no-op. */
+GBW_API gbw_status gnf4_moe_layer(const uint16_t* x, int64_t T, int64_t H,
+                                  const uint16_t* router_w, const float* router_bias,
+                                  const uint8_t* gu_packed, const float* gu_absmax,
+                                  const uint8_t* dn_packed, const float* dn_absmax, int32_t E,
+                                  int64_t I, int32_t k, int32_t renormalize, uint16_t* out,
+                                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The same with MXFP4 experts (blocks [E, 2I, H/32, 16] + scales [E, 2I, H/32],
+ * blocks [E, H, I/32, 16] + scales [E, H, I/32], e8m0, 2-byte aligned). */
+GBW_API gbw_status gmxfp4_moe_layer(const uint16_t* x, int64_t T, int64_t H,
+                                    const uint16_t* router_w, const float* router_bias,
+                                    const uint8_t* gu_blocks, const uint8_t* gu_scales,
+                                    const uint8_t* dn_blocks, const uint8_t* dn_scales, int32_t E,
+                                    int64_t I, int32_t k, int32_t renormalize, uint16_t* out,
+                                    void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace the two calls above need. */
+GBW_API int64_t gmoe_layer_workspace(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I);
+
 /* Activations to MXFP4: routed row p of the output is x row row_to_token[p]
  * (row p when row_to_token is NULL; T >= P then), packed like the weights.
  *   swiglu == 0: x [T, K] bf16, v = the row

@@ -1,0 +1,311 @@
+"""The whole mixture-of-experts layer for a few tokens against a plain 64-bit
+layer: every format, token count, split and mask, on streams, in graphs and
+with two calls at once."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+import moe_plain as mp
+
+gbw = pytest.importorskip("grouped_bit_weight_b200")
+DEV = "cuda:0"
+
+
+def _levels_error():
+    """Largest relative error of an NF4 level in the kernel's table: 1.437
+    times the level, rounded to bf16."""
+    v = torch.from_numpy(mp.NF4) * float(np.float32(1.437))
+    r = v.to(torch.bfloat16).double()
+    nz = v != 0
+    return float(((r - v)[nz] / v[nz]).abs().max())
+
+
+def _pack(fmt, E, N, K, rng, std):
+    """(codes, scales, 64-bit weights) of random 4-bit weights."""
+    codes = rng.integers(0, 256, (E, N, K // 2), dtype=np.uint8)
+    lo, hi = codes & 15, codes >> 4
+    if fmt == "nf4":
+        q = np.stack([hi, lo], -1).reshape(E, N, K)
+        s = (std * (2 + rng.random((E, N, K // 64)))).astype(np.float32)
+        return codes, s, mp.NF4[q] * np.repeat(s.astype(np.float64), 64, -1)
+    q = np.stack([lo, hi], -1).reshape(E, N, K)
+    s = rng.integers(118, 122, (E, N, K // 32), dtype=np.uint8)
+    v = mp.E2M1[q & 7] * np.where(q & 8, -1.0, 1.0)
+    return (codes.reshape(E, N, K // 32, 16), s,
+            v * np.repeat(2.0 ** (s.astype(np.float64) - 127), 32, -1))
+
+
+class Layer:
+    def __init__(self, fmt, E, k, H, I, seed=0, renorm=True, bias=False):
+        rng = np.random.default_rng(seed)
+        self.fmt, self.E, self.k, self.H, self.I, self.renorm = fmt, E, k, H, I, renorm
+        self.gu = _pack(fmt, E, 2 * I, H, rng, 1 / np.sqrt(H))
+        self.dn = _pack(fmt, E, H, I, rng, 1 / np.sqrt(I))
+        self.rw = torch.from_numpy(rng.standard_normal((E, H)) * 1.5 / np.sqrt(H)).to(torch.bfloat16)
+        self.rb = torch.from_numpy(rng.standard_normal(E) * 0.5).float() if bias else None
+        t = lambda a: torch.from_numpy(a).to(DEV)
+        self.args = (self.rw.to(DEV), t(self.gu[0]), t(self.gu[1]), t(self.dn[0]), t(self.dn[1]))
+        self.kw = dict(k=k, renormalize=renorm, router_bias=None if self.rb is None else self.rb.to(DEV))
+        self.fn = gbw.gnf4_moe_layer if fmt == "nf4" else gbw.gmxfp4_moe_layer
+
+    def __call__(self, x, **kw):
+        return self.fn(x, *self.args, **self.kw, **kw)
+
+    def plain(self, x):
+        """(out, allowed error, tokens whose choice is not near a tie)."""
+        x = x.cpu().double().numpy()
+        l = x @ self.rw.double().numpy().T
+        mag = np.abs(x) @ np.abs(self.rw.double().numpy()).T
+        if self.rb is not None:
+            l = l + self.rb.double().numpy()
+        ids, w = mp.route(l, self.k, self.renorm)
+        # logits: products of bf16 exact, fp32 chains of at most H / 256 and
+        # then 13 steps, each 2^-24 of the magnitudes: an absolute error dl,
+        # and a relative one of 2 dl (+ 16 roundings) in the weights
+        dl = 2.0 ** -24 * (self.H / 256 * 8 + 16) * mag.max(1)
+        s = -np.sort(-l, 1)
+        far = np.ones(len(l), bool)
+        if self.k < self.E:
+            far = s[:, self.k - 1] - s[:, self.k] > 2 * dl
+        dw = 4 * dl + 16 * 2.0 ** -24
+        # gate and up: each weight off by `lev`, sums of H products in fp32
+        lev = _levels_error() + 2.0 ** -22 if self.fmt == "nf4" else 0.0
+        e1, e2 = (lev + (n + 8) * 2.0 ** -24 for n in (self.H, self.I))
+        out, tol = np.zeros_like(x), np.zeros_like(x)
+        for t in range(len(x)):
+            for e, we in zip(ids[t], w[t]):
+                if we == 0:
+                    continue
+                a = self.gu[2][e] @ x[t]
+                m = np.abs(self.gu[2][e]) @ np.abs(x[t])
+                g, u, dg, du = a[:self.I], a[self.I:], e1 * m[:self.I], e1 * m[self.I:]
+                h = mp.silu(g) * u
+                # |silu'| <= 1.1; h is kept to 2^-16, silu to 8 roundings
+                dh = 1.1 * dg * (np.abs(u) + du) + np.abs(mp.silu(g)) * du + 2.0 ** -16 * np.abs(h)
+                y = self.dn[2][e] @ h
+                dy = np.abs(self.dn[2][e]) @ (dh + e2 * np.abs(h))
+                out[t] += we * y
+                tol[t] += we * (dy + dw[t] * np.abs(y)) + (self.k + 1) * 2.0 ** -24 * we * np.abs(y)
+        return out, tol, far
+
+    def check(self, x, got):
+        ref, tol, far = self.plain(x)
+        assert far.all(), "the inputs have a choice next to a tie: choose another seed"
+        mp.bf16_close(got.cpu().double().numpy(), ref, tol)
+        # the bound above is for the worst signs: most errors are far inside
+        err = np.linalg.norm(got.cpu().double().numpy() - ref) / max(np.linalg.norm(ref), 1e-30)
+        assert err < 4e-3, err
+        assert gbw.device_status() == 0
+
+
+def _x(T, H, seed, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn((T, H), generator=g) * std).to(torch.bfloat16).to(DEV)
+
+
+SHAPES = [  # T, E, k, H, I
+    (1, 1, 1, 64, 64), (1, 8, 2, 128, 64), (2, 4, 4, 192, 320), (3, 16, 8, 512, 128),
+    (7, 8, 1, 320, 192), (8, 32, 8, 256, 448), (9, 2, 2, 576, 64), (31, 6, 3, 128, 704),
+    (32, 8, 4, 256, 256), (32, 1, 1, 448, 128), (32, 40, 16, 128, 64), (17, 300, 5, 64, 64),
+    (5, 1024, 3, 64, 64), (1, 8, 8, 2048, 768), (4, 4, 2, 704, 1472)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["nf4", "mxfp4"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_layer_matches_plain(shape, fmt):
+    T, E, k, H, I = shape
+    n = sum(shape)
+    m = Layer(fmt, E, k, H, I, seed=n, renorm=n % 2 == 0, bias=n % 3 == 0)
+    x = _x(T, H, n)
+    m.check(x, m(x))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["nf4", "mxfp4"])
+@pytest.mark.parametrize("T", [1, 32])
+def test_layer_all_tokens_on_the_same_experts(T, fmt):
+    """The bias sends every token to the same experts: one of them gets all
+    rows, and most experts none."""
+    m = Layer(fmt, 16, 3, 512, 320, seed=T)
+    m.kw["router_bias"] = torch.zeros(16, device=DEV)
+    m.kw["router_bias"][[2, 7, 15]] = 50.0
+    m.rb = m.kw["router_bias"].cpu()
+    x = _x(T, 512, 5)
+    m.check(x, m(x))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["nf4", "mxfp4"])
+def test_layer_inputs_far_from_one(fmt):
+    """Rows of very different magnitude, a row of zeros among them."""
+    m = Layer(fmt, 8, 2, 256, 128, seed=3)
+    scale = torch.tensor([1e-12, 1e-4, 0.0, 30.0, 1.0, 1e-30])[:, None].to(DEV)
+    x = (_x(6, 256, 4).float() * scale).to(torch.bfloat16)
+    ref, tol, far = m.plain(x)
+    keep = far.copy()
+    keep[[0, 2, 5]] = True  # logits of (nearly) zero: the tie goes to the lowest index
+    got = m(x).cpu().double().numpy()
+    assert (got[2] == 0).all()
+    for t in (1, 3, 4):
+        assert far[t]
+        mp.bf16_close(got[t], ref[t], tol[t])
+    assert np.isfinite(got).all() and gbw.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_layer_ties_masked_experts_and_bad_rows():
+    """Equal logits choose the lowest experts; a bias of -inf or of the lowest
+    value masks an expert; a token of NaN or infinity stays in its own row."""
+    m = Layer("nf4", 12, 4, 128, 64, seed=9)
+    m.rw.zero_()
+    m.args[0].zero_()
+    x = _x(5, 128, 1)
+    m.kw["router_bias"] = torch.zeros(12, device=DEV)
+    m.kw["router_bias"][0] = float("-inf")
+    m.kw["router_bias"][1] = torch.finfo(torch.float32).min
+    m.rb = m.kw["router_bias"].cpu()
+    ref, tol, _ = m.plain(x)
+    mp.bf16_close(m(x).cpu().double().numpy(), ref, tol)  # experts 2, 3, 4, 5, a quarter each
+    m.kw["router_bias"] = torch.full((12,), float("-inf"), device=DEV)
+    m.rb = m.kw["router_bias"].cpu()
+    assert (m(x) == 0).all()                              # nothing left: weights of zero
+    m.kw["router_bias"][7] = 1.0                          # one expert left of the four asked for
+    m.rb = m.kw["router_bias"].cpu()
+    ref, tol, _ = m.plain(x)
+    mp.bf16_close(m(x).cpu().double().numpy(), ref, tol)
+    good = m(x)
+    x[1, 3] = float("nan")
+    x[3, 0] = float("inf")
+    got = m(x)
+    assert torch.equal(got[[0, 2, 4]], good[[0, 2, 4]])
+    # (a row of NaN logits has no expert at all: its output is zero)
+    assert gbw.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["nf4", "mxfp4"])
+def test_layer_rows_do_not_depend_on_the_batch(fmt):
+    """A token's output is bit for bit the same alone and in a batch whenever
+    the split of its sums is the same; and repeats are identical."""
+    m = Layer(fmt, 16, 4, 256, 192, seed=6)
+    x = _x(24, 256, 8)
+    a = m(x)
+    for _ in range(3):
+        assert torch.equal(m(x), a)
+    perm = torch.randperm(24, generator=torch.Generator().manual_seed(2)).to(DEV)
+    assert torch.equal(m(x[perm].contiguous()), a[perm])
+
+
+@pytest.mark.gpu
+def test_layer_workspaces_streams_graphs_and_two_calls_at_once():
+    m, n = Layer("nf4", 16, 4, 256, 128, seed=1), Layer("mxfp4", 8, 2, 512, 256, seed=2)
+    x, z = _x(5, 256, 1), _x(9, 512, 2)
+    a, b = m(x), n(z)
+    m.check(x, a)
+    n.check(z, b)
+    # a workspace and an output of the caller's, full of garbage
+    need = gbw.lib.gmoe_layer_workspace(5, 16, 4, 256, 128)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    out = torch.full((5, 256), float("nan"), dtype=torch.bfloat16, device=DEV)
+    for _ in range(2):
+        assert m(x, out=out, workspace=ws) is out and torch.equal(out, a)
+    # two streams at once, many calls each
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (s1, s2):
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(40):
+        with torch.cuda.stream(s1):
+            got.append((m(x), a))
+        with torch.cuda.stream(s2):
+            got.append((n(z), b))
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, v) for u, v in got)
+    # two graphs, replayed on two streams at once, on other inputs
+    graphs = []
+    for layer, inp in ((m, x), (n, z)):
+        layer(inp)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = layer(inp)
+        graphs.append((g, o))
+    x.copy_(_x(5, 256, 11))
+    z.copy_(_x(9, 512, 12))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (g, _) in zip((s1, s2), graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    m.check(x, graphs[0][1])
+    n.check(z, graphs[1][1])
+    assert torch.equal(graphs[0][1], m(x)) and torch.equal(graphs[1][1], n(z))
+
+
+@pytest.mark.gpu
+def test_layer_equals_route_experts_combine():
+    """The layer against the calls a larger batch makes, within the roundings
+    of the intermediate tensors those store in bf16."""
+    m = Layer("nf4", 8, 2, 256, 128, seed=4)
+    x = _x(32, 256, 3)
+    l = (x.float() @ m.args[0].float().T).contiguous()
+    r = gbw.gmoe_route(l, 2)
+    y, _ = gbw.gnf4_grouped_expert_mlp(x, *m.args[1:], r.expert_offsets, r.row_to_token)
+    z = gbw.gmoe_combine(y, r.row_of_slot, r.topk_weights).float()
+    d = (m(x).float() - z).norm() / z.norm()
+    assert d < 1.5e-2  # gate, up, h, y and out each rounded to 2^-8, weights too
+
+
+@pytest.mark.gpu
+def test_layer_without_tokens():
+    m = Layer("nf4", 4, 2, 64, 64)
+    assert m(torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)).shape == (0, 64)
+
+
+# ---------------------------------------------------------------- refusals
+
+
+def test_layer_refusals():
+    z = lambda *s, d=torch.uint8: torch.zeros(s, dtype=d)
+    bf = torch.bfloat16
+    good = dict(x=z(2, 128, d=bf), router_w=z(4, 128, d=bf), gu_packed=z(4, 128, 64),
+                gu_absmax=z(4, 128, 2, d=torch.float32), dn_packed=z(4, 128, 32),
+                dn_absmax=z(4, 128, 1, d=torch.float32), k=2)
+    for change, text in (
+            (dict(x=z(33, 128, d=bf)), "at most 32 tokens"), (dict(k=0), "k=0"), (dict(k=5), "k=5"),
+            (dict(router_w=z(4, 64, d=bf)), "router_w"), (dict(gu_packed=z(4, 127, 64)), "gate_up"),
+            (dict(gu_absmax=z(4, 128, 1, d=torch.float32)), "gate_up scales"),
+            (dict(dn_packed=z(4, 64, 32)), "down"), (dict(dn_packed=z(4, 128, 16)), "down weights"),
+            (dict(dn_absmax=z(4, 128, 2, d=torch.float32)), "down scales"),
+            (dict(router_bias=z(3, d=torch.float32)), "router_bias"),
+            (dict(out=z(2, 64, d=bf)), "out must"), (dict(workspace=z(100)), "workspace"),
+            (dict(gu_packed=z(4, 64, 64)), "multiples of 64"), (dict(), "CUDA tensor")):
+        with pytest.raises(ValueError, match=text):
+            gbw.gnf4_moe_layer(**{**good, **change})
+    with pytest.raises(TypeError, match="x must"):
+        gbw.gnf4_moe_layer(**{**good, "x": z(2, 128, d=torch.float16)})
+    with pytest.raises(ValueError, match="contiguous"):
+        gbw.gnf4_moe_layer(**{**good, "x": z(128, 2, d=bf).t()})
+
+
+def test_layer_host_validation():
+    L, p, NULL, SHAPE, ALIGN = gbw.lib, C.c_void_p(256), 1, 2, 3
+    assert gbw.lib.gmoe_layer_workspace(33, 8, 2, 64, 64) == 0
+    need = L.gmoe_layer_workspace(4, 8, 2, 128, 64)
+    assert need > 4 * 8 * 4 + 2 * 8 * 64 * 2 + 8 * 128 * 4
+
+    for fn in (L.gnf4_moe_layer, L.gmxfp4_moe_layer):
+        def call(x=p, T=4, H=128, rw=p, rb=None, gu=p, gs=p, dn=p, ds=p, E=8, I=64, k=2, out=p,
+                 ws=p, n=need):
+            return fn(x, T, H, rw, rb, gu, gs, dn, ds, E, I, k, 1, out, ws, n, None)
+        assert call(T=33) == SHAPE and call(T=-1) == SHAPE and call(H=96) == SHAPE
+        assert call(I=32) == SHAPE and call(E=1025) == SHAPE and call(k=9) == SHAPE
+        assert call(E=64, k=17) == SHAPE and call(n=need - 1) == SHAPE and call(k=0) == SHAPE
+        assert call(x=None) == NULL and call(rw=None) == NULL and call(ws=None) == NULL
+        assert call(ds=None) == NULL and call(out=None) == NULL
+        assert call(x=C.c_void_p(8)) == ALIGN and call(ws=C.c_void_p(16)) == ALIGN
+        assert call(rb=C.c_void_p(2)) == ALIGN and call(gs=C.c_void_p(257)) == ALIGN
+        assert call(out=C.c_void_p(24)) == ALIGN
