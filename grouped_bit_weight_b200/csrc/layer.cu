@@ -31,6 +31,8 @@
 // keeps the down projection's input at 16 bits of mantissa, at one more mma
 // and no conversion.  A unit's K is split over several warps (joined through
 // shared memory in a fixed order) when a CTA has fewer units than warps.
+#include <algorithm>
+
 #include "common.cuh"
 #include "launch.cuh"
 #include "route.cuh"
@@ -43,7 +45,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxE = 1024;
 constexpr int kMaxT = 32;
 constexpr int kMaxP = 512;
-constexpr int NT = kMaxT / 8;      // token tiles (MMA N = 8) of one expert
+constexpr int NT = kMaxT / 4;      // most column tiles (MMA N = 8) of one expert
 constexpr int CKB = 128;           // bytes per weight row and stage: 256 k
 constexpr int D = 4;               // stages per warp
 constexpr int kStage = 16 * CKB;   // 2 KB
@@ -142,57 +144,52 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router(const LayerArgs a) 
 // without it).
 constexpr float kLevelScale = 1.437f;
 
-// Codebook values as bf16 bit patterns.
-__device__ __forceinline__ uint32_t code_bf16(Fmt f, int q) {
-  constexpr float nf4[16] = {-1.0f, -0.6961928009986877f, -0.5250730514526367f,
-                             -0.39491748809814453f, -0.28444138169288635f, -0.18477343022823334f,
-                             -0.09105003625154495f, 0.0f, 0.07958029955625534f,
-                             0.16093020141124725f, 0.24611230194568634f, 0.33791524171829224f,
-                             0.44070982933044434f, 0.5626170039176941f, 0.7229568362236023f, 1.0f};
-  constexpr float e2m1[8] = {0.0f, 0.5f, 1.0f, 1.5f, 2.0f, 3.0f, 4.0f, 6.0f};
-  const float v = f == Fmt::NF4 ? __fmul_rn(nf4[q], kLevelScale) : (q & 8) ? -e2m1[q & 7] : e2m1[q & 7];
+// Codebook value q as its bf16 bit pattern (a select tree: an indexed array
+// would live in local memory).
+template <Fmt F>
+__device__ __forceinline__ uint32_t code_bf16(int q) {
+  float v;
+  if (F == Fmt::NF4) {
+    const float a0 = q & 1 ? -0.6961928009986877f : -1.0f;
+    const float a1 = q & 1 ? -0.39491748809814453f : -0.5250730514526367f;
+    const float a2 = q & 1 ? -0.18477343022823334f : -0.28444138169288635f;
+    const float a3 = q & 1 ? 0.0f : -0.09105003625154495f;
+    const float a4 = q & 1 ? 0.16093020141124725f : 0.07958029955625534f;
+    const float a5 = q & 1 ? 0.33791524171829224f : 0.24611230194568634f;
+    const float a6 = q & 1 ? 0.5626170039176941f : 0.44070982933044434f;
+    const float a7 = q & 1 ? 1.0f : 0.7229568362236023f;
+    const float b0 = q & 2 ? a1 : a0, b1 = q & 2 ? a3 : a2, b2 = q & 2 ? a5 : a4, b3 = q & 2 ? a7 : a6;
+    const float c0 = q & 4 ? b1 : b0, c1 = q & 4 ? b3 : b2;
+    v = __fmul_rn(q & 8 ? c1 : c0, kLevelScale);
+  } else {
+    // e2m1: 0, 1/2, then (1 + m / 2) 2^(x - 1)
+    const int x = (q >> 1) & 3, m = q & 1;
+    v = x ? (float)((2 + m) << (x - 1)) * 0.5f : 0.5f * m;
+    v = q & 8 ? -v : v;
+  }
   return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
 // D += A (16 x 16, row) * B (16 x 8, col), bf16 in, fp32 out.
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+// A table entry: the table does not change after the block has built it, so
+// the load may be moved freely (its address comes from data read later).
+__device__ __forceinline__ uint32_t lds_table(uint32_t addr) {
   uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr));
+  asm("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-// 16 bytes from L2: h is written by other CTAs of the same launch.
-__device__ __forceinline__ uint4 ldcg128(const uint16_t* p) {
-  uint4 v;
-  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
 __device__ __forceinline__ int ld_acquire(const int* p) {
   int v;
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -207,12 +204,15 @@ __device__ __forceinline__ uint32_t swizzle(int r) {
   return F == Fmt::NF4 ? 2u * (r & 3) : (uint32_t)(r & 7);
 }
 
-// One phase's share of this CTA: units [u0, u0 + n) of K / 256 chunks each,
-// every unit split into S parts.
+// One phase's share of this CTA: units [u0, u0 + n) of nc chunks (256 k)
+// each, every unit split into 1 << lgS parts.
 struct Share {
   int phase;  // 0: gate_up, 1: down
-  int u0, n, S;
-  int nc;     // chunks of a full unit
+  int u0, n, lgS;
+  int nc;
+  __device__ __forceinline__ int items() const { return n << lgS; }
+  // first chunk of part sp
+  __device__ __forceinline__ int chunk0(int sp) const { return (sp * nc) >> lgS; }
 };
 
 // A warp's place in its stream of (item, chunk) over both shares.
@@ -222,8 +222,14 @@ struct Cursor {
   const uint8_t* sc;        // scales of row 0 of the unit
 };
 
-template <Fmt F, int NPL>
-__global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a) {
+// Column tiles of an expert with cnt rows.  Phase A: 8 rows a tile.  Phase B:
+// 4 rows, the high parts of h in columns 0..3 and the low parts in 4..7.
+__device__ __forceinline__ int col_tiles(int phase, int cnt) {
+  return phase ? (cnt + 3) >> 2 : (cnt + 7) >> 3;
+}
+
+template <Fmt F, int NPL, bool kFew>
+__global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, const int aligned) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const LayerProblem& p = a.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -241,10 +247,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a) {
   // misc: 0 claim A, 1 claim B, 2 next claim, 3 abort, 4 active experts, 5 last of a tile,
   // 6 rows of the largest expert
 
-  for (int b = warp; b < 256; b += kWarps) {
-    const uint32_t lo = code_bf16(F, F == Fmt::NF4 ? b >> 4 : b & 15);
-    const uint32_t hi = code_bf16(F, F == Fmt::NF4 ? b & 15 : b >> 4);
-    sts32(sbase + Smem::table + b * 256 + lane * 4, lo | (hi << 16));
+  {
+    // warp w writes the 16 bytes of high nibble w: lane l holds level l & 15
+    const uint32_t level = code_bf16<F>(lane & 15), top = code_bf16<F>(warp);
+#pragma unroll
+    for (int l = 0; l < 16; ++l) {
+      const uint32_t low = __shfl_sync(0xffffffffu, level, l);
+      sts32(sbase + Smem::table + (warp * 16 + l) * 256 + lane * 4,
+            F == Fmt::NF4 ? top | (low << 16) : low | (top << 16));
+    }
   }
   for (int e = threadIdx.x; e < E; e += kThreads) count[e] = 0;
   if (threadIdx.x == 0) misc[3] = misc[6] = 0;
@@ -301,26 +312,33 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a) {
   }
   __syncthreads();
   const int A = misc[4];
-  const int most = (misc[6] + 7) / 8;  // token tiles of the largest expert
   const int G = gridDim.x;
   int next_a = misc[0], next_b = misc[1];
   const int tiles_a = I / 8, tiles_b = H / 16;
 
+  const int largest = misc[6];  // rows of the largest expert
   auto make_share = [&](int phase, int idx) -> Share {
     Share s;
     s.phase = phase;
-    const int64_t total = phase ? (int64_t)tiles_b * A : (int64_t)tiles_a * A;
-    s.u0 = (int)(total * idx / G);
-    s.n = idx < G ? (int)(total * (idx + 1) / G) - s.u0 : 0;
-    s.nc = ((phase ? I : H) + 255) / 256;
+    const int tiles = phase ? tiles_b : tiles_a;
+    // phase B, aligned: whole tiles, so that no tile is shared between CTAs
+    const int per = phase && aligned ? A : 1;
+    const unsigned total = (unsigned)(tiles * (A / per));
+    const unsigned q = total / (unsigned)G, r = total - q * (unsigned)G;
+    s.u0 = (int)(q * idx + min((unsigned)idx, r)) * per;
+    s.n = idx < G ? (int)(q + (idx < (int)r)) * per : 0;
+    s.nc = ((phase ? I : H) + 255) >> 8;
     // the split with the least work for the busiest warp, as far as the
-    // partial sums (4 rows of 32 for each token tile) fit
-    s.S = 1;
+    // partial sums (4 rows of 32 for each column tile) fit
+    const int rows4 = 4 * col_tiles(phase, largest);
+    s.lgS = 0;
     int best = ((s.n + kWarps - 1) / kWarps) * 8;  // eighths of a unit
-    for (int S = 2; S <= 8; S *= 2) {
-      if (S > s.nc || s.n * S * most * 4 > kParts) break;
-      const int cost = ((s.n * S + kWarps - 1) / kWarps) * (8 / S);
-      if (cost < best) { best = cost; s.S = S; }
+#pragma unroll
+    for (int l = 1; l <= 3; ++l) {
+      if ((1 << l) <= s.nc && (s.n << l) * rows4 <= kParts) {
+        const int cost = (((s.n << l) + kWarps - 1) / kWarps) << (3 - l);
+        if (cost < best) { best = cost; s.lgS = l; }
+      }
     }
     return s;
   };
@@ -344,9 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a) {
   auto seek = [&](Cursor& cur, const Share& s, int item) {
     cur.phase = s.phase;
     cur.item = item;
-    const int u = item / s.S, sp = item - u * s.S;
-    cur.c = sp * s.nc / s.S;
-    cur.c1 = (sp + 1) * s.nc / s.S;
+    const int u = item >> s.lgS, sp = item - (u << s.lgS);
+    cur.c = s.chunk0(sp);
+    cur.c1 = s.chunk0(sp + 1);
     int ai, tile;
     unit_of(s.phase, s.u0 + u, ai, tile);
     const int64_t e = active[ai];
@@ -421,16 +439,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a) {
   bool more;                     // whether there is one
   auto start = [&]() {  // the stream from share sa's first item
     more = true;
-    if (warp < sa.n * sa.S) seek(pc, sa, warp);
-    else if (warp < sb.n * sb.S) seek(pc, sb, warp);
+    if (warp < sa.items()) seek(pc, sa, warp);
+    else if (warp < sb.items()) seek(pc, sb, warp);
     else more = false;
   };
   auto advance = [&]() {
     if (++pc.c < pc.c1) return;
     const Share& s = pc.phase ? sb : sa;
     const int item = pc.item + kWarps;
-    if (item < s.n * s.S) seek(pc, s, item);
-    else if (pc.phase == 0 && warp < sb.n * sb.S) seek(pc, sb, warp);
+    if (item < s.items()) seek(pc, s, item);
+    else if (pc.phase == 0 && warp < sb.items()) seek(pc, sb, warp);
     else more = false;
   };
   auto issue = [&]() {
@@ -447,106 +465,147 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a) {
   const int g = lane >> 2, t4 = lane & 3;
   const uint32_t lut = (uint32_t)lane * 4u;
 
-  // Sums one item's chunks: acc[nt] = D fragment of token tile nt.
-  auto run_item = [&](const Share& s, int item, float (&acc)[NT][4], int& cnt, int& r0, int& tile) {
-    const int u = item / s.S, sp = item - u * s.S;
-    int ai;
-    unit_of(s.phase, s.u0 + u, ai, tile);
-    r0 = first[ai];
-    cnt = first[ai + 1] - r0;
-    const int c0 = sp * s.nc / s.S, c1 = (sp + 1) * s.nc / s.S;
-    const int64_t kb = s.phase ? kb_b : kb_a;
+  constexpr int kSecond = F == Fmt::NF4 ? 8 : 32;  // distance of a lane's second 8 k
+
+  // This lane's column in column tile i of an expert's rows, at its first k of
+  // a stage, or null.
+  auto column = [&](int phase, int i, int r0, int cnt) -> const uint16_t* {
+    const int row = phase ? i * 4 + (g & 3) : i * 8 + g;
+    if (row >= cnt) return nullptr;
+    const int slot = rows[r0 + row], k0 = t4 * (F == Fmt::NF4 ? 16 : 8);
+    if (phase == 0) return p.x + (int64_t)(slot / k) * H + k0;
+    return (g < 4 ? a.hhi : a.hlo) + (int64_t)slot * I + k0;
+  };
+  // plain loads: h was written by other CTAs of this launch, before the wait
+  auto load_x = [&](const uint16_t* src, int c, int b, uint4& x0, uint4& x1) {
+    x0 = x1 = make_uint4(0, 0, 0, 0);
+    if (src) {
+      const uint16_t* xp = src + c * 256 + b * 64;
+      x0 = *reinterpret_cast<const uint4*>(xp);
+      x1 = *reinterpret_cast<const uint4*>(xp + kSecond);
+    }
+  };
+  // Weight fragments of block b of a stage: the lane's 16 weights of rows g and
+  // g + 8 (same swizzle).  NF4, one scale block: bytes 8 t4 .. of its 32;
+  // MXFP4, two blocks of 16 bytes: 4 bytes of each, so that every mma stays
+  // inside a scale block.
+  auto decode = [&](const uint8_t* st, int b, uint32_t (&fa)[8], uint32_t (&fb)[8]) {
+    uint2 wa, wb;
+    if (F == Fmt::NF4) {
+      const uint32_t at = ((uint32_t)(2 * b + (t4 >> 1)) ^ swizzle<F>(g)) * 16 + (t4 & 1) * 8;
+      wa = *reinterpret_cast<const uint2*>(st + at);
+      wb = *reinterpret_cast<const uint2*>(st + 8 * CKB + at);
+    } else {
+      const uint32_t a0 = ((uint32_t)(2 * b) ^ swizzle<F>(g)) * 16 + t4 * 4;
+      const uint32_t a1 = ((uint32_t)(2 * b + 1) ^ swizzle<F>(g)) * 16 + t4 * 4;
+      auto word = [&](uint32_t at) { return *reinterpret_cast<const uint32_t*>(st + at); };
+      wa = make_uint2(word(a0), word(a1));
+      wb = make_uint2(word(8 * CKB + a0), word(8 * CKB + a1));
+    }
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t sel = 0x7704u | ((uint32_t)(i & 3) << 4);  // byte i & 3 to bits 8..15
+      fa[i] = lds_table(sbase + Smem::table + prmt(i < 4 ? wa.x : wa.y, lut, sel));
+      fb[i] = lds_table(sbase + Smem::table + prmt(i < 4 ? wb.x : wb.y, lut, sel));
+    }
+  };
+  // acc += block b (scale words sg, sh of rows g, g + 8) times the lane's x
+  auto mma_block = [&](float (&acc)[4], const uint32_t (&fa)[8], const uint32_t (&fb)[8],
+                       const uint4& x0, const uint4& x1, uint32_t sg, uint32_t sh) {
+    const uint32_t xb[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+    constexpr int kPer = F == Fmt::NF4 ? 4 : 2;  // mma of one scale block
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-    // this lane's column of each token tile
-    const uint16_t* src[NT];
-    int64_t lo_off = 0;
+    for (int m0 = 0; m0 < 4; m0 += kPer) {
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      src[i] = nullptr;
-      if (i * 8 + g < cnt) {
-        const int slot = rows[r0 + i * 8 + g];
-        src[i] = s.phase ? a.hhi + (int64_t)slot * I : p.x + (int64_t)(slot / k) * H;
+      for (int m = m0; m < m0 + kPer; ++m) {
+        const uint32_t fr[4] = {fa[2 * m], fb[2 * m], fa[2 * m + 1], fb[2 * m + 1]};
+        mma16816(d, fr, xb[2 * m], xb[2 * m + 1]);
+      }
+      const uint32_t wg = F == Fmt::NF4 ? sg : m0 ? sg & 0xFFFF0000u : sg << 16;
+      const uint32_t wh = F == Fmt::NF4 ? sh : m0 ? sh & 0xFFFF0000u : sh << 16;
+      acc[0] = fmaf(d[0], __uint_as_float(wg), acc[0]);
+      acc[1] = fmaf(d[1], __uint_as_float(wg), acc[1]);
+      acc[2] = fmaf(d[2], __uint_as_float(wh), acc[2]);
+      acc[3] = fmaf(d[3], __uint_as_float(wh), acc[3]);
+    }
+  };
+
+  // Chunks [c0, c1) of one unit against N column tiles.  One tile (the usual
+  // case): the columns of the next chunk are loaded while this one is
+  // multiplied.
+  auto run_one = [&](int phase, int c0, int c1, int r0, int cnt, float (&acc)[4]) {
+    const int K = phase ? I : H;
+    const uint16_t* src = column(phase, 0, r0, cnt);
+    uint4 x[4][2];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) load_x(c0 * 256 + b * 64 < K ? src : nullptr, c0, b, x[b][0], x[b][1]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = 0.0f;
+    for (int c = c0; c < c1; ++c, ++q_out) {
+      issue();
+      uint4 y[4][2];
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        load_x(c + 1 < c1 && (c + 1) * 256 + b * 64 < K ? src : nullptr, c + 1, b, y[b][0], y[b][1]);
+      cp_async_wait_group<D - 1>();
+      __syncwarp();
+      const uint32_t slot = q_out & (D - 1);
+      const uint8_t* st = smem + Smem::ring + (warp * D + slot) * kStage + g * CKB;
+      const uint8_t* ss = smem + Smem::scales + (warp * D + slot) * kScStage + g * 16;
+      const uint4 s0 = *reinterpret_cast<const uint4*>(ss);
+      const uint4 s1 = *reinterpret_cast<const uint4*>(ss + 8 * 16);
+      const uint32_t sx[4] = {s0.x, s0.y, s0.z, s0.w}, sy[4] = {s1.x, s1.y, s1.z, s1.w};
+      const int nb = (K - c * 256) >> 6;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (b < nb) {
+          uint32_t fa[8], fb[8];
+          decode(st, b, fa, fb);
+          mma_block(acc, fa, fb, x[b][0], x[b][1], sx[b], sy[b]);
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        x[b][0] = y[b][0];
+        x[b][1] = y[b][1];
       }
     }
-    if (s.phase) lo_off = a.hlo - a.hhi;
+  };
+  auto run_many = [&](int phase, int c0, int c1, int r0, int cnt, int nt, auto& acc) {
+    constexpr int N = sizeof(acc) / sizeof(acc[0]);
+    const int K = phase ? I : H;
+    const uint16_t* src[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      src[i] = i < nt ? column(phase, i, r0, cnt) : nullptr;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+    }
     for (int c = c0; c < c1; ++c, ++q_out) {
       issue();
       cp_async_wait_group<D - 1>();
       __syncwarp();
       const uint32_t slot = q_out & (D - 1);
-      const uint32_t st = ring + slot * kStage + g * CKB;
-      const uint4 s0 = lds128(scr + slot * kScStage + g * 16);
-      const uint4 s1 = lds128(scr + slot * kScStage + (g + 8) * 16);
-      const int nb = min(4, (int)((kb - (int64_t)c * CKB) >> 5));
+      const uint8_t* st = smem + Smem::ring + (warp * D + slot) * kStage + g * CKB;
+      const uint8_t* ss = smem + Smem::scales + (warp * D + slot) * kScStage + g * 16;
+      const int nb = min(4, (K - c * 256) >> 6);
+      for (int b = 0; b < nb; ++b) {
+        uint4 x0[2], x1[2];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        if (b >= nb) break;
-        // the lane's 16 weights of rows g and g + 8 (same swizzle): NF4, one
-        // scale block: bytes 8 t4 .. of its 32; MXFP4, two blocks of 16 bytes:
-        // 4 bytes of each, so that every mma stays inside a scale block
-        uint2 wa, wb;
-        if (F == Fmt::NF4) {
-          const uint32_t at = ((uint32_t)(2 * b + (t4 >> 1)) ^ swizzle<F>(g)) * 16 + (t4 & 1) * 8;
-          wa = lds64(st + at);
-          wb = lds64(st + 8 * CKB + at);
-        } else {
-          const uint32_t a0 = ((uint32_t)(2 * b) ^ swizzle<F>(g)) * 16 + t4 * 4;
-          const uint32_t a1 = ((uint32_t)(2 * b + 1) ^ swizzle<F>(g)) * 16 + t4 * 4;
-          wa = make_uint2(lds32(st + a0), lds32(st + a1));
-          wb = make_uint2(lds32(st + 8 * CKB + a0), lds32(st + 8 * CKB + a1));
-        }
+        for (int i = 0; i < 2; ++i) load_x(src[i], c, b, x0[i], x1[i]);
+        const uint32_t sg = *reinterpret_cast<const uint32_t*>(ss + b * 4);
+        const uint32_t sh = *reinterpret_cast<const uint32_t*>(ss + 8 * 16 + b * 4);
         uint32_t fa[8], fb[8];
+        decode(st, b, fa, fb);
+        mma_block(acc[0], fa, fb, x0[0], x1[0], sg, sh);
+        mma_block(acc[1], fa, fb, x0[1], x1[1], sg, sh);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t sel = 0x7704u | ((uint32_t)(i & 3) << 4);  // byte i & 3 to bits 8..15
-          fa[i] = lds32(sbase + Smem::table + prmt(i < 4 ? wa.x : wa.y, lut, sel));
-          fb[i] = lds32(sbase + Smem::table + prmt(i < 4 ? wb.x : wb.y, lut, sel));
-        }
-        const uint32_t sx[4] = {s0.x, s0.y, s0.z, s0.w}, sy[4] = {s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          if (i * 8 >= cnt) break;
-          uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0, l0 = x0, l1 = x0;
-          if (src[i]) {
-            constexpr int kSecond = F == Fmt::NF4 ? 8 : 32;  // the second 8 of the lane's k
-            const uint16_t* xp = src[i] + c * 256 + b * 64 + t4 * (F == Fmt::NF4 ? 16 : 8);
-            if (s.phase) {
-              x0 = ldcg128(xp);
-              x1 = ldcg128(xp + kSecond);
-              l0 = ldcg128(xp + lo_off);
-              l1 = ldcg128(xp + lo_off + kSecond);
-            } else {
-              x0 = __ldg(reinterpret_cast<const uint4*>(xp));
-              x1 = __ldg(reinterpret_cast<const uint4*>(xp + kSecond));
-            }
-          }
-          const uint32_t xb[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-          const uint32_t lb[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
-          constexpr int kPer = F == Fmt::NF4 ? 4 : 2;  // mma of one scale block
-#pragma unroll
-          for (int m0 = 0; m0 < 4; m0 += kPer) {
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int m = m0; m < m0 + kPer; ++m) {
-              const uint32_t fr[4] = {fa[2 * m], fb[2 * m], fa[2 * m + 1], fb[2 * m + 1]};
-              mma16816(d, fr, xb[2 * m], xb[2 * m + 1]);
-              if (s.phase) mma16816(d, fr, lb[2 * m], lb[2 * m + 1]);
-            }
-            float fg, fh;
-            if (F == Fmt::NF4) {
-              fg = __uint_as_float(sx[b]);
-              fh = __uint_as_float(sy[b]);
-            } else {
-              fg = __uint_as_float(m0 ? sx[b] & 0xFFFF0000u : sx[b] << 16);
-              fh = __uint_as_float(m0 ? sy[b] & 0xFFFF0000u : sy[b] << 16);
-            }
-            acc[i][0] = fmaf(d[0], fg, acc[i][0]);
-            acc[i][1] = fmaf(d[1], fg, acc[i][1]);
-            acc[i][2] = fmaf(d[2], fh, acc[i][2]);
-            acc[i][3] = fmaf(d[3], fh, acc[i][3]);
+        for (int i = 2; i < N; ++i) {
+          if (i < nt) {
+            load_x(src[i], c, b, x0[0], x1[0]);
+            mma_block(acc[i], fa, fb, x0[0], x1[0], sg, sh);
           }
         }
       }
@@ -554,14 +613,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a) {
     }
   };
 
-  // Writes one token tile of a finished unit: h (phase A) or y (phase B).
+  // Writes one column tile of a finished unit: h (phase A) or y (phase B).
   auto finish = [&](int phase, const float (&d)[4], int cnt, int r0, int tile, int nt) {
+    if (phase == 0) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int c = nt * 8 + 2 * t4 + j;
-      if (c < cnt) {
-        const int slot = rows[r0 + c];
-        if (phase == 0) {
+      for (int j = 0; j < 2; ++j) {
+        const int c = nt * 8 + 2 * t4 + j;
+        if (c < cnt) {
+          const int slot = rows[r0 + c];
           const float h = __fdiv_rn(d[j], 1.0f + expf(-d[j])) * d[2 + j];
           const __nv_bfloat16 hi = __float2bfloat16_rn(h);
           // an infinite high part keeps a zero low part (inf - inf is NaN)
@@ -569,10 +628,20 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a) {
           const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(low) ? low : 0.0f);
           a.hhi[(int64_t)slot * I + tile * 8 + g] = __bfloat16_as_ushort(hi);
           a.hlo[(int64_t)slot * I + tile * 8 + g] = __bfloat16_as_ushort(lo);
-        } else {
-          float* y = a.y + (int64_t)slot * H + tile * 16 + g;
-          y[0] = d[j];
-          y[8] = d[2 + j];
+        }
+      }
+    } else {
+      // high and low parts of a row: columns c and c + 4, lanes t4 and t4 + 2
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = d[j] + __shfl_xor_sync(0xffffffffu, d[j], 2);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int c = nt * 4 + 2 * t4 + j;
+        if (t4 < 2 && c < cnt) {
+          float* y = a.y + (int64_t)rows[r0 + c] * H + tile * 16 + g;
+          y[0] = v[j];
+          y[8] = v[2 + j];
         }
       }
     }
@@ -581,38 +650,51 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a) {
   float* parts = reinterpret_cast<float*>(smem + Smem::table + 128);  // row i at i * 64 floats
   // All items of a share, their partial sums joined, results written.
   auto run_share = [&](const Share& s) {
-    for (int item = warp; item < s.n * s.S; item += kWarps) {
-      float acc[NT][4];
-      int cnt, r0, tile;
-      run_item(s, item, acc, cnt, r0, tile);
-      if (s.S == 1) {
+    const int items = s.items();
+    const int per = items ? kParts / items : 0;  // part rows of an item: [tile][4] of 32 floats
+    for (int item = warp; item < items; item += kWarps) {
+      const int u = item >> s.lgS, sp = item - (u << s.lgS);
+      int ai, tile;
+      unit_of(s.phase, s.u0 + u, ai, tile);
+      const int r0 = first[ai], cnt = first[ai + 1] - r0;
+      const int c0 = s.chunk0(sp), c1 = s.chunk0(sp + 1), nt = col_tiles(s.phase, cnt);
+      auto store = [&](const float (&d)[4], int i) {
+        if (s.lgS == 0) {
+          finish(s.phase, d, cnt, r0, tile, i);
+        } else {
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-          if (i * 8 < cnt) finish(s.phase, acc[i], cnt, r0, tile, i);
+          for (int j = 0; j < 4; ++j) parts[(item * per + i * 4 + j) * 64 + lane] = d[j];
+        }
+      };
+      if (nt == 1) {
+        float acc[4];
+        run_one(s.phase, c0, c1, r0, cnt, acc);
+        store(acc, 0);
+      } else if (kFew || nt == 2) {
+        float acc[2][4];
+        run_many(s.phase, c0, c1, r0, cnt, nt, acc);
+        store(acc[0], 0);
+        store(acc[1], 1);
       } else {
-        // rows of 32 floats: [item][nt][4], nt up to kParts / (4 n S)
-        const int per = kParts / (s.n * s.S);
+        float acc[NT][4];
+        run_many(s.phase, c0, c1, r0, cnt, nt, acc);
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-          if (i * 8 < cnt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) parts[(item * per + i * 4 + j) * 64 + lane] = acc[i][j];
+          if (i < nt) store(acc[i], i);
       }
     }
-    if (s.S > 1) {
+    if (s.lgS > 0) {
       __syncthreads();
-      const int per = kParts / (s.n * s.S);
-      for (int w = warp; w < s.n * NT; w += kWarps) {
-        const int u = w / NT, i = w % NT;
+      for (int u = 0; u < s.n; ++u) {
         int ai, tile;
         unit_of(s.phase, s.u0 + u, ai, tile);
-        const int r0 = first[ai], cnt = first[ai + 1] - r0;
-        if (i * 8 < cnt) {
+        const int r0 = first[ai], cnt = first[ai + 1] - r0, nt = col_tiles(s.phase, cnt);
+        for (int i = (warp - u * nt) & (kWarps - 1); i < nt; i += kWarps) {
           float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          for (int sp = 0; sp < s.S; ++sp)
+          for (int sp = 0; sp < (1 << s.lgS); ++sp)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              d[j] += parts[((u * s.S + sp) * per + i * 4 + j) * 64 + lane];
+              d[j] += parts[(((u << s.lgS) + sp) * per + i * 4 + j) * 64 + lane];
           finish(s.phase, d, cnt, r0, tile, i);
         }
       }
@@ -661,20 +743,24 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a) {
   while (next_b < G && !misc[3]) {
     run_share(sb);
     if (threadIdx.x == 0) misc[2] = atomicAdd(&a.counters[1], 1);
-    __threadfence();
+    if (!aligned) __threadfence();
     __syncthreads();
-    // tiles that this share touches: the CTA that brings a tile's count of
-    // finished experts to A combines it
+    // Tiles that this share touches: an aligned share holds all of a tile's
+    // experts; else the CTA that brings the tile's count to A combines it.
     if (sb.n > 0) {
       const int first_tile = sb.u0 / A, last_tile = (sb.u0 + sb.n - 1) / A;
       for (int tile = first_tile; tile <= last_tile; ++tile) {
-        if (threadIdx.x == 0) {
-          const int mine = min(sb.u0 + sb.n, (tile + 1) * A) - max(sb.u0, tile * A);
-          misc[5] = atomicAdd(&a.counters[kCounters + tile], mine) + mine == A;
-          __threadfence();
+        bool whole = true;
+        if (!aligned) {
+          if (threadIdx.x == 0) {
+            const int mine = min(sb.u0 + sb.n, (tile + 1) * A) - max(sb.u0, tile * A);
+            misc[5] = atomicAdd(&a.counters[kCounters + tile], mine) + mine == A;
+            __threadfence();
+          }
+          __syncthreads();
+          whole = misc[5];
         }
-        __syncthreads();
-        if (misc[5]) {
+        if (whole) {
           for (int i = threadIdx.x; i < T * 16; i += kThreads) {
             const int t = i >> 4, n = tile * 16 + (i & 15);
             float v = 0.0f;
@@ -685,13 +771,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a) {
             p.out[(int64_t)t * H + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
           }
         }
-        __syncthreads();
+        if (!aligned) __syncthreads();
       }
     }
     next_b = misc[2];
     if (next_b < G) {
       cp_async_wait_group<0>();
-      __syncthreads();
+      __syncthreads();  // before misc[2] and the part rows are written again
       sa.n = 0;
       sb = make_share(1, next_b);
       sv_to = 0xffffffffu;
@@ -721,9 +807,9 @@ Layout layout_of(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I) {
   return l;
 }
 
-template <Fmt F, int NPL>
+template <Fmt F, int NPL, bool kFew>
 cudaError_t launch_t(const LayerArgs& a, int num_sms, cudaStream_t s) {
-  constexpr auto k = moe_experts<F, NPL>;
+  constexpr auto k = moe_experts<F, NPL, kFew>;
   cudaError_t e = opt_in_smem<k>(Smem::total);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -732,7 +818,23 @@ cudaError_t launch_t(const LayerArgs& a, int num_sms, cudaStream_t s) {
   cfg.stream = s;
   e = cudaLaunchKernelEx(&cfg, moe_router, a);
   if (e != cudaSuccess) return e;
-  return launch_kernel<k>(num_sms, kThreads, Smem::total, s, true, a);
+  // Whole tiles of H per CTA in phase B spare the counting of a tile's experts
+  // across CTAs (about 1.5 us) but leave the last round of tiles uneven: taken
+  // when that costs at most kAlignChunks chunks of 2 KB per CTA (about 46 ns
+  // each at the measured HBM rate).
+  constexpr int64_t kAlignChunks = 32;
+  const int64_t tiles = a.p.H / 16, A = std::min<int64_t>(a.p.E, a.p.T * a.p.k);
+  const int64_t whole = (tiles + num_sms - 1) / num_sms * A;
+  const int64_t even = (tiles * A + num_sms - 1) / num_sms;
+  const int aligned = (whole - even) * ((a.p.I + 255) / 256) <= kAlignChunks;
+  return launch_kernel<k>(num_sms, kThreads, Smem::total, s, true, a, aligned);
+}
+
+template <Fmt F>
+cudaError_t launch_f(const LayerArgs& a, int num_sms, cudaStream_t s) {
+  const bool few = a.p.T <= 8;  // at most 8 rows per expert: two column tiles
+  if (a.p.E <= 128) return few ? launch_t<F, 4, true>(a, num_sms, s) : launch_t<F, 4, false>(a, num_sms, s);
+  return launch_t<F, 32, false>(a, num_sms, s);
 }
 
 }  // namespace
@@ -752,11 +854,7 @@ cudaError_t launch_layer(Fmt f, const LayerProblem& p, void* workspace, int num_
                     reinterpret_cast<uint16_t*>(w + l.hlo),
                     reinterpret_cast<float*>(w + l.y),
                     reinterpret_cast<int*>(w + l.counters)};
-  if (p.E <= 256)
-    return f == Fmt::NF4 ? launch_t<Fmt::NF4, 8>(a, num_sms, s)
-                         : launch_t<Fmt::MXFP4, 8>(a, num_sms, s);
-  return f == Fmt::NF4 ? launch_t<Fmt::NF4, 32>(a, num_sms, s)
-                       : launch_t<Fmt::MXFP4, 32>(a, num_sms, s);
+  return f == Fmt::NF4 ? launch_f<Fmt::NF4>(a, num_sms, s) : launch_f<Fmt::MXFP4>(a, num_sms, s);
 }
 
 }  // namespace gbw
