@@ -51,28 +51,75 @@ __device__ __forceinline__ void choose(const TL* row, int E, int k, int renorm, 
     key[j] = e < E ? order_key(no_nan(load_logit(row + e))) : 0u;
   }
   float all = 0.0f, m = 0.0f, v = 0.0f;
-  for (int s = 0; s < k; ++s) {
-    uint32_t lk = 0u;
-    int le = 0;
+  if (NPL <= 4) {
+    // each lane's keys in falling order (equal ones by index), so that a
+    // choice looks at one key of each lane
+    int at[NPL];
 #pragma unroll
-    for (int j = 0; j < NPL; ++j)
-      if (key[j] > lk) { lk = key[j]; le = j * 32 + lane; }
-    const uint32_t g = __reduce_max_sync(0xffffffffu, lk);
-    const int e = (int)__reduce_min_sync(0xffffffffu, lk == g ? (unsigned)le : 0xffffffffu);
-    if (s == 0) {
-      m = key_value(g);
-      if (!renorm) {
-        float t = 0.0f;
+    for (int j = 0; j < NPL; ++j) at[j] = j * 32 + lane;
 #pragma unroll
-        for (int j = 0; j < NPL; ++j)
-          if (key[j]) t += share(key_value(key[j]), m);
-        all = warp_sum(t);
+    for (int i = 1; i < NPL; ++i)
+#pragma unroll
+      for (int j = i; j > 0; --j)
+        if (key[j] > key[j - 1]) {
+          const uint32_t tk = key[j];
+          key[j] = key[j - 1];
+          key[j - 1] = tk;
+          const int ta = at[j];
+          at[j] = at[j - 1];
+          at[j - 1] = ta;
+        }
+    m = key_value(__reduce_max_sync(0xffffffffu, key[0]));
+    if (!renorm) {
+      float t = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NPL; ++j)
+        if (key[j]) t += share(key_value(key[j]), m);
+      all = warp_sum(t);
+    }
+    for (int s = 0; s < k; ++s) {
+      const uint32_t g = __reduce_max_sync(0xffffffffu, key[0]);
+      const unsigned who = __ballot_sync(0xffffffffu, key[0] == g);
+      int e;
+      if (who & (who - 1))  // a tie: the lowest index
+        e = (int)__reduce_min_sync(0xffffffffu, key[0] == g ? (unsigned)at[0] : 0xffffffffu);
+      else
+        e = __shfl_sync(0xffffffffu, at[0], __ffs(who) - 1);
+      if (lane == s) { id = e; v = key_value(g); }
+      if (at[0] == e) {
+#pragma unroll
+        for (int j = 0; j + 1 < NPL; ++j) {
+          key[j] = key[j + 1];
+          at[j] = at[j + 1];
+        }
+        key[NPL - 1] = 0u;
+        at[NPL - 1] = -1;
       }
     }
-    if (lane == s) { id = e; v = key_value(g); }
+  } else {
+    for (int s = 0; s < k; ++s) {
+      uint32_t lk = 0u;
+      int le = 0;
 #pragma unroll
-    for (int j = 0; j < NPL; ++j)
-      if (e == j * 32 + lane) key[j] = 0u;
+      for (int j = 0; j < NPL; ++j)
+        if (key[j] > lk) { lk = key[j]; le = j * 32 + lane; }
+      const uint32_t g = __reduce_max_sync(0xffffffffu, lk);
+      const int e = (int)__reduce_min_sync(0xffffffffu, lk == g ? (unsigned)le : 0xffffffffu);
+      if (s == 0) {
+        m = key_value(g);
+        if (!renorm) {
+          float t = 0.0f;
+#pragma unroll
+          for (int j = 0; j < NPL; ++j)
+            if (key[j]) t += share(key_value(key[j]), m);
+          all = warp_sum(t);
+        }
+      }
+      if (lane == s) { id = e; v = key_value(g); }
+#pragma unroll
+      for (int j = 0; j < NPL; ++j)
+        if (e == j * 32 + lane) key[j] = 0u;
+    }
   }
   const float p = lane < k ? share(v, m) : 0.0f;
   const float total = renorm ? warp_sum(p) : all;
