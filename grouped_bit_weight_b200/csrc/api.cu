@@ -476,7 +476,7 @@ static gbw_status moe_layer(Fmt f, const uint16_t* x, int64_t T, int64_t H, cons
   if (E > kMaxExperts) return fail(GBW_ERR_SHAPE, "at most 1024 experts");
   if (k > E || k > 16) return fail(GBW_ERR_SHAPE, "need k <= min(E, 16)");
   if (H > (int64_t)1 << 30 || I > (int64_t)1 << 29 || (int64_t)E * 2 * I > INT32_MAX ||
-      (int64_t)E * H > INT32_MAX)
+      (int64_t)E * H > INT32_MAX || H * I > (int64_t)1 << 33)
     return fail(GBW_ERR_SHAPE, "sizes exceed the 32-bit row indices");
   const int64_t need = gmoe_layer_workspace(T, E, k, H, I);
   if (T > 0 && (!x || !router_w || !gu || !gu_scale || !dn || !dn_scale || !out || !workspace))
@@ -486,11 +486,8 @@ static gbw_status moe_layer(Fmt f, const uint16_t* x, int64_t T, int64_t H, cons
     return fail(GBW_ERR_ALIGN, "x, router_w, packed weights and out must be 16-byte aligned");
   if (reinterpret_cast<uintptr_t>(workspace) & 255u)
     return fail(GBW_ERR_ALIGN, "the workspace must be 256-byte aligned");
-  if (f == Fmt::NF4 && (!aligned4(gu_scale) || !aligned4(dn_scale)))
-    return fail(GBW_ERR_ALIGN, "absmax must be 4-byte aligned");
-  if (f == Fmt::MXFP4 &&
-      ((reinterpret_cast<uintptr_t>(gu_scale) | reinterpret_cast<uintptr_t>(dn_scale)) & 1u))
-    return fail(GBW_ERR_ALIGN, "MXFP4 scales must be 2-byte aligned");
+  if (!aligned16(gu_scale) || !aligned16(dn_scale))
+    return fail(GBW_ERR_ALIGN, "the layer's scales must be 16-byte aligned");
   if (!aligned4(router_bias)) return fail(GBW_ERR_ALIGN, "router_bias must be 4-byte aligned");
   int* err = nullptr;
   int sms = 0;

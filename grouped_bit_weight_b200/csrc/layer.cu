@@ -40,7 +40,7 @@
 namespace gbw {
 namespace {
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 12;  // 168 registers a thread: nothing spills
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxE = 1024;
 constexpr int kMaxP = 512;
@@ -48,33 +48,40 @@ constexpr int kRows = 8;           // most rows of a group: rows of one expert t
 constexpr int CKB = 128;           // bytes per weight row and stage: 256 k
 constexpr int D = 4;               // stages per warp
 constexpr int kStage = 16 * CKB;   // 2 KB
-constexpr int kScStage = 256;      // scales of a stage
+constexpr int kScStage = 512;      // scales of a stage: two 16-byte units per row
 
 // Shared memory by address in the shared window (dynamic shared memory starts
 // at 1 KB).  The table lies at 64 KB: entry b of lane l at 65536 + b * 256 +
 // l * 4, so that one byte permute of a packed word gives the whole address.
-// The other half of each 256 bytes holds partial sums: two pieces per warp of
-// up to 8 rows of 32 floats.  The warps' rings lie on both sides of it.
-static_assert(kWarps * 2 * 8 <= 256, "partial sums fit beside the table");
+// The other half of each 256 bytes holds partial sums (kParts rows of 32
+// floats).  The warps' rings lie on both sides of it.  Everything stays within
+// the 196 KB carve-out, which leaves L1 60 KB: with the largest one its few
+// lines held up the loads of x.
+constexpr int kParts = 256;
 constexpr int kLowWarps = 7;
 struct Smem {
-  static constexpr int ids = 1024;               // [kMaxP] int
+  static constexpr int base = 1024;
+  static constexpr int ids = base;               // [kMaxP] int
   static constexpr int wts = ids + 4 * kMaxP;    // [kMaxP] float
   static constexpr int rows = wts + 4 * kMaxP;   // [kMaxP] uint16 slot of sorted row
   static constexpr int active = rows + 2 * kMaxP;  // [kMaxP] uint16 expert
   static constexpr int misc = active + 2 * kMaxP;  // 16 ints
-  static constexpr int part = misc + 64;           // [kWarps] scan parts
+  static constexpr int share = misc + 64;          // [2] Share, 32 bytes apart
+  static constexpr int part = share + 64;          // [kWarps] scan parts
   static constexpr int low_end = part + 4 * kWarps;
   static constexpr int table = 65536;
   static constexpr int ring_low = table - kLowWarps * D * kStage;
+  static constexpr int count = ring_low;  // [kMaxE] int: token bits, then first row (before the ring is used)
   static constexpr int ring_high = 2 * table;
   static constexpr int scales = ring_high + (kWarps - kLowWarps) * D * kStage;
   static constexpr int first = scales + kWarps * D * kScStage;  // [kMaxP + 4] int first sorted row
-  static constexpr int count = first + 4 * (kMaxP + 4);  // [kMaxE] int: token bits, then first row
-  static constexpr int end = count + 4 * kMaxE;
+  static constexpr int e8m0 = first + 4 * (kMaxP + 4);  // [256] float (MXFP4)
+  static constexpr int end = e8m0 + 1024;
+  static constexpr int bytes = end - base;  // dynamic
 };
 static_assert(Smem::low_end <= Smem::ring_low, "the small arrays fit below the rings");
-static_assert(Smem::end <= 232448, "shared memory exceeds the 227 KB a CTA can have");
+static_assert(Smem::ring_low + 4 * kMaxE <= Smem::table, "the expert counts fit the rings below");
+static_assert(Smem::end <= 196 * 1024, "shared memory within the 196 KB carve-out");
 
 struct LayerArgs {
   LayerProblem p;
@@ -143,7 +150,7 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router(const LayerArgs a) 
 // kernel 2
 // ----------------------------------------------------------------------
 
-// The NF4 levels enter the table times this, and the scales times its inverse:
+// The NF4 levels enter the table times this, and the sums are divided by it:
 // of the factors in [1, 2) it is the one whose products with the 16 levels
 // round to bf16 with the least error, 6.3e-4 of their root mean square (1.1e-3
 // without it).
@@ -201,10 +208,6 @@ __device__ __forceinline__ uint32_t lds_table(uint32_t addr) {
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ void sts64(uint32_t addr, uint32_t x, uint32_t y) {
-  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
-}
-
 __device__ __forceinline__ int ld_acquire(const int* p) {
   int v;
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -219,22 +222,24 @@ __device__ __forceinline__ uint32_t swizzle(int r) {
   return F == Fmt::NF4 ? 2u * (r & 3) : (uint32_t)(r & 7);
 }
 
-// One phase's share of this CTA: units [u0, u0 + n) of nc chunks (256 k)
-// each.  Warp w multiplies chunks [w L / 16, (w + 1) L / 16) of the L = n * nc,
-// so that all warps have the same work; a unit that ends up in several warps
-// is joined from their partial sums in order.
+// One phase's share of this CTA, kept in shared memory: units [u0, u0 + n) of
+// nc chunks (256 k) each.  Warp w takes whole units w, w + 12, .. of the first
+// `whole` (a multiple of 12) and parts of the others, which are cut into
+// 1 << lgS parts each and joined through shared memory.
 struct Share {
-  int phase;  // 0: gate_up, 1: down
-  int u0, n, nc;
-  __device__ __forceinline__ int begin(int w) const { return (w * n * nc) / kWarps; }
-};
-
-// A lane's place in its warp's stream of chunks to load.
-struct Cursor {
-  int phase, left;          // chunks left of this share's range
-  int ai, tile, c;          // group, output tile and chunk of the unit
-  const uint8_t* w;         // this lane's first 16 code bytes of the chunk
-  const uint8_t* sc;        // this lane's first scale of the chunk
+  int u0, n, nc, whole, lgS;
+  // Item `i` of warp w: chunks [c, c1) of unit u; false past the last.
+  __device__ __forceinline__ bool item(int w, int i, int& u, int& c, int& c1) const {
+    u = w + i * kWarps;
+    c = 0;
+    c1 = nc;
+    if (u < whole) return true;
+    const int l = lgS, j = u - whole, sp = j & ((1 << l) - 1);
+    u = whole + (j >> l);
+    c = (sp * nc) >> l;
+    c1 = ((sp + 1) * nc) >> l;
+    return u < n;
+  }
 };
 
 template <Fmt F, int NPL>
@@ -253,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
   volatile int* misc = reinterpret_cast<volatile int*>(smem + Smem::misc);
   int* part = reinterpret_cast<int*>(smem + Smem::part);
   int* count = reinterpret_cast<int*>(smem + Smem::count);
-  if (smem_u32(smem_raw) > Smem::ids) {  // (the layout above takes 1 KB as given)
+  if (smem_u32(smem_raw) != Smem::base) {  // (the layout above takes 1 KB as given)
     raise_error(p.err, GBW_DEVERR_TIMEOUT);
     return;
   }
@@ -261,22 +266,29 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
   // 6 rows of the largest expert
 
   {
-    // warp w writes the 16 bytes of high nibble w: lane l holds level l & 15
-    const uint32_t level = code_bf16<F>(lane & 15), top = code_bf16<F>(warp);
+    // a warp writes the 16 bytes of one high nibble: lane l holds level l & 15
+    const uint32_t level = code_bf16<F>(lane & 15);
+#pragma unroll 1
+    for (int h = warp; h < 16; h += kWarps) {
+      const uint32_t top = __shfl_sync(0xffffffffu, level, h);
 #pragma unroll
-    for (int l = 0; l < 16; ++l) {
-      const uint32_t low = __shfl_sync(0xffffffffu, level, l);
-      sts32(Smem::table + (warp * 16 + l) * 256 + lane * 4,
-            F == Fmt::NF4 ? top | (low << 16) : low | (top << 16));
+      for (int l = 0; l < 16; ++l) {
+        const uint32_t low = __shfl_sync(0xffffffffu, level, l);
+        sts32(Smem::table + (h * 16 + l) * 256 + lane * 4,
+              F == Fmt::NF4 ? top | (low << 16) : low | (top << 16));
+      }
     }
+    if (F == Fmt::MXFP4)
+      for (int i = threadIdx.x; i < 256; i += kThreads)
+        sts32(Smem::e8m0 + 4 * i, i == 0 ? 0x00400000u : i == 255 ? 0x7FC00000u : (uint32_t)i << 23);
   }
   for (int e = threadIdx.x; e < E; e += kThreads) count[e] = 0;
   if (threadIdx.x == 0) misc[3] = misc[6] = 0;
   __syncthreads();
   grid_dependency_wait();
-  if (threadIdx.x == 0) {
-    misc[0] = atomicAdd(&a.counters[0], 1);
-    misc[1] = atomicAdd(&a.counters[1], 1);
+  if (threadIdx.x >= kThreads - 2) {  // (a warp without a token, usually)
+    const int i = threadIdx.x - (kThreads - 2);
+    misc[i] = atomicAdd(&a.counters[i], 1);
   }
 
   // ---- the choice of experts, the same in every CTA
@@ -293,48 +305,59 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
   }
   __syncthreads();
   // rows sorted by expert and cut into groups of at most kRows rows of one
-  // expert: two packed scans (rows below, groups below), two experts per thread.
-  // count[e] holds the tokens of expert e as bits (T <= 32), so a slot's place
-  // among its expert's rows is the number of lower bits: the same in every
-  // CTA, as it must be for the groups to hold the same rows everywhere.
+  // expert: a packed scan (rows below, groups below) over three experts per
+  // thread.  count[e] holds the tokens of expert e as bits (T <= 32), so a
+  // slot's place among its expert's rows is the number of lower bits: the same
+  // in every CTA, as it must be for the groups to hold the same rows everywhere.
   {
-    static_assert(kMaxP <= kThreads, "one slot per thread");
-    const int e0 = threadIdx.x * 2;
-    const int c0 = e0 < E ? __popc(count[e0]) : 0, c1 = e0 + 1 < E ? __popc(count[e0 + 1]) : 0;
-    const int slot = threadIdx.x, id = slot < P ? ids[slot] : 0;
-    const int at = slot < P ? __popc(count[id] & ((1 << (slot / k)) - 1)) : 0;
-    const int g0 = (c0 + kRows - 1) / kRows, g1 = (c1 + kRows - 1) / kRows;
-    const int v = (c0 + c1) | ((g0 + g1) << 16);
-    int incl = v;
+    constexpr int kPer = 3;
+    static_assert(kPer * kThreads >= kMaxE && 2 * kThreads >= kMaxP, "one round each");
+    const int e0 = threadIdx.x * kPer;
+    int c[kPer], sum = 0, top = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      c[j] = e0 + j < E ? __popc(count[e0 + j]) : 0;
+      sum += c[j] | (((c[j] + kRows - 1) / kRows) << 16);
+      top = max(top, c[j]);
+    }
+    int at[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int slot = threadIdx.x + j * kThreads;
+      at[j] = slot < P ? __popc(count[ids[slot]] & ((1 << (slot / k)) - 1)) : 0;
+    }
+    int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int s = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += s;
     }
     if (lane == 31) part[warp] = incl;
-    const int top = __reduce_max_sync(0xffffffffu, max(c0, c1));
+    top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) atomicMax(const_cast<int*>(&misc[6]), top);
     __syncthreads();
-    int below = incl - v;
+    int below = incl - sum;
     for (int i = 0; i < warp; ++i) below += part[i];
-    const int r0 = below & 0xFFFF, a0 = below >> 16;
-    for (int j = 0; j < g0; ++j) {
-      active[a0 + j] = (uint16_t)e0;
-      first[a0 + j] = r0 + j * kRows;
-    }
-    for (int j = 0; j < g1; ++j) {
-      active[a0 + g0 + j] = (uint16_t)(e0 + 1);
-      first[a0 + g0 + j] = r0 + c0 + j * kRows;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int r = below & 0xFFFF, n = (c[j] + kRows - 1) / kRows;
+      for (int i = 0; i < n; ++i) {
+        active[(below >> 16) + i] = (uint16_t)(e0 + j);
+        first[(below >> 16) + i] = r + i * kRows;
+      }
+      if (e0 + j < E) count[e0 + j] = r;
+      below += c[j] | (n << 16);
     }
     if (threadIdx.x == kThreads - 1) {
-      misc[4] = (below + v) >> 16;
-      first[(below + v) >> 16] = P;
+      misc[4] = below >> 16;
+      first[below >> 16] = P;
     }
     __syncthreads();
-    if (e0 < E) count[e0] = r0;
-    if (e0 + 1 < E) count[e0 + 1] = r0 + c0;
-    __syncthreads();
-    if (slot < P) rows[count[id] + at] = (uint16_t)slot;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int slot = threadIdx.x + j * kThreads;
+      if (slot < P) rows[count[ids[slot]] + at[j]] = (uint16_t)slot;
+    }
   }
   __syncthreads();
   const int A = misc[4];  // groups
@@ -345,59 +368,78 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
   // Column tiles of 8: phase A, up to 8 rows of a group are one tile; phase B,
   // 4 rows a tile, the high parts of h in columns 0..3, the low ones in 4..7.
   const bool two_tiles = misc[6] > 4;  // some group has more than 4 rows
-  auto make_share = [&](int phase, int idx) __attribute__((always_inline)) -> Share {
-    Share s;
-    s.phase = phase;
+  auto share = [&](int phase) __attribute__((always_inline)) -> const Share& {
+    return *reinterpret_cast<const Share*>(smem + Smem::share + phase * 32);
+  };
+  // Share idx of a phase, by one thread; idx >= G: an empty one.
+  auto set_share = [&](int phase, int idx) __attribute__((always_inline)) {
+    Share* s = reinterpret_cast<Share*>(smem + Smem::share + phase * 32);
     const int tiles = phase ? tiles_b : tiles_a;
     // phase B, aligned: whole tiles, so that no tile is shared between CTAs
     const int per = phase && aligned ? A : 1;
     const unsigned total = (unsigned)(per > 1 ? tiles : tiles * A);
     const unsigned q = total / (unsigned)G, r = total - q * (unsigned)G;
-    s.u0 = (int)(q * idx + min((unsigned)idx, r)) * per;
-    s.n = idx < G ? (int)(q + (idx < (int)r)) * per : 0;
-    s.nc = ((phase ? I : H) + 255) >> 8;
-    return s;
+    const int n = idx < G ? (int)(q + (idx < (int)r)) * per : 0, nc = ((phase ? I : H) + 255) >> 8;
+    // the split of the last units with the least work for the busiest warp, as
+    // far as the partial sums fit (4 rows for each column tile)
+    const int whole = n - n % kWarps;
+    const int rest = n - whole, rows4 = phase && two_tiles ? 8 : 4;
+    int lgS = 0, best = rest ? 8 : 0;  // eighths of a unit
+    for (int l = 1; l <= 3; ++l) {
+      if ((1 << l) <= nc && (rest << l) * rows4 <= kParts) {
+        const int cost = (((rest << l) + kWarps - 1) / kWarps) << (3 - l);
+        if (cost < best) { best = cost; lgS = l; }
+      }
+    }
+    s->u0 = (int)(q * idx + min((unsigned)idx, r)) * per;
+    s->n = n;
+    s->nc = nc;
+    s->whole = whole;
+    s->lgS = lgS;
   };
 
-  // (group, output tile) of unit u, and of the one after it
+  // (group, output tile) of unit u
   auto unit_of = [&](int phase, int u, int& ai, int& tile) __attribute__((always_inline)) {
     const int d = phase ? A : tiles_a, q = u / d, r = u - q * d;
     ai = phase ? r : q;
     tile = phase ? q : r;
   };
-  auto next_unit = [&](int phase, int& ai, int& tile) __attribute__((always_inline)) {
-    if (phase) {
-      if (++ai == A) { ai = 0; ++tile; }
-    } else {
-      if (++tile == tiles_a) { tile = 0; ++ai; }
-    }
-  };
 
-  constexpr int kScChunk = F == Fmt::NF4 ? 16 : 8;                // scale bytes per row and chunk
-  const int kb_a = H / 2, kb_b = I / 2;                           // bytes of codes per row
-  const int sr_a = F == Fmt::NF4 ? H / 16 : H / 32;               // scale bytes per row
+  constexpr int kScChunk = F == Fmt::NF4 ? 16 : 8;       // scale bytes of a row and chunk
+  const int kb_a = H / 2, kb_b = I / 2;                  // bytes of codes per row
+  const int sr_a = F == Fmt::NF4 ? H / 16 : H / 32;      // scale bytes per row
   const int sr_b = F == Fmt::NF4 ? I / 16 : I / 32;
 
-  // cp.async: this lane copies 16-byte unit my_unit of rows my_row + 4 j
+  // cp.async: this lane copies 16-byte unit my_unit of rows my_row + 4 j, and
+  // of row sc_row's scales the first or second 16-byte unit that holds them
   const int my_row = lane >> 3, my_unit = lane & 7;
-  const int sc_row = lane >> 1, sc_half = lane & 1;  // and two scale words of row sc_row
+  const int sc_row = lane >> 1, sc_unit = lane & 1;
+  auto row_skip = [&](int phase, int r) __attribute__((always_inline)) { return phase == 0 && r >= 8 ? I - 8 : 0; };
 
-  // Points cur's lane pointers at its chunk.  Rows 8 .. 15 of a gate_up unit
-  // are the up rows, I - 8 further.
-  auto point = [&](Cursor& cur) __attribute__((always_inline)) {
-    const int e = active[cur.ai];
-    if (cur.phase) {
-      const int64_t row = (int64_t)e * H + cur.tile * 16;
-      cur.w = p.dn + (row + my_row) * kb_b + cur.c * CKB + my_unit * 16;
-      cur.sc = static_cast<const uint8_t*>(p.dn_scale) + (row + sc_row) * sr_b + cur.c * kScChunk +
-               sc_half * (kScChunk / 2);
-    } else {
-      const int64_t row = (int64_t)e * 2 * I + cur.tile * 8;
-      cur.w = p.gu + (row + my_row) * kb_a + cur.c * CKB + my_unit * 16;
-      cur.sc = static_cast<const uint8_t*>(p.gu_scale) +
-               (row + sc_row + (sc_row >= 8 ? I - 8 : 0)) * sr_a + cur.c * kScChunk +
-               sc_half * (kScChunk / 2);
+  // This lane's place in its warp's stream of chunks to load: item pc_item of
+  // phase pc_phase (-1: no more), its chunks [pc_c, pc_c1), the lane's first 16
+  // code bytes of the chunk, the chunk's first scale in row sc_row and the bytes
+  // from there to the end of the scales.
+  int pc_phase = 0, pc_item = 0, pc_c = 0, pc_c1 = 0, pc_have = 0;
+  const uint8_t *pc_w = nullptr, *pc_s = nullptr;
+  // Opens item pc_item.  Rows 8 .. 15 of a gate_up unit are the up rows, I - 8
+  // further.
+  auto enter = [&]() __attribute__((always_inline)) {
+    const Share& s = share(pc_phase);
+    int u, ai, tile;
+    if (!s.item(warp, pc_item, u, pc_c, pc_c1)) {
+      pc_item = -1;
+      return;
     }
+    unit_of(pc_phase, s.u0 + u, ai, tile);
+    const int e = active[ai];
+    const int kb = pc_phase ? kb_b : kb_a, sr = pc_phase ? sr_b : sr_a;
+    const int64_t row = pc_phase ? (int64_t)e * H + tile * 16 : (int64_t)e * 2 * I + tile * 8;
+    pc_w = (pc_phase ? p.dn : p.gu) + (row + my_row) * kb + pc_c * CKB + my_unit * 16;
+    const int64_t off = (row + sc_row + row_skip(pc_phase, sc_row)) * sr + pc_c * kScChunk;
+    pc_s = static_cast<const uint8_t*>(pc_phase ? p.dn_scale : p.gu_scale) + off;
+    const int64_t all = (pc_phase ? (int64_t)E * H : (int64_t)E * 2 * I) * sr;
+    pc_have = (int)min(all - off, (int64_t)1 << 30);
   };
 
   // this warp's ring, as shared addresses
@@ -406,81 +448,40 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
   const uint32_t ring_s = Smem::scales + warp * (D * kScStage);
   const uint32_t put_w0 = ring + my_row * CKB + (my_unit ^ swizzle<F>(my_row)) * 16;
   const uint32_t put_w1 = ring + (my_row + 4) * CKB + (my_unit ^ swizzle<F>(my_row + 4)) * 16;
-  const uint32_t put_s = ring_s + sc_row * 16 + sc_half * 8;
-  uint32_t sv0 = 0, sv1 = 0;  // scales loaded for the stage before
-  uint32_t sv_to = 0;         // their place, or 0: none pending
 
-  auto put_scales = [&]() __attribute__((always_inline)) {
-    if (sv_to == 0) return;
-    if (F == Fmt::NF4) {
-      sv0 = __float_as_uint(__uint_as_float(sv0) * (1.0f / kLevelScale));
-      sv1 = __float_as_uint(__uint_as_float(sv1) * (1.0f / kLevelScale));
-    } else {
-      // e8m0 byte s -> bf16 bits of 2^(s - 127): s << 7, but 0 and 255
-      const uint32_t v = prmt(sv0, sv1, 0x5410u);
-      sv0 = prmt(v, 0u, 0x4140u) << 7;
-      sv1 = prmt(v, 0u, 0x4342u) << 7;
-      const uint32_t zero = (v - 0x01010101u) & ~v, ones = (~v - 0x01010101u) & v;
-      if ((zero | ones) & 0x80808080u) {  // a byte of 0 or 255 among them
-        auto fix = [](uint32_t h) -> uint32_t { return h == 0u ? 0x40u : h == 0x7F80u ? 0x7FC0u : h; };
-        sv0 = fix(sv0 & 0xFFFFu) | (fix(sv0 >> 16) << 16);
-        sv1 = fix(sv1 & 0xFFFFu) | (fix(sv1 >> 16) << 16);
-      }
-    }
-    sts64(sv_to, sv0, sv1);
-    sv_to = 0;
-  };
-
-  // ---- the warp's stream of chunks: share A, then share B
-  Share sa = make_share(0, next_a), sb = make_share(1, next_b);
   uint32_t q_in = 0, q_out = 0;  // ring slots of the next chunk to load and to multiply
-  Cursor pc{};                   // next chunk to load, if pc.left > 0
-  auto enter = [&](const Share& s) __attribute__((always_inline)) {
-    const int f = s.begin(warp);
-    pc.phase = s.phase;
-    pc.left = s.begin(warp + 1) - f;
-    if (pc.left > 0) {
-      const int u = f / s.nc;
-      pc.c = f - u * s.nc;
-      unit_of(s.phase, s.u0 + u, pc.ai, pc.tile);
-      point(pc);
-    }
-  };
-  // Loads the next chunk into its ring slot; its scales reach shared memory
-  // with the call after this one, two calls before they are read.
+  // Loads the next chunk, codes and scales, into its ring slot.
   auto issue = [&]() __attribute__((always_inline)) {
-    put_scales();
-    if (pc.left == 0 && pc.phase == 0) enter(sb);
-    if (pc.left > 0) {
-      const int kb = pc.phase ? kb_b : kb_a;
-      const int bytes = kb - pc.c * CKB;  // of a row, from this chunk on
+    if (pc_item >= 0) {
+      const int kb = pc_phase ? kb_b : kb_a;
+      const int bytes = kb - pc_c * CKB;  // of a row, from this chunk on
       const uint32_t slot = q_in * kStage;
-      const uint8_t* up = pc.w + (int64_t)(pc.phase ? 8 : I) * kb;
+      const uint8_t* up = pc_w + (int64_t)(pc_phase ? 8 : I) * kb;
       if (my_unit * 16 < bytes) {
-        cp_async_16(put_w0 + slot, pc.w);
-        cp_async_16(put_w1 + slot, pc.w + 4 * kb);
+        cp_async_16(put_w0 + slot, pc_w);
+        cp_async_16(put_w1 + slot, pc_w + 4 * kb);
         cp_async_16(put_w0 + slot + 8 * CKB, up);
         cp_async_16(put_w1 + slot + 8 * CKB, up + 4 * kb);
       }
-      const int words = (bytes >> 5) - sc_half * 2;  // scale words left: one per 64 k
-      if (F == Fmt::NF4) {
-        if (words > 0) sv0 = __ldg(reinterpret_cast<const uint32_t*>(pc.sc));
-        if (words > 1) sv1 = __ldg(reinterpret_cast<const uint32_t*>(pc.sc) + 1);
-      } else {
-        if (words > 0) sv0 = __ldg(reinterpret_cast<const uint16_t*>(pc.sc));
-        if (words > 1) sv1 = __ldg(reinterpret_cast<const uint16_t*>(pc.sc) + 1);
-      }
-      sv_to = put_s + q_in * kScStage;
+      // the aligned units that the row's scales of this chunk lie in, as far as
+      // the array goes; past L1, whose few lines such small loads would fill
+      const int odd = (int)(reinterpret_cast<uintptr_t>(pc_s) & 15);
+      const int have = min(16, pc_have + odd - 16 * sc_unit);
+      if (have > 0 && odd + kScChunk > 16 * sc_unit)
+        cp_async_16_fill(ring_s + q_in * kScStage + lane * 16, pc_s - odd + 16 * sc_unit, (uint32_t)have);
+      pc_s += kScChunk;
+      pc_have -= kScChunk;
       q_in = (q_in + 1) & (D - 1);
-      --pc.left;
-      ++pc.c;
-      if (bytes > CKB) {
-        pc.w += CKB;
-        pc.sc += kScChunk;
-      } else {
-        pc.c = 0;
-        next_unit(pc.phase, pc.ai, pc.tile);
-        if (pc.left > 0) point(pc);
+      pc_w += CKB;
+      if (++pc_c == pc_c1) {
+        ++pc_item;
+#pragma unroll 1
+        for (;;) {
+          enter();
+          if (pc_item >= 0 || pc_phase) break;
+          pc_phase = 1;
+          pc_item = 0;
+        }
       }
     }
     cp_async_commit();
@@ -512,7 +513,37 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
   // differ in address bits 5 and 6 alone.
   const uint32_t get_w = ring + g * CKB + (F == Fmt::NF4 ? ((t4 >> 1) ^ swizzle<F>(g)) * 16 + (t4 & 1) * 8
                                                          : swizzle<F>(g) * 16 + t4 * 4);
-  const uint32_t get_s = ring_s + g * 16;
+  // Scales of rows g and g + 8: 32 bytes a row in a stage, the first at the low
+  // four bits of its address in the array.
+  const uint32_t get_s = ring_s + g * 32;
+  auto scale_at = [&](int phase, int ai, int tile, int r) __attribute__((always_inline)) -> uint32_t {
+    const int e = active[ai];
+    const unsigned row = phase ? (unsigned)e * H + tile * 16 + r
+                               : (unsigned)e * 2 * I + tile * 8 + r + row_skip(phase, r);
+    return row * (unsigned)(phase ? sr_b : sr_a);
+  };
+  // The scales of a chunk for this lane: NF4, the fp32 absmax of block b is read
+  // when it is needed; MXFP4, lane t4 of a row converts the two bytes of block
+  // t4, and the others get them by shuffle.
+  struct Scales {
+    const uint8_t *g, *h;   // NF4: rows g and g + 8
+    float g0, g1, h0, h1;   // MXFP4: block t4, its two halves
+  };
+  auto scales_of = [&](uint32_t slot, uint32_t og, uint32_t oh) __attribute__((always_inline)) -> Scales {
+    Scales v;
+    v.g = smem + get_s + slot * kScStage + (og & 15u);
+    v.h = smem + get_s + slot * kScStage + 8 * 32 + (oh & 15u);
+    if (F == Fmt::MXFP4) {
+      const uint32_t a0 = *reinterpret_cast<const uint16_t*>(v.g + 2 * t4);
+      const uint32_t a1 = *reinterpret_cast<const uint16_t*>(v.h + 2 * t4);
+      auto f = [&](uint32_t b) { return *reinterpret_cast<const float*>(smem + Smem::e8m0 + b * 4); };
+      v.g0 = f(a0 & 255u);
+      v.g1 = f(a0 >> 8);
+      v.h0 = f(a1 & 255u);
+      v.h1 = f(a1 >> 8);
+    }
+    return v;
+  };
   auto decode = [&](uint32_t st, int b, uint32_t (&fa)[8], uint32_t (&fb)[8]) __attribute__((always_inline)) {
     uint2 wa, wb;
     const uint8_t* at = smem + (st ^ (b * 32));
@@ -534,9 +565,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
       fb[i] = lds_table(prmt(i < 4 ? wb.x : wb.y, lut, sel));
     }
   };
-  // acc += block b (scale words sg, sh of rows g, g + 8) times the lane's x
+  // acc += block b times the lane's x
   auto mma_block = [&](float (&acc)[4], const uint32_t (&fa)[8], const uint32_t (&fb)[8],
-                       const uint4& x0, const uint4& x1, uint32_t sg, uint32_t sh) __attribute__((always_inline)) {
+                       const uint4& x0, const uint4& x1, const Scales& v, int b) __attribute__((always_inline)) {
     const uint32_t xb[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
     constexpr int kPer = F == Fmt::NF4 ? 4 : 2;  // mma of one scale block
 #pragma unroll
@@ -549,12 +580,19 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
         else
           mma16816(d, fa[2 * m], fb[2 * m], fa[2 * m + 1], fb[2 * m + 1], xb[2 * m], xb[2 * m + 1]);
       }
-      const uint32_t wg = F == Fmt::NF4 ? sg : m0 ? sg & 0xFFFF0000u : sg << 16;
-      const uint32_t wh = F == Fmt::NF4 ? sh : m0 ? sh & 0xFFFF0000u : sh << 16;
-      acc[0] = fmaf(d[0], __uint_as_float(wg), acc[0]);
-      acc[1] = fmaf(d[1], __uint_as_float(wg), acc[1]);
-      acc[2] = fmaf(d[2], __uint_as_float(wh), acc[2]);
-      acc[3] = fmaf(d[3], __uint_as_float(wh), acc[3]);
+      float fg, fh;
+      if (F == Fmt::NF4) {
+        fg = *reinterpret_cast<const float*>(v.g + 4 * b);
+        fh = *reinterpret_cast<const float*>(v.h + 4 * b);
+      } else {
+        const int from = (lane & 28) | b;
+        fg = __shfl_sync(0xffffffffu, m0 ? v.g1 : v.g0, from);
+        fh = __shfl_sync(0xffffffffu, m0 ? v.h1 : v.h0, from);
+      }
+      acc[0] = fmaf(d[0], fg, acc[0]);
+      acc[1] = fmaf(d[1], fg, acc[1]);
+      acc[2] = fmaf(d[2], fh, acc[2]);
+      acc[3] = fmaf(d[3], fh, acc[3]);
     }
   };
 
@@ -569,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
   // One column tile, the `nb` blocks of one chunk: x holds the columns of its
   // first two blocks; at the end those at nsrc, the next ones the warp needs.
   auto step_one = [&](uint4 (&x)[2][2], const uint16_t* src, int nb, const uint16_t* nsrc, int nnb,
-                      float (&acc)[4]) __attribute__((always_inline)) {
+                      uint32_t og, uint32_t oh, float (&acc)[4]) __attribute__((always_inline)) {
     issue();
     uint4 y[2][2];
     auto load_cols = [&](uint4 (&v)[2][2], const uint16_t* from, int n) __attribute__((always_inline)) {
@@ -579,33 +617,33 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
     load_cols(y, src + 128, nb - 2);
     const uint32_t slot = wait_stage();
     const uint32_t st = get_w + slot * kStage;
-    const uint4 s0 = *reinterpret_cast<const uint4*>(smem + get_s + slot * kScStage);
-    const uint4 s1 = *reinterpret_cast<const uint4*>(smem + get_s + slot * kScStage + 8 * 16);
-    auto block = [&](int b, const uint4 (&v)[2], uint32_t sg, uint32_t sh) __attribute__((always_inline)) {
+    const Scales sc = scales_of(slot, og, oh);
+    auto block = [&](int b, const uint4 (&v)[2]) __attribute__((always_inline)) {
       uint32_t fa[8], fb[8];
       decode(st, b, fa, fb);
-      mma_block(acc, fa, fb, v[0], v[1], sg, sh);
+      mma_block(acc, fa, fb, v[0], v[1], sc, b);
     };
     if (nb >= 4) {
-      block(0, x[0], s0.x, s1.x);
-      block(1, x[1], s0.y, s1.y);
+      block(0, x[0]);
+      block(1, x[1]);
       load_cols(x, nsrc, nnb);
-      block(2, y[0], s0.z, s1.z);
-      block(3, y[1], s0.w, s1.w);
+      block(2, y[0]);
+      block(3, y[1]);
     } else {
-      block(0, x[0], s0.x, s1.x);
-      if (nb > 1) block(1, x[1], s0.y, s1.y);
+      block(0, x[0]);
+      if (nb > 1) block(1, x[1]);
       load_cols(x, nsrc, nnb);
-      if (nb > 2) block(2, y[0], s0.z, s1.z);
+      if (nb > 2) block(2, y[0]);
     }
     __syncwarp();
   };
   // Phase B, two column tiles: the columns are loaded a block ahead.
-  auto step_two = [&](uint4 (&x)[2][2][2], const uint16_t* s0, const uint16_t* s1, int left,
-                      float (&acc)[2][4]) __attribute__((always_inline)) {
+  auto step_two = [&](uint4 (&x)[2][2][2], const uint16_t* s0, const uint16_t* s1, int left, uint32_t og,
+                      uint32_t oh, float (&acc)[2][4]) __attribute__((always_inline)) {
     issue();
     const uint32_t slot = wait_stage();
     const uint32_t st = get_w + slot * kStage;
+    const Scales sc = scales_of(slot, og, oh);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       if (b < left) {
@@ -613,17 +651,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
           load_x(s0 + b * 64 + 64, x[(b + 1) & 1][0][0], x[(b + 1) & 1][0][1]);
           load_x(s1 + b * 64 + 64, x[(b + 1) & 1][1][0], x[(b + 1) & 1][1][1]);
         }
-        const uint32_t sg = *reinterpret_cast<const uint32_t*>(smem + get_s + slot * kScStage + b * 4);
-        const uint32_t sh = *reinterpret_cast<const uint32_t*>(smem + get_s + slot * kScStage + 128 + b * 4);
         uint32_t fa[8], fb[8];
         decode(st, b, fa, fb);
-        mma_block(acc[0], fa, fb, x[b & 1][0][0], x[b & 1][0][1], sg, sh);
-        mma_block(acc[1], fa, fb, x[b & 1][1][0], x[b & 1][1][1], sg, sh);
+        mma_block(acc[0], fa, fb, x[b & 1][0][0], x[b & 1][0][1], sc, b);
+        mma_block(acc[1], fa, fb, x[b & 1][1][0], x[b & 1][1][1], sc, b);
       }
     }
     __syncwarp();
   };
 
+  constexpr float kUnscale = F == Fmt::NF4 ? 1.0f / kLevelScale : 1.0f;
   // Writes one column tile of a finished unit: h (phase A) or y (phase B).
   auto finish = [&](int phase, const float (&d)[4], int cnt, int r0, int tile, int nt) __attribute__((always_inline)) {
     if (phase == 0) {
@@ -632,7 +669,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
         const int c = nt * 8 + 2 * t4 + j;
         if (c < cnt) {
           const int slot = rows[r0 + c];
-          const float h = __fdiv_rn(d[j], 1.0f + expf(-d[j])) * d[2 + j];
+          const float gate = d[j] * kUnscale, up = d[2 + j] * kUnscale;
+          const float h = __fdividef(gate, 1.0f + __expf(-gate)) * up;
           const __nv_bfloat16 hi = __float2bfloat16_rn(h);
           // an infinite high part keeps a zero low part (inf - inf is NaN)
           const float low = h - __bfloat162float(hi);
@@ -651,52 +689,52 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
         const int c = nt * 4 + 2 * t4 + j;
         if (t4 < 2 && c < cnt) {
           float* y = a.y + (int64_t)rows[r0 + c] * H + tile * 16 + g;
-          y[0] = v[j];
-          y[8] = v[2 + j];
+          y[0] = v[j] * kUnscale;
+          y[8] = v[2 + j] * kUnscale;
         }
       }
     }
   };
 
   float* parts = reinterpret_cast<float*>(smem + Smem::table + 128);  // row i at i * 64
-  // A share: this warp's range of chunks, then the units that several warps
-  // shared, joined in order.
-  auto run_share = [&](const Share& s) __attribute__((always_inline)) {
-    const int nc = s.nc, K = s.phase ? I : H, nbk = K >> 6;  // blocks of a unit
-    const bool wide = s.phase && two_tiles;
-    const int rows4 = wide ? 8 : 4;                          // part rows of a piece
-    int f = s.begin(warp);
-    const int f1 = s.begin(warp + 1);
-    if (f < f1) {
-      const int u0 = f / nc;
-      int u = u0, c = f - u0 * nc, ai, tile;
-      unit_of(s.phase, s.u0 + u, ai, tile);
-      int r0 = first[ai], cnt = first[ai + 1] - r0;
-      const uint16_t* src = column(s.phase, r0, cnt, 0) + c * 256;
+  // A phase's share: this warp's items, then the units cut into parts, joined.
+  auto run_share = [&](int phase) __attribute__((always_inline)) {
+    const Share& s = share(phase);
+    const int nbk = (phase ? I : H) >> 6;  // blocks of a unit
+    const bool wide = phase && two_tiles;
+    const int rows4 = wide ? 8 : 4;        // part rows of an item
+    int item = 0, u, c, c1;
+    if (s.item(warp, 0, u, c, c1)) {
       uint4 x[2][2];
-      if (!wide) {
-        load_x(src, x[0][0], x[0][1]);
-        if (nbk - c * 4 > 1) load_x(src + 64, x[1][0], x[1][1]);
-      }
+      const uint16_t* src = nullptr;
 #pragma unroll 1
       for (;;) {
-        // the piece: chunks [c, c1) of unit u; then the next unit's first
-        const int c1 = min(nc, c + f1 - f);
-        const bool more = f + (c1 - c) < f1;
-        int nai = ai, ntile = tile;
-        if (more) next_unit(s.phase, nai, ntile);
-        const int nr0 = first[nai], ncnt = first[nai + 1] - nr0;
-        const uint16_t* nsrc = column(s.phase, nr0, ncnt, 0);
+        int ai, tile;
+        unit_of(phase, s.u0 + u, ai, tile);
+        const int r0 = first[ai], cnt = first[ai + 1] - r0;
+        const uint32_t og = scale_at(phase, ai, tile, g), oh = scale_at(phase, ai, tile, g + 8);
+        // the columns of the item after this one, to be loaded with its last chunk
+        int nu, nc0, nc1, nai, ntile;
+        const bool more = s.item(warp, item + 1, nu, nc0, nc1);
+        unit_of(phase, s.u0 + (more ? nu : u), nai, ntile);
+        const uint16_t* nsrc = column(phase, first[nai], first[nai + 1] - first[nai], 0) + nc0 * 256;
+        const int nnb = more ? nbk - nc0 * 4 : 0;
+        if (item == 0) {
+          src = column(phase, r0, cnt, 0) + c * 256;
+          if (!wide) {
+            load_x(src, x[0][0], x[0][1]);
+            if (nbk - c * 4 > 1) load_x(src + 64, x[1][0], x[1][1]);
+          }
+        }
         float acc[2][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[0][j] = acc[1][j] = 0.0f;
-        const bool whole = c == 0 && c1 == nc;
-        f += c1 - c;
         if (!wide) {
 #pragma unroll 1
           for (; c < c1; ++c, src += 256) {
             const bool last = c + 1 == c1;
-            step_one(x, src, nbk - c * 4, last ? nsrc : src + 256, last ? nbk : nbk - c * 4 - 4, acc[0]);
+            step_one(x, src, nbk - c * 4, last ? nsrc : src + 256, last ? nnb : nbk - c * 4 - 4,
+                     og + c * kScChunk, oh + c * kScChunk, acc[0]);
           }
         } else {
           const uint16_t* src1 = column(1, r0, cnt, cnt > 4 ? 1 : 0) + c * 256;
@@ -705,14 +743,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
           load_x(src1, y[0][1][0], y[0][1][1]);
 #pragma unroll 1
           for (; c < c1; ++c, src += 256, src1 += 256)
-            step_two(y, src, src1, c + 1 < c1 ? nbk - c * 4 : min(4, nbk - c * 4), acc);
+            step_two(y, src, src1, c + 1 < c1 ? nbk - c * 4 : min(4, nbk - c * 4),
+                     og + c * kScChunk, oh + c * kScChunk, acc);
         }
-        if (whole) {
-          finish(s.phase, acc[0], cnt, r0, tile, 0);
+        if (u < s.whole || s.lgS == 0) {
+          finish(phase, acc[0], cnt, r0, tile, 0);
           if (wide && cnt > 4) finish(1, acc[1], cnt, r0, tile, 1);
         } else {
-          // a warp's first piece in its first slot, its last in the second
-          float* to = parts + ((warp * 2 + (u != u0)) * rows4) * 64 + lane;
+          // the part's place among the parts of the split units
+          float* to = parts + (warp + item * kWarps - s.whole) * rows4 * 64 + lane;
 #pragma unroll
           for (int j = 0; j < 4; ++j) to[j * 64] = acc[0][j];
           if (wide)
@@ -720,34 +759,29 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
             for (int j = 0; j < 4; ++j) to[(4 + j) * 64] = acc[1][j];
         }
         if (!more) break;
-        ++u;
-        ai = nai;
-        tile = ntile;
-        r0 = nr0;
-        cnt = ncnt;
+        ++item;
+        u = nu;
+        c = nc0;
+        c1 = nc1;
         src = nsrc;
-        c = 0;
       }
     }
-    __syncthreads();
-    // units cut by a warp's border: warp w joins the one that begins in its
-    // range and goes on behind it
-    const int e = s.begin(warp + 1);
-    if (s.begin(warp) < e && e % nc) {
-      const int u = e / nc;
-      if (u * nc >= s.begin(warp)) {
+    if (s.lgS) {
+      __syncthreads();
+      const int uj = s.whole + warp;  // fewer than kWarps units are split
+      if (uj < s.n) {
         int ai, tile;
-        unit_of(s.phase, s.u0 + u, ai, tile);
+        unit_of(phase, s.u0 + uj, ai, tile);
         const int r0 = first[ai], cnt = first[ai + 1] - r0;
-        for (int i = 0; i < (wide && cnt > 4 ? 2 : 1); ++i) {
+        const float* from = parts + (warp << s.lgS) * rows4 * 64 + lane;
+#pragma unroll 1
+        for (int i = 0; i < (wide && cnt > 4 ? 2 : 1); ++i, from += 4 * 64) {
           float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          for (int w = warp; w < kWarps && s.begin(w) < (u + 1) * nc; ++w) {
-            if (s.begin(w) == s.begin(w + 1)) continue;
-            const float* from = parts + ((w * 2 + (s.begin(w) / nc != u)) * rows4 + i * 4) * 64 + lane;
+#pragma unroll 2
+          for (int sp = 0; sp < (1 << s.lgS); ++sp)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) d[j] += from[j * 64];
-          }
-          finish(s.phase, d, cnt, r0, tile, i);
+            for (int j = 0; j < 4; ++j) d[j] += from[(sp * rows4 + j) * 64];
+          finish(phase, d, cnt, r0, tile, i);
         }
       }
     }
@@ -781,12 +815,22 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
     }
   };
 
+  if (threadIdx.x < 2) set_share(threadIdx.x, threadIdx.x ? next_b : next_a);
+  __syncthreads();
   bool in_a = next_a < G, fresh = true, waited = in_a;
 #pragma unroll 1
   for (;;) {
     if (fresh) {
       fresh = false;
-      enter(sa);
+      pc_phase = 0;
+      pc_item = 0;
+#pragma unroll 1
+      for (;;) {
+        enter();
+        if (pc_item >= 0 || pc_phase) break;
+        pc_phase = 1;
+        pc_item = 0;
+      }
 #pragma unroll 1
       for (int i = 0; i < D - 1; ++i) issue();
     }
@@ -795,24 +839,23 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
       wait_a();
     }
     if (!in_a && (next_b >= G || misc[3])) break;
-    const Share cur = in_a ? sa : sb;
-    run_share(cur);
+    run_share(in_a ? 0 : 1);
     if (threadIdx.x == 0) misc[2] = atomicAdd(&a.counters[in_a ? 0 : 1], 1);
     if (in_a || !aligned) __threadfence();
     __syncthreads();
     const int next = misc[2];
     if (in_a) {
       if (threadIdx.x == 0) atomicAdd(&a.counters[2], 1);
-    } else if (cur.n > 0) {
+    } else if (share(1).n > 0) {
       // tiles that this share touches: an aligned share holds all of a tile's
       // experts; else the CTA that brings the tile's count to A combines it
-      const int last_tile = (cur.u0 + cur.n - 1) / A;
-      for (int tile = cur.u0 / A; tile <= last_tile; ++tile) {
+      const int ub = share(1).u0, ue = ub + share(1).n, last_tile = (ue - 1) / A;
+      for (int tile = ub / A; tile <= last_tile; ++tile) {
         if (aligned) {
           combine(tile);
         } else {
           if (threadIdx.x == 0) {
-            const int mine = min(cur.u0 + cur.n, (tile + 1) * A) - max(cur.u0, tile * A);
+            const int mine = min(ue, (tile + 1) * A) - max(ub, tile * A);
             misc[5] = atomicAdd(&a.counters[kCounters + tile], mine) + mine == A;
             __threadfence();
           }
@@ -827,13 +870,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
       // drop what is in flight and start the stream again
       cp_async_wait_group<0>();
       __syncthreads();  // before misc[2], the rings and the part rows are written again
-      if (in_a) {
-        sa = make_share(0, next);
-      } else {
-        sa.n = 0;  // (enter: no chunks of share A)
-        sb = make_share(1, next);
+      if (threadIdx.x == 0) {
+        if (!in_a) set_share(0, G);
+        set_share(in_a ? 0 : 1, next);
       }
-      q_in = q_out = sv_to = 0;
+      __syncthreads();
+      q_in = q_out = 0;
       fresh = true;
     } else if (in_a) {
       in_a = waited = false;
@@ -864,7 +906,7 @@ Layout layout_of(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I) {
 template <Fmt F, int NPL>
 cudaError_t launch_t(const LayerArgs& a, int num_sms, cudaStream_t s) {
   constexpr auto k = moe_experts<F, NPL>;
-  cudaError_t e = opt_in_smem<k>(Smem::end);
+  cudaError_t e = opt_in_smem<k>(Smem::bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.p.E, (unsigned)((a.p.T + kRouterTokens - 1) / kRouterTokens));
@@ -881,7 +923,7 @@ cudaError_t launch_t(const LayerArgs& a, int num_sms, cudaStream_t s) {
   const int64_t whole = (tiles + num_sms - 1) / num_sms * A;
   const int64_t even = (tiles * A + num_sms - 1) / num_sms;
   const int aligned = (whole - even) * ((a.p.I + 255) / 256) <= kAlignChunks;
-  return launch_kernel<k>(num_sms, kThreads, Smem::end, s, true, a, aligned);
+  return launch_kernel<k>(num_sms, kThreads, Smem::bytes, s, true, a, aligned);
 }
 
 template <Fmt F>

@@ -302,7 +302,8 @@ GBW_API gbw_status gmoe_combine_bwd(const uint16_t* dout, const uint16_t* y, int
  * slot of weight 0 adds nothing, whatever its expert gives.
  * Requires T <= 32 (larger batches: gmoe_route, gnf4_grouped_expert_mlp,
  * gmoe_combine), 1 <= E <= 1024, 1 <= k <= min(E, 16), H % 64 == 0,
- * I % 64 == 0, 16-byte aligned x, router_w, packed weights and out.  T == 0 is
+ * I % 64 == 0, H * I <= 2^33, 16-byte aligned x, router_w, packed weights,
+ * scales and out.  T == 0 is
  * a no-op. */
 GBW_API gbw_status gnf4_moe_layer(const uint16_t* x, int64_t T, int64_t H,
                                   const uint16_t* router_w, const float* router_bias,
@@ -312,7 +313,7 @@ GBW_API gbw_status gnf4_moe_layer(const uint16_t* x, int64_t T, int64_t H,
                                   void* workspace, int64_t workspace_bytes, void* stream);
 
 /* The same with MXFP4 experts (blocks [E, 2I, H/32, 16] + scales [E, 2I, H/32],
- * blocks [E, H, I/32, 16] + scales [E, H, I/32], e8m0, 2-byte aligned). */
+ * blocks [E, H, I/32, 16] + scales [E, H, I/32], e8m0). */
 GBW_API gbw_status gmxfp4_moe_layer(const uint16_t* x, int64_t T, int64_t H,
                                     const uint16_t* router_w, const float* router_bias,
                                     const uint8_t* gu_blocks, const uint8_t* gu_scales,
