@@ -38,6 +38,11 @@
 #include "route.cuh"
 
 namespace gbw {
+
+cudaError_t make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base,
+                        uint64_t d0, uint64_t d1, uint64_t pitch, uint32_t b0,
+                        uint32_t b1, CUtensorMapSwizzle sw);
+
 namespace {
 
 constexpr int kWarps = 12;  // 168 registers a thread: nothing spills
@@ -68,7 +73,8 @@ struct Smem {
   static constexpr int misc = active + 2 * kMaxP;  // 16 ints
   static constexpr int share = misc + 64;          // [2] Share, 32 bytes apart
   static constexpr int part = share + 64;          // [kWarps] scan parts
-  static constexpr int low_end = part + 4 * kWarps;
+  static constexpr int bars = part + 4 * kWarps;   // [kWarps][D] stage full
+  static constexpr int low_end = bars + 8 * kWarps * D;
   static constexpr int table = 65536;
   static constexpr int ring_low = table - kLowWarps * D * kStage;
   static constexpr int count = ring_low;  // [kMaxE] int: token bits, then first row (before the ring is used)
@@ -214,12 +220,14 @@ __device__ __forceinline__ int ld_acquire(const int* p) {
   return v;
 }
 
-// 16-byte unit u of row r of a stage is stored at u ^ swizzle(r): the rows'
-// lanes then read different banks (NF4: 8 bytes a lane, 4 rows a wavefront;
-// MXFP4: 4 bytes a lane, 8 rows).
-template <Fmt F>
-__device__ __forceinline__ uint32_t swizzle(int r) {
-  return F == Fmt::NF4 ? 2u * (r & 3) : (uint32_t)(r & 7);
+// 8 rows x 128 bytes of a packed matrix to shared address dst, 128B swizzle
+// (16-byte unit u of row r at u ^ r), counted in bytes on barrier `bar`.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
 }
 
 // One phase's share of this CTA, kept in shared memory: units [u0, u0 + n) of
@@ -243,7 +251,9 @@ struct Share {
 };
 
 template <Fmt F, int NPL>
-__global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, const int aligned) {
+__global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, const int aligned,
+                                                            const __grid_constant__ CUtensorMap map_gu,
+                                                            const __grid_constant__ CUtensorMap map_dn) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const LayerProblem& p = a.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -283,7 +293,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
         sts32(Smem::e8m0 + 4 * i, i == 0 ? 0x00400000u : i == 255 ? 0x7FC00000u : (uint32_t)i << 23);
   }
   for (int e = threadIdx.x; e < E; e += kThreads) count[e] = 0;
-  if (threadIdx.x == 0) misc[3] = misc[6] = 0;
+  if (threadIdx.x == 0) {
+    misc[3] = misc[6] = 0;
+    tma_prefetch_desc(&map_gu);
+    tma_prefetch_desc(&map_dn);
+  }
+  // a stage is full when its codes have landed and every lane's scales have
+  if (threadIdx.x < kWarps * D) {
+    mbar_init(reinterpret_cast<uint64_t*>(smem + Smem::bars) + threadIdx.x, 33);
+    fence_barrier_init();
+  }
   __syncthreads();
   grid_dependency_wait();
   if (threadIdx.x >= kThreads - 2) {  // (a warp without a token, usually)
@@ -406,22 +425,20 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
   };
 
   constexpr int kScChunk = F == Fmt::NF4 ? 16 : 8;       // scale bytes of a row and chunk
-  const int kb_a = H / 2, kb_b = I / 2;                  // bytes of codes per row
   const int sr_a = F == Fmt::NF4 ? H / 16 : H / 32;      // scale bytes per row
   const int sr_b = F == Fmt::NF4 ? I / 16 : I / 32;
 
-  // cp.async: this lane copies 16-byte unit my_unit of rows my_row + 4 j, and
-  // of row sc_row's scales the first or second 16-byte unit that holds them
-  const int my_row = lane >> 3, my_unit = lane & 7;
+  // of row sc_row's scales this lane copies the first or second 16-byte unit
+  // that holds them
   const int sc_row = lane >> 1, sc_unit = lane & 1;
   auto row_skip = [&](int phase, int r) __attribute__((always_inline)) { return phase == 0 && r >= 8 ? I - 8 : 0; };
 
-  // This lane's place in its warp's stream of chunks to load: item pc_item of
-  // phase pc_phase (-1: no more), its chunks [pc_c, pc_c1), the lane's first 16
-  // code bytes of the chunk, the chunk's first scale in row sc_row and the bytes
-  // from there to the end of the scales.
-  int pc_phase = 0, pc_item = 0, pc_c = 0, pc_c1 = 0, pc_have = 0;
-  const uint8_t *pc_w = nullptr, *pc_s = nullptr;
+  // This warp's place in its stream of chunks to load: item pc_item of phase
+  // pc_phase (-1: no more), its chunks [pc_c, pc_c1), its first matrix row; for
+  // this lane, the chunk's first scale in row sc_row and the bytes from there to
+  // the end of the scales.
+  int pc_phase = 0, pc_item = 0, pc_c = 0, pc_c1 = 0, pc_row = 0, pc_have = 0;
+  const uint8_t* pc_s = nullptr;
   // Opens item pc_item.  Rows 8 .. 15 of a gate_up unit are the up rows, I - 8
   // further.
   auto enter = [&]() __attribute__((always_inline)) {
@@ -433,46 +450,42 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
     }
     unit_of(pc_phase, s.u0 + u, ai, tile);
     const int e = active[ai];
-    const int kb = pc_phase ? kb_b : kb_a, sr = pc_phase ? sr_b : sr_a;
-    const int64_t row = pc_phase ? (int64_t)e * H + tile * 16 : (int64_t)e * 2 * I + tile * 8;
-    pc_w = (pc_phase ? p.dn : p.gu) + (row + my_row) * kb + pc_c * CKB + my_unit * 16;
-    const int64_t off = (row + sc_row + row_skip(pc_phase, sc_row)) * sr + pc_c * kScChunk;
+    pc_row = pc_phase ? e * H + tile * 16 : e * 2 * I + tile * 8;
+    const int64_t sr = pc_phase ? sr_b : sr_a;
+    const int64_t off = (pc_row + sc_row + row_skip(pc_phase, sc_row)) * sr + pc_c * kScChunk;
     pc_s = static_cast<const uint8_t*>(pc_phase ? p.dn_scale : p.gu_scale) + off;
     const int64_t all = (pc_phase ? (int64_t)E * H : (int64_t)E * 2 * I) * sr;
     pc_have = (int)min(all - off, (int64_t)1 << 30);
   };
 
-  // this warp's ring, as shared addresses
+  // this warp's ring and its barriers, as shared addresses
   const uint32_t ring = warp < kLowWarps ? Smem::ring_low + warp * (D * kStage)
                                          : Smem::ring_high + (warp - kLowWarps) * (D * kStage);
   const uint32_t ring_s = Smem::scales + warp * (D * kScStage);
-  const uint32_t put_w0 = ring + my_row * CKB + (my_unit ^ swizzle<F>(my_row)) * 16;
-  const uint32_t put_w1 = ring + (my_row + 4) * CKB + (my_unit ^ swizzle<F>(my_row + 4)) * 16;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Smem::bars) + warp * D;
 
-  uint32_t q_in = 0, q_out = 0;  // ring slots of the next chunk to load and to multiply
+  uint32_t q_in = 0, q_out = 0;  // chunks loaded and multiplied so far
   // Loads the next chunk, codes and scales, into its ring slot.
   auto issue = [&]() __attribute__((always_inline)) {
     if (pc_item >= 0) {
-      const int kb = pc_phase ? kb_b : kb_a;
-      const int bytes = kb - pc_c * CKB;  // of a row, from this chunk on
-      const uint32_t slot = q_in * kStage;
-      const uint8_t* up = pc_w + (int64_t)(pc_phase ? 8 : I) * kb;
-      if (my_unit * 16 < bytes) {
-        cp_async_16(put_w0 + slot, pc_w);
-        cp_async_16(put_w1 + slot, pc_w + 4 * kb);
-        cp_async_16(put_w0 + slot + 8 * CKB, up);
-        cp_async_16(put_w1 + slot + 8 * CKB, up + 4 * kb);
+      const uint32_t slot = q_in & (D - 1);
+      if (lane == 0) {
+        const CUtensorMap* m = pc_phase ? &map_dn : &map_gu;
+        const uint32_t dst = ring + slot * kStage, bar = Smem::bars + (warp * D + slot) * 8;
+        mbar_arrive_expect_tx(&full[slot], kStage);
+        tma_box(dst, m, pc_c * CKB, pc_row, bar);
+        tma_box(dst + kStage / 2, m, pc_c * CKB, pc_row + (pc_phase ? 8 : I), bar);
       }
       // the aligned units that the row's scales of this chunk lie in, as far as
       // the array goes; past L1, whose few lines such small loads would fill
       const int odd = (int)(reinterpret_cast<uintptr_t>(pc_s) & 15);
       const int have = min(16, pc_have + odd - 16 * sc_unit);
       if (have > 0 && odd + kScChunk > 16 * sc_unit)
-        cp_async_16_fill(ring_s + q_in * kScStage + lane * 16, pc_s - odd + 16 * sc_unit, (uint32_t)have);
+        cp_async_16_fill(ring_s + slot * kScStage + lane * 16, pc_s - odd + 16 * sc_unit, (uint32_t)have);
+      cp_async_arrive_noinc(&full[slot]);
       pc_s += kScChunk;
       pc_have -= kScChunk;
-      q_in = (q_in + 1) & (D - 1);
-      pc_w += CKB;
+      ++q_in;
       if (++pc_c == pc_c1) {
         ++pc_item;
 #pragma unroll 1
@@ -484,7 +497,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
         }
       }
     }
-    cp_async_commit();
   };
 
   const int g = lane >> 2, t4 = lane & 3;
@@ -506,16 +518,18 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
     x0 = *reinterpret_cast<const uint4*>(xp);
     x1 = *reinterpret_cast<const uint4*>(xp + kSecond);
   };
-  // Weight fragments of block b of a stage: the lane's 16 weights of rows g and
-  // g + 8 (same swizzle).  NF4, one scale block: bytes 8 t4 .. of its 32;
-  // MXFP4, two blocks of 16 bytes: 4 bytes of each, so that every mma stays
-  // inside a scale block.  `st` is this lane's address in block 0; the blocks
-  // differ in address bits 5 and 6 alone.
-  const uint32_t get_w = ring + g * CKB + (F == Fmt::NF4 ? ((t4 >> 1) ^ swizzle<F>(g)) * 16 + (t4 & 1) * 8
-                                                         : swizzle<F>(g) * 16 + t4 * 4);
-  // Scales of rows g and g + 8: 32 bytes a row in a stage, the first at the low
+  // Weight fragments of block b of a stage: the lane's 16 weights of rows pg and
+  // pg + 8.  NF4, one scale block: bytes 8 t4 .. of its 32; MXFP4, two blocks of
+  // 16 bytes: 4 bytes of each, so that every mma stays inside a scale block.
+  // `st` is this lane's address in block 0; the blocks differ in address bits 5
+  // and 6 alone.  The mma's row g is row pg of the eight: with that order the
+  // swizzle spreads every access over all banks.
+  const int pg = F == Fmt::NF4 ? (g & 3) * 2 + (g >> 2) : g;
+  const uint32_t get_w = ring + pg * CKB + (F == Fmt::NF4 ? ((t4 >> 1) ^ pg) * 16 + (t4 & 1) * 8
+                                                          : pg * 16 + t4 * 4);
+  // Scales of rows pg and pg + 8: 32 bytes a row in a stage, the first at the low
   // four bits of its address in the array.
-  const uint32_t get_s = ring_s + g * 32;
+  const uint32_t get_s = ring_s + pg * 32;
   auto scale_at = [&](int phase, int ai, int tile, int r) __attribute__((always_inline)) -> uint32_t {
     const int e = active[ai];
     const unsigned row = phase ? (unsigned)e * H + tile * 16 + r
@@ -526,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
   // when it is needed; MXFP4, lane t4 of a row converts the two bytes of block
   // t4, and the others get them by shuffle.
   struct Scales {
-    const uint8_t *g, *h;   // NF4: rows g and g + 8
+    const uint8_t *g, *h;   // NF4: rows pg and pg + 8
     float g0, g1, h0, h1;   // MXFP4: block t4, its two halves
   };
   auto scales_of = [&](uint32_t slot, uint32_t og, uint32_t oh) __attribute__((always_inline)) -> Scales {
@@ -596,13 +610,18 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
     }
   };
 
-  // Waits for the chunk to multiply; its stage's offset in the ring.
+  // Waits for the chunk to multiply; its ring slot.
   auto wait_stage = [&]() __attribute__((always_inline)) -> uint32_t {
-    cp_async_wait_group<D - 1>();
-    __syncwarp();
-    const uint32_t slot = q_out;
-    q_out = (q_out + 1) & (D - 1);
+    const uint32_t slot = q_out & (D - 1);
+    mbar_wait(&full[slot], (q_out / D) & 1u, &misc[3], p.err);
+    ++q_out;
     return slot;
+  };
+  // Before a stage may be loaded again: what was read of it has been used (the
+  // sums wait for it), by every lane.
+  auto release = [&](float (&acc)[4]) __attribute__((always_inline)) {
+    asm volatile("" : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3]) : : "memory");
+    __syncwarp();
   };
   // One column tile, the `nb` blocks of one chunk: x holds the columns of its
   // first two blocks; at the end those at nsrc, the next ones the warp needs.
@@ -635,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
       load_cols(x, nsrc, nnb);
       if (nb > 2) block(2, y[0]);
     }
-    __syncwarp();
+    release(acc);
   };
   // Phase B, two column tiles: the columns are loaded a block ahead.
   auto step_two = [&](uint4 (&x)[2][2][2], const uint16_t* s0, const uint16_t* s1, int left, uint32_t og,
@@ -657,7 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
         mma_block(acc[1], fa, fb, x[b & 1][1][0], x[b & 1][1][1], sc, b);
       }
     }
-    __syncwarp();
+    release(acc[0]);
+    release(acc[1]);
   };
 
   constexpr float kUnscale = F == Fmt::NF4 ? 1.0f / kLevelScale : 1.0f;
@@ -675,8 +695,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
           // an infinite high part keeps a zero low part (inf - inf is NaN)
           const float low = h - __bfloat162float(hi);
           const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(low) ? low : 0.0f);
-          a.hhi[(int64_t)slot * I + tile * 8 + g] = __bfloat16_as_ushort(hi);
-          a.hlo[(int64_t)slot * I + tile * 8 + g] = __bfloat16_as_ushort(lo);
+          a.hhi[(int64_t)slot * I + tile * 8 + pg] = __bfloat16_as_ushort(hi);
+          a.hlo[(int64_t)slot * I + tile * 8 + pg] = __bfloat16_as_ushort(lo);
         }
       }
     } else {
@@ -688,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
       for (int j = 0; j < 2; ++j) {
         const int c = nt * 4 + 2 * t4 + j;
         if (t4 < 2 && c < cnt) {
-          float* y = a.y + (int64_t)rows[r0 + c] * H + tile * 16 + g;
+          float* y = a.y + (int64_t)rows[r0 + c] * H + tile * 16 + pg;
           y[0] = v[j] * kUnscale;
           y[8] = v[2 + j] * kUnscale;
         }
@@ -712,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
         int ai, tile;
         unit_of(phase, s.u0 + u, ai, tile);
         const int r0 = first[ai], cnt = first[ai + 1] - r0;
-        const uint32_t og = scale_at(phase, ai, tile, g), oh = scale_at(phase, ai, tile, g + 8);
+        const uint32_t og = scale_at(phase, ai, tile, pg), oh = scale_at(phase, ai, tile, pg + 8);
         // the columns of the item after this one, to be loaded with its last chunk
         int nu, nc0, nc1, nai, ntile;
         const bool more = s.item(warp, item + 1, nu, nc0, nc1);
@@ -787,6 +807,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
     }
   };
 
+  // Lets the loads in flight land and drops them.
+  auto drain = [&]() __attribute__((always_inline)) {
+    for (; q_out != q_in; ++q_out) mbar_drain(&full[q_out & (D - 1)], (q_out / D) & 1u);
+  };
   // Waits until every share of phase A is done.
   auto wait_a = [&]() __attribute__((always_inline)) {
     if (threadIdx.x == 0) {
@@ -868,14 +892,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
     if (next < G) {
       // another share of this phase is unclaimed (some CTAs have not started):
       // drop what is in flight and start the stream again
-      cp_async_wait_group<0>();
+      drain();
       __syncthreads();  // before misc[2], the rings and the part rows are written again
       if (threadIdx.x == 0) {
         if (!in_a) set_share(0, G);
         set_share(in_a ? 0 : 1, next);
       }
       __syncthreads();
-      q_in = q_out = 0;
       fresh = true;
     } else if (in_a) {
       in_a = waited = false;
@@ -883,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
       break;
     }
   }
-  cp_async_wait_group<0>();
+  drain();
 }
 
 struct Layout {
@@ -923,7 +946,16 @@ cudaError_t launch_t(const LayerArgs& a, int num_sms, cudaStream_t s) {
   const int64_t whole = (tiles + num_sms - 1) / num_sms * A;
   const int64_t even = (tiles * A + num_sms - 1) / num_sms;
   const int aligned = (whole - even) * ((a.p.I + 255) / 256) <= kAlignChunks;
-  return launch_kernel<k>(num_sms, kThreads, Smem::bytes, s, true, a, aligned);
+  CUtensorMap gu, dn;  // packed matrices, boxes of 8 rows x 128 bytes
+  e = make_map_2d(&gu, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.p.gu, (uint64_t)a.p.H / 2,
+                  (uint64_t)a.p.E * 2 * (uint64_t)a.p.I, (uint64_t)a.p.H / 2, CKB, 8,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  e = make_map_2d(&dn, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.p.dn, (uint64_t)a.p.I / 2,
+                  (uint64_t)a.p.E * (uint64_t)a.p.H, (uint64_t)a.p.I / 2, CKB, 8,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  return launch_kernel<k>(num_sms, kThreads, Smem::bytes, s, true, a, aligned, gu, dn);
 }
 
 template <Fmt F>
