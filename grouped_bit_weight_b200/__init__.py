@@ -636,8 +636,9 @@ def gmxfp4_moe_layer(x, router_w, gu_blocks, gu_scales, dn_blocks, dn_scales, k,
 
 
 def gmxfp4_quantize_rows(x, row_to_token=None, swiglu=False):
-    """(codes [P, K/32, 16] uint8, scales [P, K/32] uint8 e8m0): bf16 rows in
-    MXFP4, gathered through row_to_token [P] int32 when given.  x [T, K]; with
+    """(codes [P, K/32, 16] uint8, scales [ceil(K/128), P, 4] uint8 e8m0): bf16
+    rows in MXFP4, gathered through row_to_token [P] int32 when given; byte b of
+    scales[a, p] belongs to block 4 a + b of row p (127 past the last).  x [T, K]; with
     swiglu x is a gate_up output [T, 2K] and silu(gate) * up is packed."""
     where = "gmxfp4_quantize_rows"
     _need(x, "x", torch.bfloat16)
@@ -658,7 +659,7 @@ def gmxfp4_quantize_rows(x, row_to_token=None, swiglu=False):
             raise ValueError(f"{where}: x has no rows")
     dev = _on_device(where, x=x, row_to_token=row_to_token)
     codes = torch.empty((P, K // 32, 16), dtype=torch.uint8, device=dev)
-    scales = torch.empty((P, K // 32), dtype=torch.uint8, device=dev)
+    scales = torch.empty(((K + 127) // 128, P, 4), dtype=torch.uint8, device=dev)
     _call(where, lib.gmxfp4_quantize_rows, dev, x.data_ptr(), T, K, _at(row_to_token), P,
           1 if swiglu else 0, codes.data_ptr(), scales.data_ptr())
     return codes, scales
@@ -666,8 +667,8 @@ def gmxfp4_quantize_rows(x, row_to_token=None, swiglu=False):
 
 def gmxfp4_grouped_gemm_a4(x_codes, x_scales, blocks, scales, expert_offsets, out=None):
     """out[P, N] bf16 = rows @ W_e^T per expert, both in MXFP4: x_codes
-    [P, K/32, 16] (or [P, K/2]) and x_scales [P, K/32] from
-    gmxfp4_quantize_rows, expert-sorted; blocks [E, N, K/32, 16] (or
+    [P, K/32, 16] and x_scales [ceil(K/128), P, 4] from gmxfp4_quantize_rows,
+    expert-sorted; blocks [E, N, K/32, 16] (or
     [E, N, K/2]), scales [E, N, K/32]."""
     where = "gmxfp4_grouped_gemm_a4"
     _need(x_codes, "x_codes", torch.uint8)
@@ -675,14 +676,12 @@ def gmxfp4_grouped_gemm_a4(x_codes, x_scales, blocks, scales, expert_offsets, ou
     _need(blocks, "packed weights", torch.uint8)
     _need(scales, "scales", torch.uint8)
     _need(expert_offsets, "expert_offsets", torch.int32)
-    if x_scales.dim() != 2 or blocks.dim() < 3 or x_codes.dim() < 2:
-        raise ValueError(f"{where}: x_codes must be [P, ...], x_scales [P, K/32] and the "
-                         "weights [E, N, ...]")
-    P, K = x_scales.shape[0], x_scales.shape[1] * 32
+    if x_codes.dim() != 3 or x_codes.shape[2] != 16 or blocks.dim() < 3:
+        raise ValueError(f"{where}: x_codes must be [P, K/32, 16] and the weights [E, N, ...]")
+    P, K = x_codes.shape[0], x_codes.shape[1] * 32
     E, N = blocks.shape[0], blocks.shape[1]
-    if K == 0 or x_codes.shape[0] != P:
-        raise ValueError(f"{where}: x_codes must hold the {P} rows of x_scales")
-    _numel(x_codes, "x_codes", P * (K // 2), where)
+    if K == 0 or tuple(x_scales.shape) != ((K + 127) // 128, P, 4):
+        raise ValueError(f"{where}: x_scales must be [{(K + 127) // 128}, {P}, 4]")
     _numel(blocks, "packed weights", E * N * (K // 2), where)
     _numel(scales, "scales", E * N * (K // 32), where)
     _numel(expert_offsets, "expert_offsets", E + 1, where)

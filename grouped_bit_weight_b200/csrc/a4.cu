@@ -62,47 +62,56 @@ __device__ __forceinline__ void unpack8(uint4 q, float (&v)[8]) {
   }
 }
 
-// A thread quantises 8 values; the 4 lanes of a 32-block share its maximum.
+// A warp quantises one row, 8 values a lane; the 4 lanes of a 32-block share
+// its maximum.  The scale bytes of 128 k are one word: word (k / 128) * P + p.
 template <bool kGLU>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(
-    const uint16_t* __restrict__ x, int64_t T, int64_t K, const int32_t* __restrict__ r2t,
-    int64_t n, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int* err) {
+    const uint16_t* __restrict__ x, int64_t T, int K, const int32_t* __restrict__ r2t, int64_t P,
+    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int* err) {
   grid_launch_dependents();
-  const int64_t U = K / 8;
-  // n is a multiple of 4: a quad is in or out of the loop as one
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const unsigned quad = 0xFu << (threadIdx.x & 28);
-    const int64_t p = i / U, c = i - p * U;
-    const int64_t t = token_of_row(r2t, (int32_t)p, T, err);
-    float v[8];
-    if (kGLU) {
-      float u[8];
-      const uint16_t* row = x + t * 2 * K + c * 8;
-      unpack8(__ldg(reinterpret_cast<const uint4*>(row)), v);
-      unpack8(__ldg(reinterpret_cast<const uint4*>(row + K)), u);
+  const int lane = threadIdx.x & 31, U = K / 8;
+  const int64_t nw = (int64_t)gridDim.x * (blockDim.x >> 5);
+  for (int64_t p = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); p < P; p += nw) {
+    const int64_t t = token_of_row(r2t, (int32_t)p, T, lane == 0 ? err : nullptr);
+    const uint4* row = reinterpret_cast<const uint4*>(x + t * K * (kGLU ? 2 : 1));
+    uint32_t* out = reinterpret_cast<uint32_t*>(codes) + p * U;
+    uint8_t* sc = scales + p * 4;
+#pragma unroll 4
+    for (int c = lane; c < ((U + 31) & ~31); c += 32) {
+      float v[8];
+      if (c < U) {
+        unpack8(__ldg(row + c), v);
+        if (kGLU) {
+          float u[8];
+          unpack8(__ldg(row + U + c), u);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fdiv_rn(v[j], 1.0f + expf(-v[j])) * u[j];
-    } else {
-      unpack8(__ldg(reinterpret_cast<const uint4*>(x + t * K + c * 8)), v);
+          for (int j = 0; j < 8; ++j) v[j] = __fdividef(v[j], 1.0f + __expf(-v[j])) * u[j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+      }
+      uint32_t m = 0;  // magnitudes order as their bits do, NaN and inf on top
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const uint32_t ex = m >> 23;
+      uint32_t byte = ex > 2u ? ex - 2u : 0u;
+      uint32_t q = 0;
+      if (ex == 255u) {
+        byte = 255u;  // a value that is not finite: the block is NaN
+      } else if (m) {
+        const float inv = __uint_as_float((254u - byte) << 23);  // 2^-X
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q |= e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv) << (8 * j);
+      }
+      if (c < U) out[c] = q;
+      // the four blocks of a word, those past the row 2^0
+      if (c >= U) byte = 127u;
+      if ((lane & 3) == 0 && ((c < U) || (c >> 4) == ((U - 1) >> 4)))
+        sc[(int64_t)(c >> 4) * P * 4 + ((c >> 2) & 3)] = (uint8_t)byte;
     }
-    uint32_t m = 0;  // magnitudes order as their bits do, NaN and inf on top
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(quad, m, 1));
-    m = max(m, __shfl_xor_sync(quad, m, 2));
-    const uint32_t ex = m >> 23;
-    uint32_t byte = ex > 2u ? ex - 2u : 0u;
-    uint32_t q = 0;
-    if (ex == 255u) {
-      byte = 255u;  // a value that is not finite: the block is NaN
-    } else if (m) {
-      const float inv = __uint_as_float((254u - byte) << 23);  // 2^-X
-#pragma unroll
-      for (int j = 0; j < 4; ++j) q |= e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv) << (8 * j);
-    }
-    reinterpret_cast<uint32_t*>(codes)[i] = q;
-    if ((c & 3) == 0) scales[i >> 2] = (uint8_t)byte;
   }
 }
 
@@ -111,8 +120,9 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(
 // ----------------------------------------------------------------------
 
 constexpr int BM = 128;       // weight rows per tile (MMA M)
-constexpr int BH = 192;       // routed rows per accumulator half (MMA N)
+constexpr int BH = 192;       // TMEM columns of an accumulator half
 constexpr int BT = 2 * BH;    // routed rows per tile
+constexpr int BN = 256;       // routed rows of one MMA at most (MMA N)
 constexpr int BKB = 128;      // bytes of codes per row and stage: 256 k
 constexpr int BOX = 64;       // routed rows per TMA box
 constexpr int ST = 3;         // ring stages
@@ -127,9 +137,13 @@ constexpr int kBHalfBytes = BH * BKB;             // 24 KB
 constexpr int kSfBytes = 2 * 512 + 2 * 4 * 512;   // A: 2 k-atoms; B: 2 halves x 2 x 2
 constexpr int kStageBytes = kABytes + 2 * kBHalfBytes + kSfBytes;
 static_assert(kStageBytes % 1024 == 0 && kBHalfBytes % 1024 == 0, "swizzle atoms stay aligned");
+constexpr int kEpiWarps = 8;
+constexpr int kEpiRow = 64 + 16;                  // 32 bf16 and a pad
+constexpr int kEpiBytes = 16 * kEpiRow;           // 16 routed rows x 32 weight rows
 
 struct Smem {
-  static constexpr int bars = ST * kStageBytes;
+  static constexpr int epi = ST * kStageBytes;
+  static constexpr int bars = epi + kEpiWarps * kEpiBytes;
   static constexpr int nbars = 2 * ST + 4 + 1;
   static constexpr int misc = bars + nbars * 8;
   static constexpr int tables = misc + 16;
@@ -138,18 +152,21 @@ static_assert(1024 + Smem::tables + 8 * (1024 + 1) <= 232448,
               "shared memory for 1024 experts exceeds the 227 KB a CTA can have");
 
 struct A4Problem {
-  const uint8_t* xs;       // [P, K/32] e8m0
+  const uint32_t* xs;      // [ceil(K/128), P] words of four e8m0
   const uint8_t* ws;       // [E, N, K/32] e8m0
   int64_t P, K, N;
   int32_t E;
   const int32_t* offsets;  // [E + 1]
   uint16_t* out;           // [P, N] bf16
   int* err;
-  int xvec, wvec;          // widest aligned load of a row's scales: 1, 2, 4 or 8 bytes
+  int wvec;                // widest aligned load of a weight row's scales: 1, 2, 4 or 8 bytes
 };
 
+// nv routed rows.  Up to BN of them are one MMA (N = nv): up to BH in one
+// accumulator half, more across both.  More than BN are two MMAs, the first nh
+// rows in the first half.
 struct Tile {
-  int32_t e, n0, p0, nv, nh;  // nv routed rows, the first nh of them in the first half
+  int32_t e, n0, p0, nv, nh;
 };
 
 __device__ __forceinline__ int32_t row_tiles(int32_t cnt) { return (cnt + BT - 1) / BT; }
@@ -172,18 +189,19 @@ __device__ __forceinline__ Tile tile_info(int64_t t, const int32_t* off, const i
   d.n0 = nt * BM;
   d.p0 = off[lo] + r * per;
   d.nv = min(per, cnt - r * per);
-  d.nh = d.nv <= BH ? d.nv : min(d.nv, ((d.nv + 31) / 32) * 16);
+  d.nh = d.nv <= BN ? d.nv : ((d.nv + 31) / 32) * 16;
   return d;
 }
 
-// Which accumulator half a tile uses (see the file comment); the MMA thread
-// and the epilogue step identical copies.
+// Which accumulator half a tile of up to BH rows uses: they alternate, so that
+// an epilogue overlaps the next tile's MMAs; a larger tile takes both.  The MMA
+// thread and the epilogue step identical copies.
 struct AccSched {
   uint32_t h = 0;
   uint32_t use0 = 0, use1 = 0;
   __device__ __forceinline__ uint32_t phase(uint32_t k) const { return (k ? use1 : use0) & 1u; }
-  __device__ __forceinline__ void next(bool wide) {
-    if (wide) {
+  __device__ __forceinline__ void next(bool both) {
+    if (both) {
       ++use0;
       ++use1;
     } else {
@@ -283,8 +301,8 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
   const int32_t ntn = (int32_t)((N + BM - 1) / BM);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1 + 8); mbar_init(&empty[i], 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 4); }
+    for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1 + 4); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], kEpiWarps); }
     mbar_init(mma_done, 1);
     *abort = 0;
     fence_barrier_init();
@@ -333,8 +351,10 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
+    // One thread issues everything, so its instructions count: descriptors are
+    // built once and advance by constants, a whole stage is unrolled.
     if (lane == 0) {
-      uint32_t g = 0;
+      uint32_t g = 0, s = 0, ph = 0;
       bool ok = true;
       AccSched acc;
       const uint64_t adesc0 = make_sdesc_sw128(smem_u32(smem), 16, 1024);
@@ -342,160 +362,189 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
       const uint64_t sdesc0 = sdesc_scales(smem_u32(smem + kABytes + 2 * kBHalfBytes));
       for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
         const Tile d = tile_info(t, off_s, ts_s, E);
-        const bool wide = d.nv > d.nh;
-        const uint32_t h0 = acc.h, h1 = acc.h ^ 1u;
+        const bool both = d.nv > BH, two = d.nv > BN;
+        const uint32_t h0 = both ? 0u : acc.h;
         const uint32_t n0 = (uint32_t)(d.nh + 15) & ~15u, n1 = (uint32_t)(d.nv - d.nh + 15) & ~15u;
+        const uint32_t i0 = idesc_mxf4(n0, 0), i1 = idesc_mxf4(n1, 0);
+        constexpr uint32_t kUpper = (2u << 4) | (2u << 29);  // the scale words' upper halves
+        const bool far0 = n0 > 128u, far1 = n1 > 128u;
+        const uint32_t d0 = tmem + h0 * BH, d1 = tmem + BH;
         if (!(ok = mbar_wait(&acc_empty[h0], acc.phase(h0) ^ 1u, abort, pb.err))) break;
-        tc_fence_after();
+        if (both && !two && !(ok = mbar_wait(&acc_empty[1], acc.phase(1) ^ 1u, abort, pb.err))) break;
         for (int ks = 0; ks < NS; ++ks, ++g) {
-          const uint32_t s = g % ST;
-          if (!(ok = mbar_wait(&full[s], (g / ST) & 1u, abort, pb.err))) break;
+          if (!(ok = mbar_wait(&full[s], ph, abort, pb.err))) break;
+          if (two && ks == 0 && !(ok = mbar_wait(&acc_empty[1], acc.phase(1) ^ 1u, abort, pb.err))) break;
           tc_fence_after();
           const uint64_t so = (uint64_t)((s * kStageBytes) >> 4);
+          const uint64_t ad = adesc0 + so, bd = bdesc0 + so, sd = sdesc0 + so;
+          const uint64_t bd1 = bd + (uint64_t)(kBHalfBytes >> 4);
           const uint32_t sf = tmem + kSfCol + (g & 1u) * kSfSet;
-          const int nk = min(4, (KB - ks * BKB + 31) / 32);  // 64-k steps of this stage
-          const int na = (nk + 1) / 2;                       // 128-k scale atoms
-          for (int a = 0; a < na; ++a) {
-            const uint64_t sd = sdesc0 + so;
+          // scales of 128-k atom a, then its two 64-k steps
+          auto atom = [&](int a, bool second) __attribute__((always_inline)) {
             tc_cp_scales(sf + a * 4, sd + a * 32);
             tc_cp_scales(sf + 8 + a * 8, sd + 64 + a * 64);
-            if (n0 > 128u) tc_cp_scales(sf + 8 + a * 8 + 4, sd + 64 + a * 64 + 32);
-            if (wide) {
+            if (far0) tc_cp_scales(sf + 8 + a * 8 + 4, sd + 64 + a * 64 + 32);
+            tc_mma_mxf4(d0, ad + 4 * a, bd + 4 * a, i0, sf + a * 4, sf + 8 + a * 8, a > 0 || ks > 0);
+            if (second)
+              tc_mma_mxf4(d0, ad + 4 * a + 2, bd + 4 * a + 2, i0 | kUpper, sf + a * 4, sf + 8 + a * 8, 1u);
+            if (two) {
               tc_cp_scales(sf + 24 + a * 8, sd + 192 + a * 64);
-              if (n1 > 128u) tc_cp_scales(sf + 24 + a * 8 + 4, sd + 192 + a * 64 + 32);
+              if (far1) tc_cp_scales(sf + 24 + a * 8 + 4, sd + 192 + a * 64 + 32);
+              tc_mma_mxf4(d1, ad + 4 * a, bd1 + 4 * a, i1, sf + a * 4, sf + 24 + a * 8, a > 0 || ks > 0);
+              if (second)
+                tc_mma_mxf4(d1, ad + 4 * a + 2, bd1 + 4 * a + 2, i1 | kUpper, sf + a * 4,
+                            sf + 24 + a * 8, 1u);
             }
-          }
-          const uint64_t ad = adesc0 + so, bd = bdesc0 + so;
-          for (int kk = 0; kk < nk; ++kk)
-            tc_mma_mxf4(tmem + h0 * BH, ad + 2 * kk, bd + 2 * kk,
-                        idesc_mxf4(n0, (uint32_t)(kk & 1) * 2u), sf + (kk >> 1) * 4,
-                        sf + 8 + (kk >> 1) * 8, (ks | kk) != 0);
-          if (wide) {
-            if (ks == 0) {
-              if (!(ok = mbar_wait(&acc_empty[h1], acc.phase(h1) ^ 1u, abort, pb.err))) break;
-              tc_fence_after();
-            }
-            const uint64_t bd1 = bd + (uint64_t)(kBHalfBytes >> 4);
-            for (int kk = 0; kk < nk; ++kk)
-              tc_mma_mxf4(tmem + h1 * BH, ad + 2 * kk, bd1 + 2 * kk,
-                          idesc_mxf4(n1, (uint32_t)(kk & 1) * 2u), sf + (kk >> 1) * 4,
-                          sf + 24 + (kk >> 1) * 8, (ks | kk) != 0);
+          };
+          const int nk = (KB - ks * BKB + 31) / 32;  // 64-k steps left
+          if (nk >= 4) {
+            atom(0, true);
+            atom(1, true);
+          } else {
+            atom(0, nk > 1);
+            if (nk > 2) atom(1, false);
           }
           tc_commit(&empty[s]);
+          if (++s == ST) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
         tc_commit(&acc_full[h0]);
-        if (wide) tc_commit(&acc_full[h1]);
-        acc.next(wide);
+        if (both) tc_commit(&acc_full[1]);
+        acc.next(both);
       }
       tc_commit(mma_done);
       mbar_drain(mma_done, 0);
     }
-  } else if (warp >= 4 && warp < 12) {
+  } else if (warp >= 4 && warp < 8) {
     // ---------------- scales ----------------
-    // thread i: rows i and i + 256 of (128 weight rows, 192 + 192 routed rows)
+    // thread i: weight row i and routed rows i, i + 128, i + 256 of the tile;
+    // loaded a stage ahead
     const int i = (warp - 4) * 32 + lane;
-    // where this thread's rows go in a stage's scale area (first k-atom), and
-    // the distance of the second k-atom
-    auto place_of = [](int r, int& atom) -> int {
-      if (r < BM) {
-        atom = 512;
-        return (r & 31) * 16 + (r >> 5) * 4;
-      }
-      const int j = (r - BM) % BH, h = (r - BM) / BH;
-      atom = 1024;
-      return 1024 + h * 2048 + (j >> 7) * 512 + (j & 31) * 16 + ((j & 127) >> 5) * 4;
-    };
-    int atom0, atom1;
-    const int at0 = place_of(i, atom0), at1 = place_of(i + 256, atom1);
-    struct Src {
-      const uint8_t* p;  // the row's scales, or null
-      int vec;
-    };
-    auto src_of = [&](const Tile& d, int r) -> Src {
-      if (r < BM) {
-        if (d.n0 + r >= N) return {nullptr, 1};
-        return {pb.ws + ((int64_t)d.e * N + d.n0 + r) * KS, pb.wvec};
-      }
-      const int j = (r - BM) % BH, h = (r - BM) / BH;
-      const int row = h ? d.nh + j : j, end = h ? d.nv : d.nh;
-      if (row >= end) return {nullptr, 1};
-      return {pb.xs + (int64_t)(d.p0 + row) * KS, pb.xvec};
-    };
+    const int spot = (i & 31) * 16 + (i >> 5) * 4;  // of row i among 128
     const uint2 ones = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    auto get = [&](const Src& s, int ks) -> uint2 {
-      return s.p ? load_scales(s.p + 8 * ks, KS - 8 * ks, s.vec) : ones;
+    const uint8_t* wp = nullptr;                    // the weight row's scales, or null
+    const uint32_t* xp[3] = {nullptr, nullptr, nullptr};  // the routed rows' first words, or null
+    int at[3] = {0, 0, 0};                          // their places in the scale area
+    const int KA = (KS + 3) / 4;                    // words of a routed row
+    auto open = [&](int64_t t) __attribute__((always_inline)) {
+      const Tile d = tile_info(t, off_s, ts_s, E);
+      wp = d.n0 + i < N ? pb.ws + ((int64_t)d.e * N + d.n0 + i) * KS : nullptr;
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        int j = i + 128 * q, h = 0;
+        bool on = j < d.nv;
+        if (d.nv > BN) {  // two MMAs: rows nh .. belong to the second half
+          h = j >= BH;
+          if (h) j -= BH;
+          on = j < (h ? d.nv - d.nh : d.nh);
+        }
+        xp[q] = on ? pb.xs + d.p0 + (h ? d.nh : 0) + j : nullptr;
+        at[q] = j < BN ? 1024 + h * 2048 + (j >> 7) * 512 + (j & 31) * 16 + ((j & 127) >> 5) * 4 : -1;
+      }
+    };
+    uint2 wv = ones, xv[3] = {ones, ones, ones};
+    auto get = [&](int ks) __attribute__((always_inline)) {
+      wv = wp ? load_scales(wp + 8 * ks, KS - 8 * ks, pb.wvec) : ones;
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        xv[q] = ones;
+        if (xp[q]) {
+          xv[q].x = __ldg(xp[q] + (int64_t)(2 * ks) * pb.P);
+          if (2 * ks + 1 < KA) xv[q].y = __ldg(xp[q] + (int64_t)(2 * ks + 1) * pb.P);
+        }
+      }
     };
     int64_t t = blockIdx.x;
     int ks = 0;
-    Src s0{nullptr, 1}, s1{nullptr, 1};
-    uint2 v0 = ones, v1 = ones;
+    int to[3] = {0, 0, 0};  // places of the stage being written
     if (t < ntiles) {
-      const Tile d = tile_info(t, off_s, ts_s, E);
-      s0 = src_of(d, i);
-      s1 = src_of(d, i + 256);
-      v0 = get(s0, 0);
-      v1 = get(s1, 0);
+      open(t);
+      get(0);
     }
-    for (uint32_t g = 0; t < ntiles; ++g) {
-      const uint2 c0 = v0, c1 = v1;
+    uint32_t s = 0, ph = 0;
+    while (t < ntiles) {
+      const uint2 w0 = wv, x0 = xv[0], x1 = xv[1], x2 = xv[2];
+#pragma unroll
+      for (int q = 0; q < 3; ++q) to[q] = at[q];
       if (++ks == NS) {
         ks = 0;
         t += gridDim.x;
-        if (t < ntiles) {
-          const Tile d = tile_info(t, off_s, ts_s, E);
-          s0 = src_of(d, i);
-          s1 = src_of(d, i + 256);
-        }
+        if (t < ntiles) open(t);
       }
-      if (t < ntiles) {
-        v0 = get(s0, ks);
-        v1 = get(s1, ks);
-      }
-      const uint32_t s = g % ST;
-      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((g / ST) & 1u) ^ 1u, abort, pb.err))) break;
+      if (t < ntiles) get(ks);
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, abort, pb.err))) break;
       uint8_t* sf = smem + s * kStageBytes + kABytes + 2 * kBHalfBytes;
-      *reinterpret_cast<uint32_t*>(sf + at0) = c0.x;
-      *reinterpret_cast<uint32_t*>(sf + at0 + atom0) = c0.y;
-      *reinterpret_cast<uint32_t*>(sf + at1) = c1.x;
-      *reinterpret_cast<uint32_t*>(sf + at1 + atom1) = c1.y;
+      *reinterpret_cast<uint32_t*>(sf + spot) = w0.x;
+      *reinterpret_cast<uint32_t*>(sf + spot + 512) = w0.y;
+      auto put = [&](int where, uint2 v) __attribute__((always_inline)) {
+        if (where >= 0) {
+          *reinterpret_cast<uint32_t*>(sf + where) = v.x;
+          *reinterpret_cast<uint32_t*>(sf + where + 1024) = v.y;
+        }
+      };
+      put(to[0], x0);
+      put(to[1], x1);
+      put(to[2], x2);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[s]);
+      if (++s == ST) { s = 0; ph ^= 1u; }
     }
-  } else if (warp >= 12) {
+  } else if (warp >= 8) {
     // ---------------- epilogue ----------------
+    // warp quarter q reads weight rows 32 q .. of the tile (TMEM lanes); the two
+    // warps of a quarter take alternate 16-row pieces of the routed rows, turn
+    // them over in shared memory and store 64-byte row segments
     const uint32_t q = (uint32_t)warp & 3u;
+    const int mine = (warp - 8) >> 2;
+    uint8_t* turn = smem + Smem::epi + (warp - 8) * kEpiBytes;
+    uint16_t* put = reinterpret_cast<uint16_t*>(turn) + lane;
+    const uint8_t* got = turn + (lane >> 2) * kEpiRow + (lane & 3) * 16;
     AccSched acc;
     bool ok = true;
     for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
       const Tile d = tile_info(t, off_s, ts_s, E);
-      const bool wide = d.nv > d.nh;
-      const int64_t n = d.n0 + (int64_t)(q * 32 + lane);
-      for (int part = 0; part < (wide ? 2 : 1); ++part) {
-        const uint32_t h = part ? acc.h ^ 1u : acc.h;
+      const bool both = d.nv > BH, two = d.nv > BN;
+      // this lane's 8 weight rows of a stored segment
+      const int64_t n = d.n0 + (int64_t)(q * 32 + (lane & 3) * 8);
+      for (int part = 0; part < (two ? 2 : 1); ++part) {
+        const uint32_t h = both ? (uint32_t)part : acc.h;
         ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[h], acc.phase(h), abort, pb.err));
+        if (ok && both && !two)
+          ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[1], acc.phase(1), abort, pb.err));
         if (!ok) break;
         tc_fence_after();
         const int rows = part ? d.nv - d.nh : d.nh;
-        uint16_t* dst = pb.out + (int64_t)(d.p0 + (part ? d.nh : 0)) * N + n;
+        uint16_t* dst = pb.out + (int64_t)(d.p0 + (part ? d.nh : 0) + (lane >> 2)) * N + n;
         const uint32_t taddr = tmem + ((q * 32u) << 16) + h * BH;
-        for (int c = 0; c < rows; c += 32) {
-          uint32_t r[32];
-          tmem_load_32x32b_x32(taddr + c, r);
+#pragma unroll 1
+        for (int c = mine * 16; c < rows; c += 32) {
+          uint32_t r[16];
+          tmem_load_32x32b_x16(taddr + c, r);
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const uint32_t v = pack_bf16x2(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+            put[j * (kEpiRow / 2)] = (uint16_t)v;
+            put[(j + 1) * (kEpiRow / 2)] = (uint16_t)(v >> 16);
+          }
+          __syncwarp();
           if (n < N) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < rows)
-                dst[(int64_t)(c + j) * N] =
-                    __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[j])));
+            for (int j = 0; j < 16; j += 8)
+              if (c + j + (lane >> 2) < rows)
+                *reinterpret_cast<uint4*>(dst + (int64_t)(c + j) * N) =
+                    *reinterpret_cast<const uint4*>(got + j * kEpiRow);
           }
+          __syncwarp();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[h]);
+        if (lane == 0) {
+          mbar_arrive(&acc_empty[h]);
+          if (both && !two) mbar_arrive(&acc_empty[1]);
+        }
       }
-      acc.next(wide);
+      acc.next(both);
     }
   }
 
@@ -516,14 +565,13 @@ int scale_vec(const void* base, int64_t pitch) {
 cudaError_t launch_quantize_rows(const uint16_t* x, int64_t T, int64_t K, const int32_t* r2t,
                                  int64_t P, bool glu, uint8_t* codes, uint8_t* scales, int* err,
                                  int num_sms, cudaStream_t s) {
-  const int64_t n = P * (K / 8);
-  if (n == 0) return cudaSuccess;
-  const int64_t need = (n + 255) / 256, most = 64 * (int64_t)num_sms;
+  if (P == 0) return cudaSuccess;
+  const int64_t need = (P + 7) / 8, most = 64 * (int64_t)num_sms;
   const int grid = (int)(need < most ? need : most);
-  return glu ? launch_kernel<quantize_rows_kernel<true>>(grid, 256, 0, s, false, x, T, K, r2t, n,
-                                                         codes, scales, err)
-             : launch_kernel<quantize_rows_kernel<false>>(grid, 256, 0, s, false, x, T, K, r2t, n,
-                                                          codes, scales, err);
+  return glu ? launch_kernel<quantize_rows_kernel<true>>(grid, 256, 0, s, false, x, T, (int)K, r2t,
+                                                         P, codes, scales, err)
+             : launch_kernel<quantize_rows_kernel<false>>(grid, 256, 0, s, false, x, T, (int)K, r2t,
+                                                          P, codes, scales, err);
 }
 
 cudaError_t launch_gemm_a4(const uint8_t* xq, const uint8_t* xs, int64_t P, int64_t K,
@@ -539,7 +587,7 @@ cudaError_t launch_gemm_a4(const uint8_t* xq, const uint8_t* xs, int64_t P, int6
   e = make_map_2d(&tmx, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, (uint64_t)K / 2, (uint64_t)P,
                   (uint64_t)K / 2, BKB, BOX, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
-  const A4Problem pb{xs, ws, P, K, N, E, offsets, out, err, scale_vec(xs, K / 32),
+  const A4Problem pb{reinterpret_cast<const uint32_t*>(xs), ws, P, K, N, E, offsets, out, err,
                      scale_vec(ws, K / 32)};
   constexpr size_t most = 1024 + Smem::tables + 8 * (1024 + 1);
   e = opt_in_smem<gemm_a4_kernel>(most);

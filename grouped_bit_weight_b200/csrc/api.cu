@@ -533,8 +533,8 @@ gbw_status gmxfp4_quantize_rows(const uint16_t* x, int64_t T, int64_t K,
   if (row_to_token && P > 0 && T < 1) return fail(GBW_ERR_SHAPE, "T must be >= 1");
   if (P > 0 && (!x || !codes || !scales)) return fail(GBW_ERR_NULL, "NULL x, codes or scales");
   if (!aligned16(x)) return fail(GBW_ERR_ALIGN, "x must be 16-byte aligned");
-  if (!aligned4(codes) || !aligned4(row_to_token))
-    return fail(GBW_ERR_ALIGN, "codes and row_to_token must be 4-byte aligned");
+  if (!aligned4(codes) || !aligned4(scales) || !aligned4(row_to_token))
+    return fail(GBW_ERR_ALIGN, "codes, scales and row_to_token must be 4-byte aligned");
   int* err = nullptr;
   int sms = 0;
   gbw_status st = device_state(&err, &sms);
@@ -559,7 +559,8 @@ gbw_status gmxfp4_grouped_gemm_a4(const uint8_t* x_codes, const uint8_t* x_scale
   if (P > 0 && (!x_codes || !x_scales || !out)) return fail(GBW_ERR_NULL, "NULL rows or out");
   if (!aligned16(x_codes) || !aligned16(blocks) || !aligned16(out))
     return fail(GBW_ERR_ALIGN, "x_codes, blocks and out must be 16-byte aligned");
-  if (!aligned4(expert_offsets)) return fail(GBW_ERR_ALIGN, "offsets must be 4-byte aligned");
+  if (!aligned4(expert_offsets) || !aligned4(x_scales))
+    return fail(GBW_ERR_ALIGN, "offsets and x_scales must be 4-byte aligned");
   int* err = nullptr;
   int sms = 0;
   gbw_status st = device_state(&err, &sms);

@@ -330,25 +330,27 @@ GBW_API int64_t gmoe_layer_workspace(int64_t T, int32_t E, int32_t k, int64_t H,
  *   swiglu != 0: x [T, 2K] bf16 (a gate_up output, gate columns first),
  *                v[k] = silu(x[k]) * x[K + k] in fp32, not rounded in between
  *   codes  [P, K/32, 16] (= [P, K/2]) uint8, low nibble = even k
- *   scales [P, K/32] uint8 e8m0
+ *   scales [ceil(K/128), P, 4] uint8 e8m0: byte b of word (a, p) is the scale of
+ *          row p's block 4 a + b, 127 past the last; the rows of a word are
+ *          next to each other, as the product loads them
  * Per 32 values: X = floor(log2 max|v|) - 2 clamped to [-127, 127], scale byte
  * X + 127, codes = nearest e2m1 to v / 2^X (ties to the even code,
  * saturating, sign kept); an all-zero block gets scale 0 and codes 0, a block
  * with a value that is not finite scale 255 (NaN) and codes 0.  Token indices
  * are clamped to [0, T) and recorded as in gmxfp4_grouped_gemm.
- * Requires K % 32 == 0, 16-byte aligned x and 4-byte aligned codes. */
+ * Requires K % 32 == 0, 16-byte aligned x, 4-byte aligned codes and scales. */
 GBW_API gbw_status gmxfp4_quantize_rows(const uint16_t* x, int64_t T, int64_t K,
                                         const int32_t* row_to_token, int64_t P, int32_t swiglu,
                                         uint8_t* codes, uint8_t* scales, void* stream);
 
 /* Grouped MXFP4 x MXFP4 product (W4A4) on the block-scaled tensor cores:
  *   out[p, n] = bf16( sum_k xq[p, k] * W_e(p)[n, k] ),  fp32 accumulation
- *   x_codes [P, K/2] uint8, x_scales [P, K/32] uint8: expert-sorted rows as
- *           gmxfp4_quantize_rows writes them
+ *   x_codes [P, K/2] uint8, x_scales [ceil(K/128), P, 4] uint8: expert-sorted
+ *           rows as gmxfp4_quantize_rows writes them
  *   blocks, scales, expert_offsets, out: as in gmxfp4_grouped_gemm (scales
  *           need no alignment here)
  * Requires K % 32 == 0, N % 8 == 0, 1 <= E <= 1024, 16-byte aligned x_codes,
- * blocks and out.  P == 0 is a no-op.  Rows of out past expert_offsets[E] are
+ * blocks and out, 4-byte aligned x_scales.  P == 0 is a no-op.  Rows of out past expert_offsets[E] are
  * not written. */
 GBW_API gbw_status gmxfp4_grouped_gemm_a4(const uint8_t* x_codes, const uint8_t* x_scales,
                                           int64_t P, int64_t K, const uint8_t* blocks,

@@ -24,6 +24,13 @@ def _codes(t):
     return np.stack([c & 15, c >> 4], -1).reshape(t.shape[0], -1)
 
 
+def _scales(t, K):
+    """scales [ceil(K/128), P, 4] uint8 -> [P, K/32]; past K they are 127."""
+    s = t.cpu().numpy().transpose(1, 0, 2).reshape(t.shape[1], -1)
+    assert (s[:, K // 32:] == 127).all()
+    return s[:, :K // 32]
+
+
 def _values(codes, scales):
     q = codes.astype(np.int64)
     v = mp.E2M1[q & 7] * np.where(q & 8, -1.0, 1.0)
@@ -51,11 +58,11 @@ def test_quantize_rows_bytes(T, K):
     x = x.to(torch.bfloat16)
     codes, scales = gbw.gmxfp4_quantize_rows(x.to(DEV))
     c, s, _ = mp.mxfp4(x.double().numpy())
-    assert codes.shape == (T, K // 32, 16) and scales.shape == (T, K // 32)
-    assert (scales.cpu().numpy() == s).all() and (_codes(codes) == c).all()
+    assert codes.shape == (T, K // 32, 16) and scales.shape == ((K + 127) // 128, T, 4)
+    assert (_scales(scales, K) == s).all() and (_codes(codes) == c).all()
     perm = torch.randint(0, T, (2 * T + 1,), generator=torch.Generator().manual_seed(1))
     codes, scales = gbw.gmxfp4_quantize_rows(x.to(DEV), perm.to(torch.int32).to(DEV))
-    assert (scales.cpu().numpy() == s[perm]).all() and (_codes(codes) == c[perm]).all()
+    assert (_scales(scales, K) == s[perm]).all() and (_codes(codes) == c[perm]).all()
     assert gbw.device_status() == 0
 
 
@@ -78,7 +85,7 @@ def test_quantize_rows_special_values():
     x = x.to(torch.bfloat16)
     codes, scales = gbw.gmxfp4_quantize_rows(x.to(DEV))
     c, s, _ = mp.mxfp4(x.double().numpy())
-    assert (scales.cpu().numpy() == s).all() and (_codes(codes) == c).all()
+    assert (_scales(scales, 64) == s).all() and (_codes(codes) == c).all()
 
 
 @pytest.mark.gpu
@@ -91,14 +98,14 @@ def test_quantize_rows_swiglu(T, K):
     x[0, :4] = torch.tensor([100.0, -100.0, 0.0, -3e38])
     h = mp.silu(x[:, :K].double().numpy()) * x[:, K:].double().numpy()
     codes, scales = gbw.gmxfp4_quantize_rows(x.to(DEV), swiglu=True)
-    got = _values(_codes(codes), scales.cpu().numpy())
+    got = _values(_codes(codes), _scales(scales, K))
     lo, hi = (mp.mxfp4(h * (1 + s * 2.0 ** -21))[2] for s in (-1, 1))
     mid = mp.mxfp4(h)[2]
     near = (got == lo) | (got == hi) | (got == mid)
     assert near.all() and (got != mid).mean() < 1e-3
     perm = torch.randint(0, T, (T + 3,), dtype=torch.int32)
     c2, s2 = gbw.gmxfp4_quantize_rows(x.to(DEV), perm.to(DEV), swiglu=True)
-    assert torch.equal(c2, codes[perm.long().to(DEV)]) and torch.equal(s2, scales[perm.long().to(DEV)])
+    assert torch.equal(c2, codes[perm.long().to(DEV)]) and torch.equal(s2, scales[:, perm.long().to(DEV)])
 
 
 def _check_product(counts, N, K, seed, rows_pad=0, xstd=None):
@@ -108,7 +115,7 @@ def _check_product(counts, N, K, seed, rows_pad=0, xstd=None):
     if xstd is not None:
         x = (x.float() * xstd[:, None]).to(torch.bfloat16)
     xq, xs = gbw.gmxfp4_quantize_rows(x.to(DEV))
-    xv = _values(_codes(xq), xs.cpu().numpy())
+    xv = _values(_codes(xq), _scales(xs, K))
     off = _offsets(counts)
     t = lambda a: torch.from_numpy(a).to(DEV)
     out = torch.full((P + rows_pad, N), 7.0, dtype=torch.bfloat16, device=DEV)
@@ -135,7 +142,7 @@ def _check_product(counts, N, K, seed, rows_pad=0, xstd=None):
     ([16], 128, 256), ([1], 8, 32), ([5, 0, 3], 136, 64), ([17, 31], 200, 96),
     ([16] * 8, 256, 512), ([0, 0, 40, 0], 264, 352), ([128, 129, 130], 128, 128),
     ([191, 192, 193], 320, 288), ([383, 384, 385], 128, 544), ([601, 2, 0, 77], 192, 320),
-    ([1000], 72, 1024), ([33], 1000, 2912), ([250, 256, 262, 20], 640, 2880),
+    ([1000], 72, 1024), ([33], 1000, 2912), ([250, 256, 262, 20], 640, 2880), ([255, 256, 257, 319, 320], 136, 640),
     ([3] * 64, 64, 160), ([2, 1] * 20, 2056, 768)])
 def test_product_matches_plain(counts, N, K):
     _check_product(counts, N, K, sum(counts) + N + K)
@@ -165,7 +172,7 @@ def test_product_scales_at_every_alignment():
         return b[n:n + a.numel()].view(a.shape)
 
     for n in (1, 2, 4, 6):
-        got = gbw.gmxfp4_grouped_gemm_a4(xq, shifted(xs, n), t(w), shifted(t(ws), 8 - n), off)
+        got = gbw.gmxfp4_grouped_gemm_a4(xq, shifted(xs, 4), t(w), shifted(t(ws), n), off)
         assert torch.equal(got, ref)
     assert gbw.device_status() == 0
 
@@ -233,7 +240,7 @@ def test_prompt_layer_in_mxfp4_from_routing_to_combine_in_a_graph():
         off, r2t, ros, _ = mp.plan(ids, E)
         assert (r.row_to_token.cpu().numpy() == r2t).all()
         xv = mp.mxfp4(x.cpu().double().numpy())[2][r2t]
-        hv = _values(_codes(h[0]), h[1].cpu().numpy())
+        hv = _values(_codes(h[0]), _scales(h[1], I))
         a64, y64 = a.cpu().double().numpy(), y.cpu().double().numpy()
         for e in range(E):
             s = slice(off[e], off[e + 1])
@@ -276,12 +283,13 @@ def test_a4_refusals():
         gbw.gmxfp4_quantize_rows(x[:0], torch.zeros(3, dtype=torch.int32))
     with pytest.raises(ValueError, match="CUDA tensor"):
         gbw.gmxfp4_quantize_rows(x)
-    a = dict(x_codes=u8(4, 2, 16), x_scales=u8(4, 2), blocks=u8(3, 8, 2, 16), scales=u8(3, 8, 2),
+    a = dict(x_codes=u8(4, 2, 16), x_scales=u8(1, 4, 4), blocks=u8(3, 8, 2, 16), scales=u8(3, 8, 2),
              expert_offsets=torch.zeros(4, dtype=torch.int32))
-    for name, bad, text in (("x_codes", u8(4, 3, 16), "x_codes"), ("scales", u8(3, 8, 3), "scales"),
+    for name, bad, text in (("x_codes", u8(4, 32), "x_codes"), ("x_codes", u8(5, 2, 16), "x_scales"),
+                            ("scales", u8(3, 8, 3), "scales"),
                             ("blocks", u8(3, 8, 3, 16), "packed weights"),
                             ("expert_offsets", torch.zeros(3, dtype=torch.int32), "expert_offsets"),
-                            ("x_scales", u8(5, 2), "x_codes")):
+                            ("x_scales", u8(4, 2), "x_scales")):
         with pytest.raises(ValueError, match=text):
             gbw.gmxfp4_grouped_gemm_a4(**{**a, name: bad})
     with pytest.raises(ValueError, match="out must"):
