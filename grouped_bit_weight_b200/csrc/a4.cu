@@ -12,21 +12,20 @@
 //
 // Quantise is bound by memory: 4 lanes share a 32-block, 16-byte loads.
 //
-// Product, one persistent CTA per SM, 16 warps ("swap AB": MMA M is 128
+// Product, one persistent CTA per SM, 20 warps ("swap AB": MMA M is 128
 // weight rows, MMA N the routed rows of one expert, so few rows give a narrow
 // N instead of a padded M):
 //   warp 0      TMA: packed weights [128 x 128 bytes = 256 k] and the rows'
 //               codes (boxes of 64 rows) into a 3-stage ring, 128B swizzle --
 //               the packed bytes are the MMA's operands as they are
-//   warps 4-11  the scale bytes of 128 weight rows and up to 384 routed rows:
-//               two rows per thread, loaded a stage ahead, written to shared
-//               memory in the 32-lane order that tcgen05.cp copies to TMEM
-//   warp 1      tcgen05.cp of a stage's scales into TMEM (two alternating
-//               sets), then tcgen05.mma.kind::mxf4.block_scale, 64 k each
-//   warps 12-15 epilogue: tcgen05.ld -> bf16 -> out, 64-byte row segments
-// A tile holds up to 384 routed rows: rows past 192 go to the second
-// accumulator half, fed by the same weights; tiles of up to 192 alternate
-// between the halves, so that an epilogue overlaps the next tile's MMAs.
+//   warps 4-11  the scale bytes of 128 weight rows and up to 384 routed rows,
+//               loaded two stages ahead and written to TMEM (a set per stage)
+//   warp 1      tcgen05.mma.kind::mxf4.block_scale, 64 k each
+//   warps 12-19 epilogue: tcgen05.ld -> bf16 -> turned over in shared memory ->
+//               64-byte row segments
+// A tile holds up to 384 routed rows, fed by the same weights: up to 256 are
+// one MMA, more are two; tiles of up to 192 alternate between two accumulator
+// halves, so that an epilogue overlaps the next tile's MMAs.
 // Tiles (expert, weight tile, row tile) run with row tiles innermost: an
 // expert's weights come from HBM once.
 #include "common.cuh"
@@ -126,15 +125,15 @@ constexpr int BN = 256;       // routed rows of one MMA at most (MMA N)
 constexpr int BKB = 128;      // bytes of codes per row and stage: 256 k
 constexpr int BOX = 64;       // routed rows per TMA box
 constexpr int ST = 3;         // ring stages
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSfCol = BT;      // scale columns: two sets
+constexpr uint32_t kSfCol = BT;      // scale columns: a set per ring stage
 constexpr uint32_t kSfSet = 8 + 2 * 16;
-static_assert(kSfCol + 2 * kSfSet <= kTmemCols, "accumulators and scales fit TMEM");
+static_assert(kSfCol + ST * kSfSet <= kTmemCols, "accumulators and scales fit TMEM");
 
 constexpr int kABytes = BM * BKB;                 // 16 KB
 constexpr int kBHalfBytes = BH * BKB;             // 24 KB
-constexpr int kSfBytes = 2 * 512 + 2 * 4 * 512;   // A: 2 k-atoms; B: 2 halves x 2 x 2
+constexpr int kSfBytes = 4096;                     // 8 scale bytes of 128 + 384 rows
 constexpr int kStageBytes = kABytes + 2 * kBHalfBytes + kSfBytes;
 static_assert(kStageBytes % 1024 == 0 && kBHalfBytes % 1024 == 0, "swizzle atoms stay aligned");
 constexpr int kEpiWarps = 8;
@@ -234,17 +233,28 @@ __device__ __forceinline__ void tc_mma_mxf4(uint32_t d, uint64_t a, uint64_t b, 
       : "memory");
 }
 
-// 512 bytes (32 lanes x 16) from shared memory to 4 TMEM columns, repeated
-// for the four groups of 32 lanes.
-__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
-               : "memory");
+// 8 or 16 columns of this warp's 32 TMEM lanes from registers; the registers
+// belong to the store until the wait, so that sits in the same statement.
+__device__ __forceinline__ void tmem_store_8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};\n"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
-// Unswizzled descriptor of such 512 bytes: 8-row groups 128 bytes apart.
-__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 16) |
-         ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1u << 46);
+// Barrier of the four warps of a scale group.
+__device__ __forceinline__ void group_sync(int group) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
 // Eight scale bytes at `p`, of which the first `nvalid` exist; the others
@@ -258,6 +268,10 @@ __device__ __forceinline__ uint2 load_scales(const uint8_t* p, int nvalid, int v
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       if (4 * i < nvalid) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+  } else if (vec == 2 && nvalid >= 8) {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+    const uint32_t a = __ldg(q), b = __ldg(q + 1), c = __ldg(q + 2), d = __ldg(q + 3);
+    return make_uint2(prmt(a, b, 0x5410u), prmt(c, d, 0x5410u));
   } else if (vec == 2) {
     uint32_t h[4];
 #pragma unroll
@@ -359,7 +373,6 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
       AccSched acc;
       const uint64_t adesc0 = make_sdesc_sw128(smem_u32(smem), 16, 1024);
       const uint64_t bdesc0 = make_sdesc_sw128(smem_u32(smem + kABytes), 16, 1024);
-      const uint64_t sdesc0 = sdesc_scales(smem_u32(smem + kABytes + 2 * kBHalfBytes));
       for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
         const Tile d = tile_info(t, off_s, ts_s, E);
         const bool both = d.nv > BH, two = d.nv > BN;
@@ -367,7 +380,6 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
         const uint32_t n0 = (uint32_t)(d.nh + 15) & ~15u, n1 = (uint32_t)(d.nv - d.nh + 15) & ~15u;
         const uint32_t i0 = idesc_mxf4(n0, 0), i1 = idesc_mxf4(n1, 0);
         constexpr uint32_t kUpper = (2u << 4) | (2u << 29);  // the scale words' upper halves
-        const bool far0 = n0 > 128u, far1 = n1 > 128u;
         const uint32_t d0 = tmem + h0 * BH, d1 = tmem + BH;
         if (!(ok = mbar_wait(&acc_empty[h0], acc.phase(h0) ^ 1u, abort, pb.err))) break;
         if (both && !two && !(ok = mbar_wait(&acc_empty[1], acc.phase(1) ^ 1u, abort, pb.err))) break;
@@ -376,20 +388,15 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
           if (two && ks == 0 && !(ok = mbar_wait(&acc_empty[1], acc.phase(1) ^ 1u, abort, pb.err))) break;
           tc_fence_after();
           const uint64_t so = (uint64_t)((s * kStageBytes) >> 4);
-          const uint64_t ad = adesc0 + so, bd = bdesc0 + so, sd = sdesc0 + so;
+          const uint64_t ad = adesc0 + so, bd = bdesc0 + so;
           const uint64_t bd1 = bd + (uint64_t)(kBHalfBytes >> 4);
-          const uint32_t sf = tmem + kSfCol + (g & 1u) * kSfSet;
-          // scales of 128-k atom a, then its two 64-k steps
+          const uint32_t sf = tmem + kSfCol + s * kSfSet;
+          // the two 64-k steps of 128-k scale atom a
           auto atom = [&](int a, bool second) __attribute__((always_inline)) {
-            tc_cp_scales(sf + a * 4, sd + a * 32);
-            tc_cp_scales(sf + 8 + a * 8, sd + 64 + a * 64);
-            if (far0) tc_cp_scales(sf + 8 + a * 8 + 4, sd + 64 + a * 64 + 32);
             tc_mma_mxf4(d0, ad + 4 * a, bd + 4 * a, i0, sf + a * 4, sf + 8 + a * 8, a > 0 || ks > 0);
             if (second)
               tc_mma_mxf4(d0, ad + 4 * a + 2, bd + 4 * a + 2, i0 | kUpper, sf + a * 4, sf + 8 + a * 8, 1u);
             if (two) {
-              tc_cp_scales(sf + 24 + a * 8, sd + 192 + a * 64);
-              if (far1) tc_cp_scales(sf + 24 + a * 8 + 4, sd + 192 + a * 64 + 32);
               tc_mma_mxf4(d1, ad + 4 * a, bd1 + 4 * a, i1, sf + a * 4, sf + 24 + a * 8, a > 0 || ks > 0);
               if (second)
                 tc_mma_mxf4(d1, ad + 4 * a + 2, bd1 + 4 * a + 2, i1 | kUpper, sf + a * 4,
@@ -415,89 +422,124 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
       tc_commit(mma_done);
       mbar_drain(mma_done, 0);
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp >= 4 && warp < 12) {
     // ---------------- scales ----------------
-    // thread i: weight row i and routed rows i, i + 128, i + 256 of the tile;
-    // loaded a stage ahead
-    const int i = (warp - 4) * 32 + lane;
-    const int spot = (i & 31) * 16 + (i >> 5) * 4;  // of row i among 128
+    // two groups of four warps take alternate stages: what bounds them is the
+    // instructions of one stage.  Thread i of a group loads the scales of weight
+    // row i and routed rows i, i + 128, i + 256 of the tile, two stages ahead;
+    // through shared memory every warp gets them all, since TMEM wants row r in
+    // lane r % 32, column r / 32 of each of the four 32-lane quarters, and a warp
+    // writes its own quarter.  (tcgen05.cp does the same from shared memory, but
+    // held up the MMAs behind it: 45 of 220 us at 8192 rows x 5760 x 2880.)
+    const int group = (warp - 4) >> 2, i = ((warp - 4) & 3) * 32 + lane;
     const uint2 ones = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
     const uint8_t* wp = nullptr;                    // the weight row's scales, or null
     const uint32_t* xp[3] = {nullptr, nullptr, nullptr};  // the routed rows' first words, or null
-    int at[3] = {0, 0, 0};                          // their places in the scale area
+    int at[3] = {0, 0, 0};                          // their places in the scale area, or -1
+    bool wide = false;
     const int KA = (KS + 3) / 4;                    // words of a routed row
-    auto open = [&](int64_t t) __attribute__((always_inline)) {
+    int64_t t = blockIdx.x;                         // stage to load: tile and step
+    int ks = 0;
+    auto open = [&]() __attribute__((always_inline)) {
       const Tile d = tile_info(t, off_s, ts_s, E);
+      wide = d.nv > BN;
       wp = d.n0 + i < N ? pb.ws + ((int64_t)d.e * N + d.n0 + i) * KS : nullptr;
 #pragma unroll
       for (int q = 0; q < 3; ++q) {
         int j = i + 128 * q, h = 0;
         bool on = j < d.nv;
-        if (d.nv > BN) {  // two MMAs: rows nh .. belong to the second half
+        if (wide) {  // two MMAs: rows nh .. belong to the second half
           h = j >= BH;
           if (h) j -= BH;
           on = j < (h ? d.nv - d.nh : d.nh);
         }
         xp[q] = on ? pb.xs + d.p0 + (h ? d.nh : 0) + j : nullptr;
-        at[q] = j < BN ? 1024 + h * 2048 + (j >> 7) * 512 + (j & 31) * 16 + ((j & 127) >> 5) * 4 : -1;
+        at[q] = j < BN ? h * BH + j : -1;
       }
     };
-    uint2 wv = ones, xv[3] = {ones, ones, ones};
-    auto get = [&](int ks) __attribute__((always_inline)) {
-      wv = wp ? load_scales(wp + 8 * ks, KS - 8 * ks, pb.wvec) : ones;
-#pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        xv[q] = ones;
-        if (xp[q]) {
-          xv[q].x = __ldg(xp[q] + (int64_t)(2 * ks) * pb.P);
-          if (2 * ks + 1 < KA) xv[q].y = __ldg(xp[q] + (int64_t)(2 * ks + 1) * pb.P);
-        }
-      }
-    };
-    int64_t t = blockIdx.x;
-    int ks = 0;
-    int to[3] = {0, 0, 0};  // places of the stage being written
-    if (t < ntiles) {
-      open(t);
-      get(0);
-    }
-    uint32_t s = 0, ph = 0;
-    while (t < ntiles) {
-      const uint2 w0 = wv, x0 = xv[0], x1 = xv[1], x2 = xv[2];
-#pragma unroll
-      for (int q = 0; q < 3; ++q) to[q] = at[q];
+    // the scales of the group's next stage, and where they go
+    uint2 w = ones, x[3] = {ones, ones, ones};
+    int to[3] = {0, 0, 0};
+    bool two = false, on = false;
+    auto step = [&]() __attribute__((always_inline)) {  // to the next stage
       if (++ks == NS) {
         ks = 0;
         t += gridDim.x;
-        if (t < ntiles) open(t);
+        if (t < ntiles) open();
       }
-      if (t < ntiles) get(ks);
-      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, abort, pb.err))) break;
-      uint8_t* sf = smem + s * kStageBytes + kABytes + 2 * kBHalfBytes;
-      *reinterpret_cast<uint32_t*>(sf + spot) = w0.x;
-      *reinterpret_cast<uint32_t*>(sf + spot + 512) = w0.y;
-      auto put = [&](int where, uint2 v) __attribute__((always_inline)) {
-        if (where >= 0) {
-          *reinterpret_cast<uint32_t*>(sf + where) = v.x;
-          *reinterpret_cast<uint32_t*>(sf + where + 1024) = v.y;
+    };
+    auto load = [&]() __attribute__((always_inline)) {
+      on = t < ntiles;
+      if (!on) return;
+      two = wide;
+      w = wp ? load_scales(wp + 8 * ks, KS - 8 * ks, pb.wvec) : ones;
+      const int64_t off = (int64_t)(2 * ks) * pb.P;
+      const bool second = 2 * ks + 1 < KA;
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        to[q] = at[q];
+        x[q] = ones;
+        if (xp[q]) {
+          x[q].x = __ldg(xp[q] + off);
+          if (second) x[q].y = __ldg(xp[q] + off + pb.P);
         }
-      };
-      put(to[0], x0);
-      put(to[1], x1);
-      put(to[2], x2);
-      fence_proxy_async();
+      }
+      step();
+      step();
+    };
+    uint32_t s = (uint32_t)group, ph = 0;
+    if (t < ntiles) open();
+    if (group) step();
+    load();
+    while (on) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, abort, pb.err))) break;
+      tc_fence_after();
+      // 8 bytes a row: 128 weight rows, then the routed rows
+      uint2* sf = reinterpret_cast<uint2*>(smem + s * kStageBytes + kABytes + 2 * kBHalfBytes);
+      sf[i] = w;
+      uint2* sb = sf + BM;
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        if (to[q] >= 0) sb[to[q]] = x[q];
+      const bool split = two;
+      load();
+      group_sync(group);
+      const uint32_t sc = tmem + (((uint32_t)warp & 3u) << 21) + kSfCol + s * kSfSet;
+      {
+        uint32_t r[8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint2 u = sf[c * 32 + lane];
+          r[c] = u.x;
+          r[4 + c] = u.y;
+        }
+        tmem_store_8(sc, r);
+      }
+      for (int h = 0; h < (split ? 2 : 1); ++h) {
+        uint32_t r[16];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          // of two MMAs each has at most 192 rows: columns 6 and 7 go unused
+          const uint2 u = !split ? sb[c * 32 + lane] : c < 6 ? sb[h * BH + c * 32 + lane] : ones;
+          r[c] = u.x;
+          r[8 + c] = u.y;
+        }
+        tmem_store_16(sc + 8 + h * 16, r);
+      }
+      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[s]);
-      if (++s == ST) { s = 0; ph ^= 1u; }
+      s += 2;
+      if (s >= ST) { s -= ST; ph ^= 1u; }
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 12) {
     // ---------------- epilogue ----------------
     // warp quarter q reads weight rows 32 q .. of the tile (TMEM lanes); the two
     // warps of a quarter take alternate 16-row pieces of the routed rows, turn
     // them over in shared memory and store 64-byte row segments
     const uint32_t q = (uint32_t)warp & 3u;
-    const int mine = (warp - 8) >> 2;
-    uint8_t* turn = smem + Smem::epi + (warp - 8) * kEpiBytes;
+    const int mine = (warp - 12) >> 2;
+    uint8_t* turn = smem + Smem::epi + (warp - 12) * kEpiBytes;
     uint16_t* put = reinterpret_cast<uint16_t*>(turn) + lane;
     const uint8_t* got = turn + (lane >> 2) * kEpiRow + (lane & 3) * 16;
     AccSched acc;
