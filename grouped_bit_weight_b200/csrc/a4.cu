@@ -123,7 +123,7 @@ constexpr int BH = 192;       // TMEM columns of an accumulator half
 constexpr int BT = 2 * BH;    // routed rows per tile
 constexpr int BN = 256;       // routed rows of one MMA at most (MMA N)
 constexpr int BKB = 128;      // bytes of codes per row and stage: 256 k
-constexpr int BOX = 64;       // routed rows per TMA box
+constexpr int BOX = 64;       // routed rows per TMA box, and twice that
 constexpr int ST = 3;         // ring stages
 constexpr int kThreads = 640;
 constexpr uint32_t kTmemCols = 512;
@@ -170,23 +170,34 @@ struct Tile {
 
 __device__ __forceinline__ int32_t row_tiles(int32_t cnt) { return (cnt + BT - 1) / BT; }
 
+// Tile t, for a caller whose tiles only grow: e is the expert of its last one
+// (0 at first).  The next is usually a few experts on.
 __device__ __forceinline__ Tile tile_info(int64_t t, const int32_t* off, const int32_t* ts,
-                                          int32_t E) {
-  int32_t lo = 0, hi = E - 1;
-  while (lo < hi) {
-    const int32_t mid = (lo + hi + 1) >> 1;
-    if (ts[mid] <= t) lo = mid; else hi = mid - 1;
+                                          int32_t E, int32_t& e) {
+  int tries = 0;
+  while (ts[e + 1] <= t && ++tries < 8) ++e;
+  if (ts[e + 1] <= t) {
+    int32_t lo = e, hi = E - 1;
+    while (lo < hi) {
+      const int32_t mid = (lo + hi + 1) >> 1;
+      if (ts[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    e = lo;
   }
-  const int32_t cnt = off[lo + 1] - off[lo];
+  const int32_t cnt = off[e + 1] - off[e];
   const int32_t rt = row_tiles(cnt);
-  const int32_t u = (int32_t)(t - ts[lo]);
-  const int32_t nt = u / rt, r = u - nt * rt;
-  // rows dealt evenly over the expert's row tiles, in sixteens
-  const int32_t per = ((cnt + rt - 1) / rt + 15) & ~15;
+  int32_t nt = (int32_t)(t - ts[e]), r = 0, per = cnt;
+  if (rt > 1) {
+    const int32_t u = nt;
+    nt = u / rt;
+    r = u - nt * rt;
+    // rows dealt evenly over the expert's row tiles, in sixteens
+    per = ((cnt + rt - 1) / rt + 15) & ~15;
+  }
   Tile d;
-  d.e = lo;
+  d.e = e;
   d.n0 = nt * BM;
-  d.p0 = off[lo] + r * per;
+  d.p0 = off[e] + r * per;
   d.nv = min(per, cnt - r * per);
   d.nh = d.nv <= BN ? d.nv : ((d.nv + 31) / 32) * 16;
   return d;
@@ -291,7 +302,7 @@ __device__ __forceinline__ uint2 load_scales(const uint8_t* p, int nvalid, int v
 
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
-               const __grid_constant__ CUtensorMap tmx) {
+               const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmx2) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -328,6 +339,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmw);
     tma_prefetch_desc(&tmx);
+    tma_prefetch_desc(&tmx2);
   }
   grid_dependency_wait();
   load_offsets_clamped(pb.offsets, E, pb.P, off_s, pb.err);
@@ -337,6 +349,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int64_t ntiles = ts_s[E];
+  int32_t at_e = 0;  // tile_info's place
 
   if (warp == 0) {
     // ---------------- codes: weights and routed rows ----------------
@@ -344,7 +357,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
       uint32_t g = 0;
       bool ok = true;
       for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
-        const Tile d = tile_info(t, off_s, ts_s, E);
+        const Tile d = tile_info(t, off_s, ts_s, E, at_e);
         const int b0 = (d.nh + BOX - 1) / BOX, b1 = (d.nv - d.nh + BOX - 1) / BOX;
         const uint32_t bytes = kABytes + (uint32_t)(b0 + b1) * (BOX * BKB);
         for (int ks = 0; ks < NS; ++ks, ++g) {
@@ -353,11 +366,13 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
           uint8_t* st = smem + s * kStageBytes;
           mbar_arrive_expect_tx(&full[s], bytes);
           tma_load_2d(st, &tmw, ks * BKB, (int32_t)((int64_t)d.e * N + d.n0), &full[s]);
-          for (int b = 0; b < b0; ++b)
-            tma_load_2d(st + kABytes + b * (BOX * BKB), &tmx, ks * BKB, d.p0 + b * BOX, &full[s]);
-          for (int b = 0; b < b1; ++b)
-            tma_load_2d(st + kABytes + kBHalfBytes + b * (BOX * BKB), &tmx, ks * BKB,
-                        d.p0 + d.nh + b * BOX, &full[s]);
+          auto rows = [&](uint8_t* dst, int p0, int n) __attribute__((always_inline)) {
+            for (; n >= 2; n -= 2, dst += 2 * BOX * BKB, p0 += 2 * BOX)
+              tma_load_2d(dst, &tmx2, ks * BKB, p0, &full[s]);
+            if (n) tma_load_2d(dst, &tmx, ks * BKB, p0, &full[s]);
+          };
+          rows(st + kABytes, d.p0, b0);
+          if (b1) rows(st + kABytes + kBHalfBytes, d.p0 + d.nh, b1);
         }
       }
       if (*abort)
@@ -374,7 +389,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
       const uint64_t adesc0 = make_sdesc_sw128(smem_u32(smem), 16, 1024);
       const uint64_t bdesc0 = make_sdesc_sw128(smem_u32(smem + kABytes), 16, 1024);
       for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
-        const Tile d = tile_info(t, off_s, ts_s, E);
+        const Tile d = tile_info(t, off_s, ts_s, E, at_e);
         const bool both = d.nv > BH, two = d.nv > BN;
         const uint32_t h0 = both ? 0u : acc.h;
         const uint32_t n0 = (uint32_t)(d.nh + 15) & ~15u, n1 = (uint32_t)(d.nv - d.nh + 15) & ~15u;
@@ -441,7 +456,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
     int64_t t = blockIdx.x;                         // stage to load: tile and step
     int ks = 0;
     auto open = [&]() __attribute__((always_inline)) {
-      const Tile d = tile_info(t, off_s, ts_s, E);
+      const Tile d = tile_info(t, off_s, ts_s, E, at_e);
       wide = d.nv > BN;
       wp = d.n0 + i < N ? pb.ws + ((int64_t)d.e * N + d.n0 + i) * KS : nullptr;
 #pragma unroll
@@ -545,7 +560,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
     AccSched acc;
     bool ok = true;
     for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
-      const Tile d = tile_info(t, off_s, ts_s, E);
+      const Tile d = tile_info(t, off_s, ts_s, E, at_e);
       const bool both = d.nv > BH, two = d.nv > BN;
       // this lane's 8 weight rows of a stored segment
       const int64_t n = d.n0 + (int64_t)(q * 32 + (lane & 3) * 8);
@@ -629,13 +644,17 @@ cudaError_t launch_gemm_a4(const uint8_t* xq, const uint8_t* xs, int64_t P, int6
   e = make_map_2d(&tmx, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, (uint64_t)K / 2, (uint64_t)P,
                   (uint64_t)K / 2, BKB, BOX, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
+  CUtensorMap tmx2;
+  e = make_map_2d(&tmx2, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, (uint64_t)K / 2, (uint64_t)P,
+                  (uint64_t)K / 2, BKB, 2 * BOX, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
   const A4Problem pb{reinterpret_cast<const uint32_t*>(xs), ws, P, K, N, E, offsets, out, err,
                      scale_vec(ws, K / 32)};
   constexpr size_t most = 1024 + Smem::tables + 8 * (1024 + 1);
   e = opt_in_smem<gemm_a4_kernel>(most);
   if (e != cudaSuccess) return e;
   const size_t smem = 1024 + Smem::tables + 8 * (size_t)(E + 1);
-  return launch_kernel<gemm_a4_kernel>(num_sms, kThreads, smem, s, true, pb, tmw, tmx);
+  return launch_kernel<gemm_a4_kernel>(num_sms, kThreads, smem, s, true, pb, tmw, tmx, tmx2);
 }
 
 }  // namespace gbw
