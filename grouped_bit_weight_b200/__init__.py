@@ -37,6 +37,9 @@ if not os.path.exists(LIB_PATH):
 
 lib = C.CDLL(LIB_PATH)
 
+# checks, allocations and calls of the entry points that take microseconds
+from . import _host  # noqa: E402
+
 MODE_AUTO, MODE_GEMM, MODE_GEMV = 0, 1, 2
 FLAG_OVERLAP_PREV = 0x100
 DEVERR_OFFSETS, DEVERR_TOKEN, DEVERR_TIMEOUT, DEVERR_ROUTE = 1, 2, 4, 8
@@ -87,6 +90,9 @@ class GbwError(RuntimeError):
         self.status = status
 
 
+_host.set_error(GbwError)
+
+
 def _check(status: int, where: str) -> None:
     if status != 0:
         raise GbwError(status, where)
@@ -129,24 +135,6 @@ def _on_device(where, **tensors):
         elif t.device != dev:
             raise ValueError(f"{where}: {name} is on {t.device}, expected {dev}")
     return dev
-
-
-def _call(where, fn, dev, *args):
-    """fn(*args, current stream of dev) with dev current; raises on a status.
-    The decode-sized calls take a few microseconds on the GPU, so the host's
-    part is kept short: the device is switched only when it is not current."""
-    i = dev.index
-    if torch.cuda.current_device() == i:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
-    if st != 0:
-        raise GbwError(st, where)
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
 
 
 _MODES = {"auto": MODE_AUTO, "gemm": MODE_GEMM, "gemv": MODE_GEMV}
@@ -432,83 +420,18 @@ class Routing(NamedTuple):
     slot_of_row: torch.Tensor     # [T * k] int32
 
 
-_LOGITS = {torch.bfloat16: LOGITS_BF16, torch.float32: LOGITS_FP32}
-
-
-def _logits(t, name, where):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _LOGITS:
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    _need(t, name, t.dtype)
-    if t.dim() != 2:
-        raise ValueError(f"{where}: {name} must be [T, E]")
-
-
 def gmoe_route(logits, k, renormalize=True):
     """Each token's k experts (largest logits, ties to the lowest index; NaN
     counts as -inf), their softmax weights (over the chosen experts, or over
     all with renormalize=False) and the plan of the routed rows, sorted by
     expert: a Routing.  logits [T, E] bf16 or fp32."""
-    where = "gmoe_route"
-    _logits(logits, "logits", where)
-    T, E = logits.shape
-    k = int(k)
-    if not 1 <= k <= min(E, 32):
-        raise ValueError(f"{where}: k={k} must be in 1 .. min(E={E}, 32)")
-    if T * k > 0x7FFFFFFF:
-        raise ValueError(f"{where}: T * k must be below 2^31")
-    dev = _on_device(where, logits=logits)
-    # one allocation for the six results: T * k entries each but the offsets
-    n = T * k
-    buf = torch.empty(5 * n + E + 1, dtype=torch.int32, device=dev)
-    parts = buf.split((n, n, n, n, n, E + 1))
-    r = Routing(parts[0].view(T, k), parts[1].view(torch.float32).view(T, k), parts[5], parts[2],
-                parts[3].view(T, k), parts[4])
-    need = lib.gmoe_route_workspace(T, E)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    at, step = buf.data_ptr(), 4 * n
-    _call(where, lib.gmoe_route, dev, logits.data_ptr(), _LOGITS[logits.dtype], T, E, k,
-          1 if renormalize else 0, at, at + step, at + 5 * step, at + 2 * step, at + 3 * step,
-          at + 4 * step, _at(ws), need)
-    return r
+    return Routing._make(_host.route(logits, k, renormalize))
 
 
 def gmoe_route_bwd(logits, topk_ids, topk_weights, dweights, renormalize=True):
     """dlogits [T, E] (in the logits' type) from dweights [T, k], the gradient
     of gmoe_route's topk_weights."""
-    where = "gmoe_route_bwd"
-    _logits(logits, "logits", where)
-    _need(topk_ids, "topk_ids", torch.int32)
-    _need(topk_weights, "topk_weights", torch.float32)
-    _need(dweights, "dweights", torch.float32)
-    T, E = logits.shape
-    k = topk_ids.shape[-1] if topk_ids.dim() == 2 else 0
-    for name, t in (("topk_ids", topk_ids), ("topk_weights", topk_weights),
-                    ("dweights", dweights)):
-        if tuple(t.shape) != (T, k) or not 1 <= k <= min(E, 32):
-            raise ValueError(f"{where}: {name} must be [T={T}, k], k in 1 .. min(E, 32)")
-    dev = _on_device(where, logits=logits, topk_ids=topk_ids, topk_weights=topk_weights,
-                     dweights=dweights)
-    out = torch.empty_like(logits)
-    _call(where, lib.gmoe_route_bwd, dev, logits.data_ptr(), _LOGITS[logits.dtype], T, E, k,
-          1 if renormalize else 0, topk_ids.data_ptr(), topk_weights.data_ptr(),
-          dweights.data_ptr(), out.data_ptr())
-    return out
-
-
-def _slots(where, y, row_of_slot, weights):
-    _need(y, "y", torch.bfloat16)
-    _need(row_of_slot, "row_of_slot", torch.int32)
-    if y.dim() != 2 or row_of_slot.dim() != 2:
-        raise ValueError(f"{where}: y must be [P, H] and row_of_slot [T, k]")
-    P, H = y.shape
-    T, k = row_of_slot.shape
-    if weights is not None:
-        _need(weights, "weights", torch.float32)
-        if tuple(weights.shape) != (T, k):
-            raise ValueError(f"{where}: weights must be [{T}, {k}]")
-    return P, H, T, k
+    return _host.route_bwd(logits, topk_ids, topk_weights, dweights, renormalize)
 
 
 def gmoe_combine(y, row_of_slot, weights=None, out=None):
@@ -516,18 +439,7 @@ def gmoe_combine(y, row_of_slot, weights=None, out=None):
     y [P, H] bf16 of each token back into one [T, H] bf16, summed in fp32 in
     slot order.  weights [T, k] fp32; None sums them unweighted (the routed
     rows' dx back into their tokens)."""
-    where = "gmoe_combine"
-    P, H, T, k = _slots(where, y, row_of_slot, weights)
-    if out is not None:
-        _need(out, "out", torch.bfloat16)
-        if tuple(out.shape) != (T, H):
-            raise ValueError(f"{where}: out must be [{T}, {H}]")
-    dev = _on_device(where, y=y, row_of_slot=row_of_slot, weights=weights, out=out)
-    if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    _call(where, lib.gmoe_combine, dev, y.data_ptr(), P, H, row_of_slot.data_ptr(), _at(weights),
-          T, k, out.data_ptr())
-    return out
+    return _host.combine(y, row_of_slot, weights, out)
 
 
 def gmoe_combine_bwd(dout, y, row_of_slot, slot_of_row, weights, dy=None):
@@ -535,81 +447,7 @@ def gmoe_combine_bwd(dout, y, row_of_slot, slot_of_row, weights, dy=None):
     gradient dout [T, H] bf16.  slot_of_row [P] int32 is the inverse of
     row_of_slot (gmoe_route gives both).  Rows that no slot names stay as they
     are in `dy`; a dy made here has zeros there when P exceeds T * k."""
-    where = "gmoe_combine_bwd"
-    P, H, T, k = _slots(where, y, row_of_slot, weights)
-    if weights is None:
-        raise ValueError(f"{where}: weights are needed")
-    _need(dout, "dout", torch.bfloat16)
-    _need(slot_of_row, "slot_of_row", torch.int32)
-    if tuple(dout.shape) != (T, H):
-        raise ValueError(f"{where}: dout must be [{T}, {H}]")
-    _numel(slot_of_row, "slot_of_row", P, where)
-    if dy is not None:
-        _need(dy, "dy", torch.bfloat16)
-        if tuple(dy.shape) != (P, H):
-            raise ValueError(f"{where}: dy must be [{P}, {H}]")
-    dev = _on_device(where, dout=dout, y=y, row_of_slot=row_of_slot, slot_of_row=slot_of_row,
-                     weights=weights, dy=dy)
-    if dy is None:
-        dy = torch.empty_like(y) if P <= T * k else torch.zeros_like(y)
-    dw = torch.empty((T, k), dtype=torch.float32, device=dev)
-    _call(where, lib.gmoe_combine_bwd, dev, dout.data_ptr(), y.data_ptr(), P, H,
-          row_of_slot.data_ptr(), slot_of_row.data_ptr(), weights.data_ptr(), T, k, dy.data_ptr(),
-          dw.data_ptr())
-    return dy, dw
-
-
-def _moe_layer(fn, where, x, rw, gu, gu_scale, dn, dn_scale, scale_dtype, sdiv, k, renormalize,
-               rb, out, workspace):
-    _need(x, "x", torch.bfloat16)
-    _need(rw, "router_w", torch.bfloat16)
-    _need(gu, "gate_up weights", torch.uint8)
-    _need(gu_scale, "gate_up scales", scale_dtype)
-    _need(dn, "down weights", torch.uint8)
-    _need(dn_scale, "down scales", scale_dtype)
-    if x.dim() != 2 or rw.dim() != 2 or gu.dim() < 3 or dn.dim() < 3:
-        raise ValueError(f"{where}: x must be [T, H], router_w [E, H] and the weights "
-                         "[E, rows, ...]")
-    T, H = x.shape
-    E, I2 = gu.shape[0], gu.shape[1]
-    I = I2 // 2
-    if T > 32:
-        raise ValueError(f"{where}: T={T}: the whole layer takes at most 32 tokens; use "
-                         "gmoe_route, the fused expert pass and gmoe_combine")
-    if I2 % 2 or dn.shape[0] != E or dn.shape[1] != H:
-        raise ValueError(f"{where}: gate_up must be [E, 2I, ...] and down [E, H={H}, ...]")
-    if tuple(rw.shape) != (E, H):
-        raise ValueError(f"{where}: router_w must be [{E}, {H}]")
-    if not 1 <= k <= min(E, 16):
-        raise ValueError(f"{where}: k={k} must be in 1 .. min(E={E}, 16)")
-    if not H or not I or H % 64 or I % 64:
-        raise ValueError(f"{where}: H={H} and I={I} must be positive multiples of 64")
-    _numel(gu, "gate_up weights", E * I2 * (H // 2), where)
-    _numel(gu_scale, "gate_up scales", E * I2 * (H // sdiv), where)
-    _numel(dn, "down weights", E * H * (I // 2), where)
-    _numel(dn_scale, "down scales", E * H * (I // sdiv), where)
-    if rb is not None:
-        _need(rb, "router_bias", torch.float32)
-        _numel(rb, "router_bias", E, where)
-    if out is not None:
-        _need(out, "out", torch.bfloat16)
-        if tuple(out.shape) != (T, H):
-            raise ValueError(f"{where}: out must be [{T}, {H}]")
-    need = lib.gmoe_layer_workspace(T, E, k, H, I)
-    if workspace is not None:
-        _need(workspace, "workspace", torch.uint8)
-        if workspace.numel() < need:
-            raise ValueError(f"{where}: workspace has {workspace.numel()} bytes, needs {need}")
-    dev = _on_device(where, x=x, router_w=rw, gu=gu, gu_scale=gu_scale, dn=dn, dn_scale=dn_scale,
-                     router_bias=rb, out=out, workspace=workspace)
-    if out is None:
-        out = torch.empty_like(x)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _call(where, fn, dev, x.data_ptr(), T, H, rw.data_ptr(), _at(rb), gu.data_ptr(),
-          gu_scale.data_ptr(), dn.data_ptr(), dn_scale.data_ptr(), E, I, k,
-          1 if renormalize else 0, out.data_ptr(), workspace.data_ptr(), workspace.numel())
-    return out
+    return _host.combine_bwd(dout, y, row_of_slot, slot_of_row, weights, dy)
 
 
 def gnf4_moe_layer(x, router_w, gu_packed, gu_absmax, dn_packed, dn_absmax, k, renormalize=True,
@@ -621,81 +459,33 @@ def gnf4_moe_layer(x, router_w, gu_packed, gu_absmax, dn_packed, dn_absmax, k, r
     weighted sum -> [T, H] bf16.  workspace: uint8, at least
     lib.gmoe_layer_workspace(T, E, k, H, I) bytes, 256-byte aligned; calls that
     may overlap need one each (allocated here when not given)."""
-    return _moe_layer(lib.gnf4_moe_layer, "gnf4_moe_layer", x, router_w, gu_packed, gu_absmax,
-                      dn_packed, dn_absmax, torch.float32, 64, k, renormalize, router_bias, out,
-                      workspace)
+    return _host.moe_layer(True, x, router_w, gu_packed, gu_absmax, dn_packed, dn_absmax, k,
+                           renormalize, router_bias, out, workspace)
 
 
 def gmxfp4_moe_layer(x, router_w, gu_blocks, gu_scales, dn_blocks, dn_scales, k, renormalize=True,
                      router_bias=None, out=None, workspace=None):
     """gnf4_moe_layer on MXFP4 experts (blocks [E, rows, K/32, 16], e8m0 scales
     [E, rows, K/32])."""
-    return _moe_layer(lib.gmxfp4_moe_layer, "gmxfp4_moe_layer", x, router_w, gu_blocks, gu_scales,
-                      dn_blocks, dn_scales, torch.uint8, 32, k, renormalize, router_bias, out,
-                      workspace)
+    return _host.moe_layer(False, x, router_w, gu_blocks, gu_scales, dn_blocks, dn_scales, k,
+                           renormalize, router_bias, out, workspace)
 
 
 def gmxfp4_quantize_rows(x, row_to_token=None, swiglu=False):
     """(codes [P, K/32, 16] uint8, scales [ceil(K/128), P, 4] uint8 e8m0): bf16
     rows in MXFP4, gathered through row_to_token [P] int32 when given; byte b of
-    scales[a, p] belongs to block 4 a + b of row p (127 past the last).  x [T, K]; with
-    swiglu x is a gate_up output [T, 2K] and silu(gate) * up is packed."""
-    where = "gmxfp4_quantize_rows"
-    _need(x, "x", torch.bfloat16)
-    if x.dim() != 2:
-        raise ValueError(f"{where}: x must be [T, {'2K' if swiglu else 'K'}]")
-    T, K = x.shape
-    if swiglu:
-        if K % 2:
-            raise ValueError(f"{where}: x must be [T, 2K]")
-        K //= 2
-    if K <= 0 or K % 32:
-        raise ValueError(f"{where}: K={K} must be a positive multiple of 32")
-    P = T
-    if row_to_token is not None:
-        _need(row_to_token, "row_to_token", torch.int32)
-        P = row_to_token.numel()
-        if P and not T:
-            raise ValueError(f"{where}: x has no rows")
-    dev = _on_device(where, x=x, row_to_token=row_to_token)
-    codes = torch.empty((P, K // 32, 16), dtype=torch.uint8, device=dev)
-    scales = torch.empty(((K + 127) // 128, P, 4), dtype=torch.uint8, device=dev)
-    _call(where, lib.gmxfp4_quantize_rows, dev, x.data_ptr(), T, K, _at(row_to_token), P,
-          1 if swiglu else 0, codes.data_ptr(), scales.data_ptr())
-    return codes, scales
+    scales[a, p] belongs to block 4 a + b of row p (127 past the last).
+    x [T, K]; with swiglu x is a gate_up output [T, 2K] and silu(gate) * up is
+    packed."""
+    return _host.quantize_rows(x, row_to_token, swiglu)
 
 
 def gmxfp4_grouped_gemm_a4(x_codes, x_scales, blocks, scales, expert_offsets, out=None):
     """out[P, N] bf16 = rows @ W_e^T per expert, both in MXFP4: x_codes
     [P, K/32, 16] and x_scales [ceil(K/128), P, 4] from gmxfp4_quantize_rows,
-    expert-sorted; blocks [E, N, K/32, 16] (or
-    [E, N, K/2]), scales [E, N, K/32]."""
-    where = "gmxfp4_grouped_gemm_a4"
-    _need(x_codes, "x_codes", torch.uint8)
-    _need(x_scales, "x_scales", torch.uint8)
-    _need(blocks, "packed weights", torch.uint8)
-    _need(scales, "scales", torch.uint8)
-    _need(expert_offsets, "expert_offsets", torch.int32)
-    if x_codes.dim() != 3 or x_codes.shape[2] != 16 or blocks.dim() < 3:
-        raise ValueError(f"{where}: x_codes must be [P, K/32, 16] and the weights [E, N, ...]")
-    P, K = x_codes.shape[0], x_codes.shape[1] * 32
-    E, N = blocks.shape[0], blocks.shape[1]
-    if K == 0 or tuple(x_scales.shape) != ((K + 127) // 128, P, 4):
-        raise ValueError(f"{where}: x_scales must be [{(K + 127) // 128}, {P}, 4]")
-    _numel(blocks, "packed weights", E * N * (K // 2), where)
-    _numel(scales, "scales", E * N * (K // 32), where)
-    _numel(expert_offsets, "expert_offsets", E + 1, where)
-    if out is not None:
-        _need(out, "out", torch.bfloat16)
-        if tuple(out.shape) != (P, N):
-            raise ValueError(f"{where}: out must be [{P}, {N}]")
-    dev = _on_device(where, x_codes=x_codes, x_scales=x_scales, blocks=blocks, scales=scales,
-                     expert_offsets=expert_offsets, out=out)
-    if out is None:
-        out = torch.empty((P, N), dtype=torch.bfloat16, device=dev)
-    _call(where, lib.gmxfp4_grouped_gemm_a4, dev, x_codes.data_ptr(), x_scales.data_ptr(), P, K,
-          blocks.data_ptr(), scales.data_ptr(), E, N, expert_offsets.data_ptr(), out.data_ptr())
-    return out
+    expert-sorted; blocks [E, N, K/32, 16] (or [E, N, K/2]), scales
+    [E, N, K/32]."""
+    return _host.grouped_gemm_a4(x_codes, x_scales, blocks, scales, expert_offsets, out)
 
 
 def device_status(device=None, clear=True) -> int:

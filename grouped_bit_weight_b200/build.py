@@ -1,20 +1,27 @@
-"""Builds libgbw.so (the sm_100a CUDA library) in-tree with nvcc.
+"""Builds libgbw.so (the sm_100a CUDA library) and _host.so (the Python module
+of its short calls) in-tree.
 
 Each .cu file compiles to its own object in parallel, then nvcc links the
-shared library next to this file.  No GPU is needed to build.
+shared library next to this file; g++ compiles the module against it and
+torch.  No GPU is needed to build.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgbw.so")
+HOST_SRC = os.path.join(CSRC, "host.cpp")
+HOST = os.path.join(HERE, "_host.so")
+HEADER = os.path.join(HERE, "..", "include", "gbw.h")
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -28,7 +35,7 @@ def _sources():
 
 def _deps():
     return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + [os.path.join(HERE, "..", "include", "gbw.h"), __file__])
+            + [HEADER, __file__])
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -51,8 +58,32 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def _host(force: bool) -> None:
+    """_host.so: against torch's headers, linked to libgbw.so beside it."""
+    deps = [HOST_SRC, HEADER, __file__]
+    if not force and os.path.exists(HOST) and all(
+            os.path.getmtime(d) <= os.path.getmtime(HOST) for d in deps):
+        return
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(NVCC) or NVCC)))
+    inc = [os.path.join(root, "include"), os.path.join(root, "include/torch/csrc/api/include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = HOST + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+           "-fvisibility=hidden", "-w", *(f"-I{d}" for d in inc),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", HOST_SRC,
+           "-o", tmp, f"-L{HERE}", "-l:libgbw.so", f"-L{os.path.join(root, 'lib')}", "-lc10",
+           "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {HOST_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, HOST)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
+        _host(force)
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=os.cpu_count() or 4) as ex:
@@ -63,6 +94,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _host(force)
     return LIB
 
 
