@@ -39,31 +39,31 @@
 
 namespace gbw {
 
-cudaError_t make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base,
-                        uint64_t d0, uint64_t d1, uint64_t pitch, uint32_t b0,
-                        uint32_t b1, CUtensorMapSwizzle sw);
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn get_encode_fn();
 
 namespace {
 
-constexpr int kWarps = 12;  // 168 registers a thread: nothing spills
-constexpr int kThreads = 32 * kWarps;
+constexpr int kWarps = 11;                 // that multiply; one more loads
+constexpr int kConsumers = 32 * kWarps;
+constexpr int kThreads = kConsumers + 32;
 constexpr int kMaxE = 1024;
 constexpr int kMaxP = 512;
 constexpr int kRows = 8;           // most rows of a group: rows of one expert that share a decode
 constexpr int CKB = 128;           // bytes per weight row and stage: 256 k
-constexpr int D = 4;               // stages per warp
-constexpr int kStage = 16 * CKB;   // 2 KB
-constexpr int kScStage = 512;      // scales of a stage: two 16-byte units per row
+constexpr int D = 3;               // stages per warp
+constexpr int kStage = 32 * CKB;   // 4 KB: 32 weight rows
 
 // Shared memory by address in the shared window (dynamic shared memory starts
 // at 1 KB).  The table lies at 64 KB: entry b of lane l at 65536 + b * 256 +
 // l * 4, so that one byte permute of a packed word gives the whole address.
 // The other half of each 256 bytes holds partial sums (kParts rows of 32
-// floats).  The warps' rings lie on both sides of it.  Everything stays within
-// the 196 KB carve-out, which leaves L1 60 KB: with the largest one its few
-// lines held up the loads of x.
+// floats).  The warps' rings lie on both sides of it.
 constexpr int kParts = 256;
-constexpr int kLowWarps = 7;
+constexpr int kLowWarps = 4;
 struct Smem {
   static constexpr int base = 1024;
   static constexpr int ids = base;               // [kMaxP] int
@@ -71,23 +71,22 @@ struct Smem {
   static constexpr int rows = wts + 4 * kMaxP;   // [kMaxP] uint16 slot of sorted row
   static constexpr int active = rows + 2 * kMaxP;  // [kMaxP] uint16 expert
   static constexpr int misc = active + 2 * kMaxP;  // 16 ints
-  static constexpr int share = misc + 64;          // [2] Share, 32 bytes apart
-  static constexpr int part = share + 64;          // [kWarps] scan parts
-  static constexpr int bars = part + 4 * kWarps;   // [kWarps][D] stage full
-  static constexpr int low_end = bars + 8 * kWarps * D;
+  static constexpr int shares = misc + 64;         // [4] Share, 32 bytes apart
+  static constexpr int bars = shares + 128;        // full and empty [kWarps][2][D], published [2]
+  static constexpr int low_end = bars + 8 * (2 * kWarps * D + 2);
   static constexpr int table = 65536;
   static constexpr int ring_low = table - kLowWarps * D * kStage;
   static constexpr int count = ring_low;  // [kMaxE] int: token bits, then first row (before the ring is used)
   static constexpr int ring_high = 2 * table;
-  static constexpr int scales = ring_high + (kWarps - kLowWarps) * D * kStage;
-  static constexpr int first = scales + kWarps * D * kScStage;  // [kMaxP + 4] int first sorted row
+  static constexpr int first = ring_high + (kWarps - kLowWarps) * D * kStage;  // [kMaxP + 4] int first sorted row
   static constexpr int e8m0 = first + 4 * (kMaxP + 4);  // [256] float (MXFP4)
-  static constexpr int end = e8m0 + 1024;
+  static constexpr int part = e8m0 + 1024;              // [kWarps + 1] scan parts
+  static constexpr int end = part + 64;
   static constexpr int bytes = end - base;  // dynamic
 };
 static_assert(Smem::low_end <= Smem::ring_low, "the small arrays fit below the rings");
 static_assert(Smem::ring_low + 4 * kMaxE <= Smem::table, "the expert counts fit the rings below");
-static_assert(Smem::end <= 196 * 1024, "shared memory within the 196 KB carve-out");
+static_assert(Smem::bytes <= 232448, "shared memory exceeds the 227 KB a CTA can have");
 
 struct LayerArgs {
   LayerProblem p;
@@ -220,21 +219,25 @@ __device__ __forceinline__ int ld_acquire(const int* p) {
   return v;
 }
 
-// 8 rows x 128 bytes of a packed matrix to shared address dst, 128B swizzle
-// (16-byte unit u of row r at u ^ r), counted in bytes on barrier `bar`.
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
+// 32 rows x 128 bytes of a packed matrix to shared address dst, 128B swizzle
+// (16-byte unit u of row r at u ^ (r & 7)), counted in bytes on barrier `bar`.
+// One box per stage: issuing a box takes about 130 cycles whatever its size (two
+// boxes of 1 KB per stage bound the whole kernel).
+__device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap* m, int x, int y, int z,
+                                         uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
 
-// One phase's share of this CTA, kept in shared memory: units [u0, u0 + n) of
-// nc chunks (256 k) each.  Warp w takes whole units w, w + 12, .. of the first
-// `whole` (a multiple of 12) and parts of the others, which are cut into
-// 1 << lgS parts each and joined through shared memory.
+// A share of one phase: units [u0, u0 + n) of nc chunks (256 k) each.  Warp w
+// takes whole units w, w + kWarps, .. of the first `whole` (a multiple of kWarps)
+// and parts of the others, which are cut into 1 << lgS parts each and joined
+// through shared memory.
 struct Share {
+  int phase;  // 0: gate_up, 1: down, 2: no more
   int u0, n, nc, whole, lgS;
   // Item `i` of warp w: chunks [c, c1) of unit u; false past the last.
   __device__ __forceinline__ bool item(int w, int i, int& u, int& c, int& c1) const {
@@ -249,6 +252,11 @@ struct Share {
     return u < n;
   }
 };
+
+// Barrier of the multiplying warps.
+__device__ __forceinline__ void consumer_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+}
 
 template <Fmt F, int NPL>
 __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, const int aligned,
@@ -272,14 +280,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
     raise_error(p.err, GBW_DEVERR_TIMEOUT);
     return;
   }
-  // misc: 0 claim A, 1 claim B, 2 next claim, 3 abort, 4 groups, 5 last of a tile,
-  // 6 rows of the largest expert
+  // misc: 0 claim A, 1 claim B, 2 shares begun, 3 abort, 4 groups, 5 last of a
+  // tile, 6 rows of the largest expert
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Smem::bars);
+  uint64_t* published = bars + 2 * kWarps * D;  // [2] share 0, 2, .. and 1, 3, .. is known
 
   {
     // a warp writes the 16 bytes of one high nibble: lane l holds level l & 15
     const uint32_t level = code_bf16<F>(lane & 15);
 #pragma unroll 1
-    for (int h = warp; h < 16; h += kWarps) {
+    for (int h = warp; h < 16; h += kWarps + 1) {
       const uint32_t top = __shfl_sync(0xffffffffu, level, h);
 #pragma unroll
       for (int l = 0; l < 16; ++l) {
@@ -294,15 +304,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
   }
   for (int e = threadIdx.x; e < E; e += kThreads) count[e] = 0;
   if (threadIdx.x == 0) {
-    misc[3] = misc[6] = 0;
+    misc[2] = misc[3] = misc[6] = 0;
     tma_prefetch_desc(&map_gu);
     tma_prefetch_desc(&map_dn);
   }
-  // a stage is full when its codes have landed and every lane's scales have
-  if (threadIdx.x < kWarps * D) {
-    mbar_init(reinterpret_cast<uint64_t*>(smem + Smem::bars) + threadIdx.x, 33);
-    fence_barrier_init();
-  }
+  for (int i = threadIdx.x; i < 2 * kWarps * D + 2; i += kThreads) mbar_init(bars + i, 1);
+  fence_barrier_init();
   __syncthreads();
   grid_dependency_wait();
   if (threadIdx.x >= kThreads - 2) {  // (a warp without a token, usually)
@@ -311,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
   }
 
   // ---- the choice of experts, the same in every CTA
-  for (int t = warp; t < T; t += kWarps) {
+  for (int t = warp; t < T; t += kWarps + 1) {
     int id = 0;
     float w = 0.0f;
     choose<LogitL2, NPL>(reinterpret_cast<const LogitL2*>(a.logits) + (int64_t)t * E, E, k, p.renorm,
@@ -381,128 +388,160 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
   __syncthreads();
   const int A = misc[4];  // groups
   const int G = gridDim.x;
-  int next_a = misc[0], next_b = misc[1];
-  const int tiles_a = I / 8, tiles_b = H / 16;
+  const int tiles_a = I / 16, tiles_b = H / 32;
 
   // Column tiles of 8: phase A, up to 8 rows of a group are one tile; phase B,
   // 4 rows a tile, the high parts of h in columns 0..3, the low ones in 4..7.
   const bool two_tiles = misc[6] > 4;  // some group has more than 4 rows
-  auto share = [&](int phase) __attribute__((always_inline)) -> const Share& {
-    return *reinterpret_cast<const Share*>(smem + Smem::share + phase * 32);
+  // The CTA's shares in order, in shared memory, four at a time.
+  auto share = [&](int i) __attribute__((always_inline)) -> Share* {
+    return reinterpret_cast<Share*>(smem + Smem::shares + (i & 3) * 32);
   };
-  // Share idx of a phase, by one thread; idx >= G: an empty one.
-  auto set_share = [&](int phase, int idx) __attribute__((always_inline)) {
-    Share* s = reinterpret_cast<Share*>(smem + Smem::share + phase * 32);
-    const int tiles = phase ? tiles_b : tiles_a;
-    // phase B, aligned: whole tiles, so that no tile is shared between CTAs
-    const int per = phase && aligned ? A : 1;
-    const unsigned total = (unsigned)(per > 1 ? tiles : tiles * A);
-    const unsigned q = total / (unsigned)G, r = total - q * (unsigned)G;
-    const int n = idx < G ? (int)(q + (idx < (int)r)) * per : 0, nc = ((phase ? I : H) + 255) >> 8;
-    // the split of the last units with the least work for the busiest warp, as
-    // far as the partial sums fit (4 rows for each column tile)
-    const int whole = n - n % kWarps;
-    const int rest = n - whole, rows4 = phase && two_tiles ? 8 : 4;
-    int lgS = 0, best = rest ? 8 : 0;  // eighths of a unit
-    for (int l = 1; l <= 3; ++l) {
-      if ((1 << l) <= nc && (rest << l) * rows4 <= kParts) {
-        const int cost = (((rest << l) + kWarps - 1) / kWarps) << (3 - l);
-        if (cost < best) { best = cost; lgS = l; }
-      }
-    }
-    s->u0 = (int)(q * idx + min((unsigned)idx, r)) * per;
-    s->n = n;
-    s->nc = nc;
-    s->whole = whole;
-    s->lgS = lgS;
-  };
-
   // (group, output tile) of unit u
   auto unit_of = [&](int phase, int u, int& ai, int& tile) __attribute__((always_inline)) {
     const int d = phase ? A : tiles_a, q = u / d, r = u - q * d;
     ai = phase ? r : q;
     tile = phase ? q : r;
   };
-
-  constexpr int kScChunk = F == Fmt::NF4 ? 16 : 8;       // scale bytes of a row and chunk
-  const int sr_a = F == Fmt::NF4 ? H / 16 : H / 32;      // scale bytes per row
-  const int sr_b = F == Fmt::NF4 ? I / 16 : I / 32;
-
-  // of row sc_row's scales this lane copies the first or second 16-byte unit
-  // that holds them
-  const int sc_row = lane >> 1, sc_unit = lane & 1;
-  auto row_skip = [&](int phase, int r) __attribute__((always_inline)) { return phase == 0 && r >= 8 ? I - 8 : 0; };
-
-  // This warp's place in its stream of chunks to load: item pc_item of phase
-  // pc_phase (-1: no more), its chunks [pc_c, pc_c1), its first matrix row; for
-  // this lane, the chunk's first scale in row sc_row and the bytes from there to
-  // the end of the scales.
-  int pc_phase = 0, pc_item = 0, pc_c = 0, pc_c1 = 0, pc_row = 0, pc_have = 0;
-  const uint8_t* pc_s = nullptr;
-  // Opens item pc_item.  Rows 8 .. 15 of a gate_up unit are the up rows, I - 8
-  // further.
-  auto enter = [&]() __attribute__((always_inline)) {
-    const Share& s = share(pc_phase);
-    int u, ai, tile;
-    if (!s.item(warp, pc_item, u, pc_c, pc_c1)) {
-      pc_item = -1;
-      return;
-    }
-    unit_of(pc_phase, s.u0 + u, ai, tile);
+  // A unit has 32 weight rows.  gate_up: 16 gate rows, then the 16 up rows of the
+  // same columns, I further; down: 32 rows in order.
+  auto first_row = [&](int phase, int ai, int tile) __attribute__((always_inline)) -> int {
     const int e = active[ai];
-    pc_row = pc_phase ? e * H + tile * 16 : e * 2 * I + tile * 8;
-    const int64_t sr = pc_phase ? sr_b : sr_a;
-    const int64_t off = (pc_row + sc_row + row_skip(pc_phase, sc_row)) * sr + pc_c * kScChunk;
-    pc_s = static_cast<const uint8_t*>(pc_phase ? p.dn_scale : p.gu_scale) + off;
-    const int64_t all = (pc_phase ? (int64_t)E * H : (int64_t)E * 2 * I) * sr;
-    pc_have = (int)min(all - off, (int64_t)1 << 30);
+    return phase ? e * H + tile * 32 : e * 2 * I + tile * 16;
   };
 
-  // this warp's ring and its barriers, as shared addresses
-  const uint32_t ring = warp < kLowWarps ? Smem::ring_low + warp * (D * kStage)
-                                         : Smem::ring_high + (warp - kLowWarps) * (D * kStage);
-  const uint32_t ring_s = Smem::scales + warp * (D * kScStage);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Smem::bars) + warp * D;
-
-  uint32_t q_in = 0, q_out = 0;  // chunks loaded and multiplied so far
-  // Loads the next chunk, codes and scales, into its ring slot.
-  auto issue = [&]() __attribute__((always_inline)) {
-    if (pc_item >= 0) {
-      const uint32_t slot = q_in & (D - 1);
-      if (lane == 0) {
-        const CUtensorMap* m = pc_phase ? &map_dn : &map_gu;
-        const uint32_t dst = ring + slot * kStage, bar = Smem::bars + (warp * D + slot) * 8;
-        mbar_arrive_expect_tx(&full[slot], kStage);
-        tma_box(dst, m, pc_c * CKB, pc_row, bar);
-        tma_box(dst + kStage / 2, m, pc_c * CKB, pc_row + (pc_phase ? 8 : I), bar);
+  if (warp == kWarps) {
+    // ---------------- loads: lane l feeds warp l's ring ----------------
+    const uint32_t ring = lane < kLowWarps ? Smem::ring_low + lane * (D * kStage)
+                                           : Smem::ring_high + (lane - kLowWarps) * (D * kStage);
+    uint64_t* full = bars + 2 * D * min(lane, kWarps - 1);
+    uint64_t* empty = full + D;
+    int known = 0;         // shares published
+    int kind = -1;         // phase of the last one; 2: no more
+    bool ended = lane >= kWarps;
+    int mine = -1;         // share this lane is at, its item and chunk
+    int item = 0, c = 0, c1 = 0;
+    int y = 0, z = 0;      // its box: row, and matrix (gate_up: [2 E] of I rows; down: one)
+    const CUtensorMap* map = nullptr;
+    bool busy = false;     // a chunk is waiting to be loaded
+    uint32_t q = 0, slot = 0, ph = 1;  // chunks loaded, next slot, its empty phase
+    uint32_t idle = 0;
+    uint64_t since = 0;
+    auto open = [&]() __attribute__((always_inline)) {
+      const Share& s = *share(mine);
+      int u, ai, tile;
+      busy = s.item(lane, item, u, c, c1);
+      if (busy) {
+        unit_of(s.phase, s.u0 + u, ai, tile);
+        const int e = active[ai];
+        y = s.phase ? e * H + tile * 32 : tile * 16;
+        z = s.phase ? 0 : 2 * e;
+        map = s.phase ? &map_dn : &map_gu;
       }
-      // the aligned units that the row's scales of this chunk lie in, as far as
-      // the array goes; past L1, whose few lines such small loads would fill
-      const int odd = (int)(reinterpret_cast<uintptr_t>(pc_s) & 15);
-      const int have = min(16, pc_have + odd - 16 * sc_unit);
-      if (have > 0 && odd + kScChunk > 16 * sc_unit)
-        cp_async_16_fill(ring_s + slot * kScStage + lane * 16, pc_s - odd + 16 * sc_unit, (uint32_t)have);
-      cp_async_arrive_noinc(&full[slot]);
-      pc_s += kScChunk;
-      pc_have -= kScChunk;
-      ++q_in;
-      if (++pc_c == pc_c1) {
-        ++pc_item;
-#pragma unroll 1
-        for (;;) {
-          enter();
-          if (pc_item >= 0 || pc_phase) break;
-          pc_phase = 1;
-          pc_item = 0;
+    };
+    for (;;) {
+      // a lane has loaded its last share, and the others have begun that one:
+      // claim the next (all of phase A before any of phase B)
+      if (kind != 2 && misc[2] >= known && __any_sync(0xffffffffu, !ended && !busy && mine + 1 == known)) {
+        int idx = 0;
+        if (kind < 0) {
+          kind = 0;
+          idx = misc[0];
+        } else if (kind == 0) {
+          if (lane == 0) idx = atomicAdd(&a.counters[0], 1);
+          idx = __shfl_sync(0xffffffffu, idx, 0);
+        } else {
+          if (lane == 0) idx = atomicAdd(&a.counters[1], 1);
+          idx = __shfl_sync(0xffffffffu, idx, 0);
+        }
+        if (kind == 0 && idx >= G) {
+          kind = 1;
+          idx = misc[1];
+        }
+        if (idx >= G) kind = 2;
+        if (lane == 0) {
+          Share* s = share(known);
+          s->phase = kind;
+          s->n = 0;
+          if (kind < 2) {
+            const int tiles = kind ? tiles_b : tiles_a;
+            // phase B, aligned: whole tiles, so that no tile is shared between CTAs
+            const int per = kind && aligned ? A : 1;
+            const unsigned total = (unsigned)(per > 1 ? tiles : tiles * A);
+            const unsigned each = total / (unsigned)G, r = total - each * (unsigned)G;
+            const int n = (int)(each + (idx < (int)r)) * per, nc = ((kind ? I : H) + 255) >> 8;
+            // the split of the last units with the least work for the busiest
+            // warp, as far as the partial sums fit (8 rows for each column tile)
+            const int whole = n - n % kWarps;
+            const int rest = n - whole, rows4 = kind && two_tiles ? 16 : 8;
+            int lgS = 0, best = rest ? 8 : 0;  // eighths of a unit
+            for (int l = 1; l <= 3; ++l) {
+              if ((1 << l) <= nc && (rest << l) * rows4 <= kParts) {
+                const int cost = (((rest << l) + kWarps - 1) / kWarps) << (3 - l);
+                if (cost < best) { best = cost; lgS = l; }
+              }
+            }
+            s->u0 = (int)(each * idx + min((unsigned)idx, r)) * per;
+            s->n = n;
+            s->nc = nc;
+            s->whole = whole;
+            s->lgS = lgS;
+          }
+          mbar_arrive(&published[known & 1]);
+        }
+        ++known;
+        __syncwarp();
+      }
+      if (!ended && !busy && mine + 1 < known) {
+        ++mine;
+        item = 0;
+        if (share(mine)->phase == 2) ended = true;
+        else open();
+      }
+      if (__all_sync(0xffffffffu, ended)) break;
+      bool went = false;
+      if (busy) {
+        if (mbar_test(&empty[slot], ph)) {
+          mbar_arrive_expect_tx(&full[slot], kStage);
+          tma_box3(ring + slot * kStage, map, c * CKB, y, z, smem_u32(&full[slot]));
+          ++q;
+          if (++slot == D) { slot = 0; ph ^= 1u; }
+          went = true;
+          if (++c == c1) {
+            ++item;
+            open();
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, went)) {
+        idle = 0;
+        since = 0;
+      } else if ((++idle & 1023u) == 0) {
+        if (misc[3]) break;
+        if (!since) since = globaltimer_ns();
+        if (globaltimer_ns() - since > kWaitLimitNs) {
+          misc[3] = 1;
+          raise_error(p.err, GBW_DEVERR_TIMEOUT);
+          break;
         }
       }
     }
-  };
+    if (misc[3] && lane < kWarps)  // let the loads in flight land
+      for (uint32_t i = q > D ? q - D : 0; i < q; ++i) mbar_drain(&full[i % D], (i / D) & 1u);
+    return;
+  }
 
+  // ---------------- the multiplying warps ----------------
   const int g = lane >> 2, t4 = lane & 3;
   const uint32_t lut = Smem::table | (uint32_t)lane * 4u;
+  const uint32_t ring = warp < kLowWarps ? Smem::ring_low + warp * (D * kStage)
+                                         : Smem::ring_high + (warp - kLowWarps) * (D * kStage);
+  uint64_t* full = bars + 2 * D * warp;
+  uint64_t* empty = full + D;
+  uint32_t slot = 0, ph = 0;  // of the next chunk to multiply
 
-  constexpr int kSecond = F == Fmt::NF4 ? 8 : 32;  // distance of a lane's second 8 k
+  constexpr int kSecond = F == Fmt::NF4 ? 8 : 32;        // distance of a lane's second 8 k
+  constexpr int kScChunk = F == Fmt::NF4 ? 16 : 8;       // scale bytes of a row and chunk
 
   // This lane's column in column tile i of a group (r0, cnt), at its first k of
   // a stage.  Columns past the group's rows repeat its last row; nothing reads
@@ -518,58 +557,29 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
     x0 = *reinterpret_cast<const uint4*>(xp);
     x1 = *reinterpret_cast<const uint4*>(xp + kSecond);
   };
-  // Weight fragments of block b of a stage: the lane's 16 weights of rows pg and
-  // pg + 8.  NF4, one scale block: bytes 8 t4 .. of its 32; MXFP4, two blocks of
+  // Weight fragments of block b of one of a stage's two halves of 16 rows: the
+  // lane's 16 weights of mma rows g and g + 8.  gate_up: gate rows 8 m + pg with
+  // the up rows of the same columns 16 rows further; down: rows 16 m + pg and 8
+  // further.  NF4, one scale block: bytes 8 t4 .. of its 32; MXFP4, two blocks of
   // 16 bytes: 4 bytes of each, so that every mma stays inside a scale block.
   // `st` is this lane's address in block 0; the blocks differ in address bits 5
-  // and 6 alone.  The mma's row g is row pg of the eight: with that order the
-  // swizzle spreads every access over all banks.
+  // and 6 alone.  Mma row g is row pg of eight: with that order the swizzle
+  // spreads every access over all banks.
   const int pg = F == Fmt::NF4 ? (g & 3) * 2 + (g >> 2) : g;
   const uint32_t get_w = ring + pg * CKB + (F == Fmt::NF4 ? ((t4 >> 1) ^ pg) * 16 + (t4 & 1) * 8
                                                           : pg * 16 + t4 * 4);
-  // Scales of rows pg and pg + 8: 32 bytes a row in a stage, the first at the low
-  // four bits of its address in the array.
-  const uint32_t get_s = ring_s + pg * 32;
-  auto scale_at = [&](int phase, int ai, int tile, int r) __attribute__((always_inline)) -> uint32_t {
-    const int e = active[ai];
-    const unsigned row = phase ? (unsigned)e * H + tile * 16 + r
-                               : (unsigned)e * 2 * I + tile * 8 + r + row_skip(phase, r);
-    return row * (unsigned)(phase ? sr_b : sr_a);
-  };
-  // The scales of a chunk for this lane: NF4, the fp32 absmax of block b is read
-  // when it is needed; MXFP4, lane t4 of a row converts the two bytes of block
-  // t4, and the others get them by shuffle.
-  struct Scales {
-    const uint8_t *g, *h;   // NF4: rows pg and pg + 8
-    float g0, g1, h0, h1;   // MXFP4: block t4, its two halves
-  };
-  auto scales_of = [&](uint32_t slot, uint32_t og, uint32_t oh) __attribute__((always_inline)) -> Scales {
-    Scales v;
-    v.g = smem + get_s + slot * kScStage + (og & 15u);
-    v.h = smem + get_s + slot * kScStage + 8 * 32 + (oh & 15u);
-    if (F == Fmt::MXFP4) {
-      const uint32_t a0 = *reinterpret_cast<const uint16_t*>(v.g + 2 * t4);
-      const uint32_t a1 = *reinterpret_cast<const uint16_t*>(v.h + 2 * t4);
-      auto f = [&](uint32_t b) { return *reinterpret_cast<const float*>(smem + Smem::e8m0 + b * 4); };
-      v.g0 = f(a0 & 255u);
-      v.g1 = f(a0 >> 8);
-      v.h0 = f(a1 & 255u);
-      v.h1 = f(a1 >> 8);
-    }
-    return v;
-  };
-  auto decode = [&](uint32_t st, int b, uint32_t (&fa)[8], uint32_t (&fb)[8]) __attribute__((always_inline)) {
+  auto decode = [&](uint32_t st, int b, int far, uint32_t (&fa)[8], uint32_t (&fb)[8]) __attribute__((always_inline)) {
     uint2 wa, wb;
     const uint8_t* at = smem + (st ^ (b * 32));
     if (F == Fmt::NF4) {
       wa = *reinterpret_cast<const uint2*>(at);
-      wb = *reinterpret_cast<const uint2*>(at + 8 * CKB);
+      wb = *reinterpret_cast<const uint2*>(at + far);
     } else {
       const uint8_t* au = smem + (st ^ (b * 32 + 16));
       wa.x = *reinterpret_cast<const uint32_t*>(at);
       wa.y = *reinterpret_cast<const uint32_t*>(au);
-      wb.x = *reinterpret_cast<const uint32_t*>(at + 8 * CKB);
-      wb.y = *reinterpret_cast<const uint32_t*>(au + 8 * CKB);
+      wb.x = *reinterpret_cast<const uint32_t*>(at + far);
+      wb.y = *reinterpret_cast<const uint32_t*>(au + far);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -578,6 +588,38 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
       fa[i] = lds_table(prmt(i < 4 ? wa.x : wa.y, lut, sel));
       fb[i] = lds_table(prmt(i < 4 ? wb.x : wb.y, lut, sel));
     }
+  };
+  // Scales of a chunk: lane t4 of a row holds those of block t4 (of its four mma
+  // rows), loaded a chunk ahead; the others get them by shuffle.
+  using Raw = uint32_t[4];  // [half m][row g, g + 8]; NF4: fp32 bits; MXFP4: two e8m0 bytes
+  auto scale_ptr = [&](int phase, int ai, int tile, int c) __attribute__((always_inline)) -> const uint8_t* {
+    const int64_t sr = F == Fmt::NF4 ? (phase ? I : H) / 16 : (phase ? I : H) / 32;
+    return static_cast<const uint8_t*>(phase ? p.dn_scale : p.gu_scale) +
+           (first_row(phase, ai, tile) + pg) * sr + c * kScChunk + t4 * (kScChunk / 4);
+  };
+  // `next`, `far`: from row pg to the second half's, and to row g + 8's, in bytes
+  auto load_scales = [&](const uint8_t* sp, int next, int64_t far, bool on, Raw& v) __attribute__((always_inline)) {
+    if (on) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const uint8_t* at = sp + (m ? next : 0);
+        if (F == Fmt::NF4) {
+          v[2 * m] = __ldg(reinterpret_cast<const uint32_t*>(at));
+          v[2 * m + 1] = __ldg(reinterpret_cast<const uint32_t*>(at + far));
+        } else {
+          v[2 * m] = __ldg(reinterpret_cast<const uint16_t*>(at));
+          v[2 * m + 1] = __ldg(reinterpret_cast<const uint16_t*>(at + far));
+        }
+      }
+    }
+  };
+  struct Scales {
+    float g0, g1, h0, h1;  // mma rows g, g + 8; MXFP4: the two halves of the block
+  };
+  auto scales_of = [&](uint32_t v0, uint32_t v1) __attribute__((always_inline)) -> Scales {
+    if (F == Fmt::NF4) return {__uint_as_float(v0), 0.0f, __uint_as_float(v1), 0.0f};
+    auto f = [&](uint32_t b) { return *reinterpret_cast<const float*>(smem + Smem::e8m0 + b * 4); };
+    return {f(v0 & 255u), f((v0 >> 8) & 255u), f(v1 & 255u), f((v1 >> 8) & 255u)};
   };
   // acc += block b times the lane's x
   auto mma_block = [&](float (&acc)[4], const uint32_t (&fa)[8], const uint32_t (&fb)[8],
@@ -594,15 +636,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
         else
           mma16816(d, fa[2 * m], fb[2 * m], fa[2 * m + 1], fb[2 * m + 1], xb[2 * m], xb[2 * m + 1]);
       }
-      float fg, fh;
-      if (F == Fmt::NF4) {
-        fg = *reinterpret_cast<const float*>(v.g + 4 * b);
-        fh = *reinterpret_cast<const float*>(v.h + 4 * b);
-      } else {
-        const int from = (lane & 28) | b;
-        fg = __shfl_sync(0xffffffffu, m0 ? v.g1 : v.g0, from);
-        fh = __shfl_sync(0xffffffffu, m0 ? v.h1 : v.h0, from);
-      }
+      const int from = (lane & 28) | b;
+      const float fg = __shfl_sync(0xffffffffu, m0 ? v.g1 : v.g0, from);
+      const float fh = __shfl_sync(0xffffffffu, m0 ? v.h1 : v.h0, from);
       acc[0] = fmaf(d[0], fg, acc[0]);
       acc[1] = fmaf(d[1], fg, acc[1]);
       acc[2] = fmaf(d[2], fh, acc[2]);
@@ -610,37 +646,44 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
     }
   };
 
-  // Waits for the chunk to multiply; its ring slot.
+  // Waits for the chunk to multiply; this lane's address in its stage.
   auto wait_stage = [&]() __attribute__((always_inline)) -> uint32_t {
-    const uint32_t slot = q_out & (D - 1);
-    mbar_wait(&full[slot], (q_out / D) & 1u, &misc[3], p.err);
-    ++q_out;
-    return slot;
+    mbar_wait(&full[slot], ph, &misc[3], p.err);
+    return get_w + slot * kStage;
   };
-  // Before a stage may be loaded again: what was read of it has been used (the
-  // sums wait for it), by every lane.
-  auto release = [&](float (&acc)[4]) __attribute__((always_inline)) {
+  // The stage may be loaded again: what was read of it has been used (the sums
+  // wait for it), by every lane.
+  auto used = [&](float (&acc)[4]) __attribute__((always_inline)) {
     asm volatile("" : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3]) : : "memory");
+  };
+  auto release = [&]() __attribute__((always_inline)) {
     __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[slot]);
+    if (++slot == D) { slot = 0; ph ^= 1u; }
   };
   // One column tile, the `nb` blocks of one chunk: x holds the columns of its
-  // first two blocks; at the end those at nsrc, the next ones the warp needs.
-  auto step_one = [&](uint4 (&x)[2][2], const uint16_t* src, int nb, const uint16_t* nsrc, int nnb,
-                      uint32_t og, uint32_t oh, float (&acc)[4]) __attribute__((always_inline)) {
-    issue();
+  // first two blocks, raw its scales; at the end those of the chunk after it,
+  // whose columns are at nsrc and scales at nsp.
+  auto step_one = [&](int phase, uint4 (&x)[2][2], Raw& raw, const uint16_t* src, int nb,
+                      const uint16_t* nsrc, const uint8_t* nsp, int next, int64_t far, int nnb,
+                      float (&acc)[2][4]) __attribute__((always_inline)) {
     uint4 y[2][2];
     auto load_cols = [&](uint4 (&v)[2][2], const uint16_t* from, int n) __attribute__((always_inline)) {
       if (n > 0) load_x(from, v[0][0], v[0][1]);
       if (n > 1) load_x(from + 64, v[1][0], v[1][1]);
     };
     load_cols(y, src + 128, nb - 2);
-    const uint32_t slot = wait_stage();
-    const uint32_t st = get_w + slot * kStage;
-    const Scales sc = scales_of(slot, og, oh);
+    const Scales sc[2] = {scales_of(raw[0], raw[1]), scales_of(raw[2], raw[3])};
+    load_scales(nsp, next, far, t4 < nnb, raw);
+    const uint32_t st = wait_stage();
+    const int half = phase ? 16 * CKB : 8 * CKB, other = phase ? 8 * CKB : 16 * CKB;
     auto block = [&](int b, const uint4 (&v)[2]) __attribute__((always_inline)) {
-      uint32_t fa[8], fb[8];
-      decode(st, b, fa, fb);
-      mma_block(acc, fa, fb, v[0], v[1], sc, b);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        uint32_t fa[8], fb[8];
+        decode(st + (m ? half : 0), b, other, fa, fb);
+        mma_block(acc[m], fa, fb, v[0], v[1], sc[m], b);
+      }
     };
     if (nb >= 4) {
       block(0, x[0]);
@@ -654,15 +697,17 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
       load_cols(x, nsrc, nnb);
       if (nb > 2) block(2, y[0]);
     }
-    release(acc);
+    used(acc[0]);
+    used(acc[1]);
+    release();
   };
   // Phase B, two column tiles: the columns are loaded a block ahead.
-  auto step_two = [&](uint4 (&x)[2][2][2], const uint16_t* s0, const uint16_t* s1, int left, uint32_t og,
-                      uint32_t oh, float (&acc)[2][4]) __attribute__((always_inline)) {
-    issue();
-    const uint32_t slot = wait_stage();
-    const uint32_t st = get_w + slot * kStage;
-    const Scales sc = scales_of(slot, og, oh);
+  auto step_two = [&](uint4 (&x)[2][2][2], Raw& raw, const uint16_t* s0, const uint16_t* s1, int left,
+                      const uint8_t* nsp, int next, int64_t far, int nnb,
+                      float (&acc)[2][2][4]) __attribute__((always_inline)) {
+    const Scales sc[2] = {scales_of(raw[0], raw[1]), scales_of(raw[2], raw[3])};
+    load_scales(nsp, next, far, t4 < nnb, raw);
+    const uint32_t st = wait_stage();
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       if (b < left) {
@@ -670,19 +715,26 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
           load_x(s0 + b * 64 + 64, x[(b + 1) & 1][0][0], x[(b + 1) & 1][0][1]);
           load_x(s1 + b * 64 + 64, x[(b + 1) & 1][1][0], x[(b + 1) & 1][1][1]);
         }
-        uint32_t fa[8], fb[8];
-        decode(st, b, fa, fb);
-        mma_block(acc[0], fa, fb, x[b & 1][0][0], x[b & 1][0][1], sc, b);
-        mma_block(acc[1], fa, fb, x[b & 1][1][0], x[b & 1][1][1], sc, b);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          uint32_t fa[8], fb[8];
+          decode(st + m * 16 * CKB, b, 8 * CKB, fa, fb);
+          mma_block(acc[0][m], fa, fb, x[b & 1][0][0], x[b & 1][0][1], sc[m], b);
+          mma_block(acc[1][m], fa, fb, x[b & 1][1][0], x[b & 1][1][1], sc[m], b);
+        }
       }
     }
-    release(acc[0]);
-    release(acc[1]);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      used(acc[0][m]);
+      used(acc[1][m]);
+    }
+    release();
   };
 
   constexpr float kUnscale = F == Fmt::NF4 ? 1.0f / kLevelScale : 1.0f;
-  // Writes one column tile of a finished unit: h (phase A) or y (phase B).
-  auto finish = [&](int phase, const float (&d)[4], int cnt, int r0, int tile, int nt) __attribute__((always_inline)) {
+  // Writes half m of one column tile of a finished unit: h (phase A) or y (B).
+  auto finish = [&](int phase, const float (&d)[4], int cnt, int r0, int tile, int nt, int m) __attribute__((always_inline)) {
     if (phase == 0) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -695,8 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
           // an infinite high part keeps a zero low part (inf - inf is NaN)
           const float low = h - __bfloat162float(hi);
           const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(low) ? low : 0.0f);
-          a.hhi[(int64_t)slot * I + tile * 8 + pg] = __bfloat16_as_ushort(hi);
-          a.hlo[(int64_t)slot * I + tile * 8 + pg] = __bfloat16_as_ushort(lo);
+          a.hhi[(int64_t)slot * I + tile * 16 + m * 8 + pg] = __bfloat16_as_ushort(hi);
+          a.hlo[(int64_t)slot * I + tile * 16 + m * 8 + pg] = __bfloat16_as_ushort(lo);
         }
       }
     } else {
@@ -708,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
       for (int j = 0; j < 2; ++j) {
         const int c = nt * 4 + 2 * t4 + j;
         if (t4 < 2 && c < cnt) {
-          float* y = a.y + (int64_t)rows[r0 + c] * H + tile * 16 + pg;
+          float* y = a.y + (int64_t)rows[r0 + c] * H + tile * 32 + m * 16 + pg;
           y[0] = v[j] * kUnscale;
           y[8] = v[2 + j] * kUnscale;
         }
@@ -717,44 +769,52 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
   };
 
   float* parts = reinterpret_cast<float*>(smem + Smem::table + 128);  // row i at i * 64
-  // A phase's share: this warp's items, then the units cut into parts, joined.
-  auto run_share = [&](int phase) __attribute__((always_inline)) {
-    const Share& s = share(phase);
+  // A share: this warp's items, then the units cut into parts, joined.
+  auto run_share = [&](const Share& s) __attribute__((always_inline)) {
+    const int phase = s.phase;
     const int nbk = (phase ? I : H) >> 6;  // blocks of a unit
+    const int64_t sr = F == Fmt::NF4 ? (phase ? I : H) / 16 : (phase ? I : H) / 32;
+    const int64_t far = (phase ? 8 : I) * sr;
+    const int next = (int)((phase ? 16 : 8) * sr);
     const bool wide = phase && two_tiles;
-    const int rows4 = wide ? 8 : 4;        // part rows of an item
+    const int rows4 = wide ? 16 : 8;       // part rows of an item
     int item = 0, u, c, c1;
     if (s.item(warp, 0, u, c, c1)) {
       uint4 x[2][2];
+      Raw raw = {0, 0, 0, 0};
       const uint16_t* src = nullptr;
+      const uint8_t* sp = nullptr;
 #pragma unroll 1
       for (;;) {
         int ai, tile;
         unit_of(phase, s.u0 + u, ai, tile);
         const int r0 = first[ai], cnt = first[ai + 1] - r0;
-        const uint32_t og = scale_at(phase, ai, tile, pg), oh = scale_at(phase, ai, tile, pg + 8);
-        // the columns of the item after this one, to be loaded with its last chunk
+        // the columns and scales of the item after this one, loaded with its
+        // last chunk
         int nu, nc0, nc1, nai, ntile;
         const bool more = s.item(warp, item + 1, nu, nc0, nc1);
         unit_of(phase, s.u0 + (more ? nu : u), nai, ntile);
         const uint16_t* nsrc = column(phase, first[nai], first[nai + 1] - first[nai], 0) + nc0 * 256;
+        const uint8_t* nsp = scale_ptr(phase, nai, ntile, nc0);
         const int nnb = more ? nbk - nc0 * 4 : 0;
         if (item == 0) {
           src = column(phase, r0, cnt, 0) + c * 256;
+          sp = scale_ptr(phase, ai, tile, c);
+          load_scales(sp, next, far, t4 < nbk - c * 4, raw);
           if (!wide) {
             load_x(src, x[0][0], x[0][1]);
             if (nbk - c * 4 > 1) load_x(src + 64, x[1][0], x[1][1]);
           }
         }
-        float acc[2][4];
+        float acc[2][2][4];  // [column tile][half]
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[0][j] = acc[1][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) acc[0][0][j] = acc[0][1][j] = acc[1][0][j] = acc[1][1][j] = 0.0f;
         if (!wide) {
 #pragma unroll 1
-          for (; c < c1; ++c, src += 256) {
+          for (; c < c1; ++c, src += 256, sp += kScChunk) {
             const bool last = c + 1 == c1;
-            step_one(x, src, nbk - c * 4, last ? nsrc : src + 256, last ? nnb : nbk - c * 4 - 4,
-                     og + c * kScChunk, oh + c * kScChunk, acc[0]);
+            step_one(phase, x, raw, src, nbk - c * 4, last ? nsrc : src + 256,
+                     last ? nsp : sp + kScChunk, next, far, last ? nnb : nbk - c * 4 - 4, acc[0]);
           }
         } else {
           const uint16_t* src1 = column(1, r0, cnt, cnt > 4 ? 1 : 0) + c * 256;
@@ -762,21 +822,31 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
           load_x(src, y[0][0][0], y[0][0][1]);
           load_x(src1, y[0][1][0], y[0][1][1]);
 #pragma unroll 1
-          for (; c < c1; ++c, src += 256, src1 += 256)
-            step_two(y, src, src1, c + 1 < c1 ? nbk - c * 4 : min(4, nbk - c * 4),
-                     og + c * kScChunk, oh + c * kScChunk, acc);
+          for (; c < c1; ++c, src += 256, src1 += 256, sp += kScChunk) {
+            const bool last = c + 1 == c1;
+            step_two(y, raw, src, src1, last ? min(4, nbk - c * 4) : nbk - c * 4,
+                     last ? nsp : sp + kScChunk, next, far, last ? nnb : nbk - c * 4 - 4, acc);
+          }
         }
         if (u < s.whole || s.lgS == 0) {
-          finish(phase, acc[0], cnt, r0, tile, 0);
-          if (wide && cnt > 4) finish(1, acc[1], cnt, r0, tile, 1);
+          finish(phase, acc[0][0], cnt, r0, tile, 0, 0);
+          finish(phase, acc[0][1], cnt, r0, tile, 0, 1);
+          if (wide && cnt > 4) {
+            finish(1, acc[1][0], cnt, r0, tile, 1, 0);
+            finish(1, acc[1][1], cnt, r0, tile, 1, 1);
+          }
         } else {
           // the part's place among the parts of the split units
           float* to = parts + (warp + item * kWarps - s.whole) * rows4 * 64 + lane;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) to[j * 64] = acc[0][j];
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) to[(m * 4 + j) * 64] = acc[0][m][j];
           if (wide)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) to[(4 + j) * 64] = acc[1][j];
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) to[(8 + m * 4 + j) * 64] = acc[1][m][j];
         }
         if (!more) break;
         ++item;
@@ -784,33 +854,32 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
         c = nc0;
         c1 = nc1;
         src = nsrc;
+        sp = nsp;
       }
     }
     if (s.lgS) {
-      __syncthreads();
-      const int uj = s.whole + warp;  // fewer than kWarps units are split
-      if (uj < s.n) {
-        int ai, tile;
-        unit_of(phase, s.u0 + uj, ai, tile);
-        const int r0 = first[ai], cnt = first[ai + 1] - r0;
-        const float* from = parts + (warp << s.lgS) * rows4 * 64 + lane;
+      consumer_sync();
+      // fewer than kWarps units are split: a piece is half a column tile of one
+      const int rest = s.n - s.whole, pieces = wide ? 4 : 2;
 #pragma unroll 1
-        for (int i = 0; i < (wide && cnt > 4 ? 2 : 1); ++i, from += 4 * 64) {
+      for (int w = warp; w < rest * pieces; w += kWarps) {
+        const int uj = w / pieces, i = w - uj * pieces;
+        int ai, tile;
+        unit_of(phase, s.u0 + s.whole + uj, ai, tile);
+        const int r0 = first[ai], cnt = first[ai + 1] - r0;
+        if (i < 2 || cnt > 4) {
+          const float* from = parts + ((uj << s.lgS) * rows4 + i * 4) * 64 + lane;
           float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 2
-          for (int sp = 0; sp < (1 << s.lgS); ++sp)
+          for (int part_i = 0; part_i < (1 << s.lgS); ++part_i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) d[j] += from[(sp * rows4 + j) * 64];
-          finish(phase, d, cnt, r0, tile, i);
+            for (int j = 0; j < 4; ++j) d[j] += from[(part_i * rows4 + j) * 64];
+          finish(phase, d, cnt, r0, tile, i >> 1, i & 1);
         }
       }
     }
   };
 
-  // Lets the loads in flight land and drops them.
-  auto drain = [&]() __attribute__((always_inline)) {
-    for (; q_out != q_in; ++q_out) mbar_drain(&full[q_out & (D - 1)], (q_out / D) & 1u);
-  };
   // Waits until every share of phase A is done.
   auto wait_a = [&]() __attribute__((always_inline)) {
     if (threadIdx.x == 0) {
@@ -824,12 +893,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
       }
       __threadfence();
     }
-    __syncthreads();
+    consumer_sync();
   };
   // Combines the slots of output tile `tile` in slot order.
   auto combine = [&](int tile) __attribute__((always_inline)) {
-    for (int i = threadIdx.x; i < T * 16; i += kThreads) {
-      const int t = i >> 4, n = tile * 16 + (i & 15);
+    for (int i = threadIdx.x; i < T * 32; i += kConsumers) {
+      const int t = i >> 5, n = tile * 32 + (i & 31);
       float v = 0.0f;
       for (int s = 0; s < k; ++s) {
         const float w = wts[t * k + s];
@@ -839,74 +908,57 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
     }
   };
 
-  if (threadIdx.x < 2) set_share(threadIdx.x, threadIdx.x ? next_b : next_a);
-  __syncthreads();
-  bool in_a = next_a < G, fresh = true, waited = in_a;
+  bool waited = false;
 #pragma unroll 1
-  for (;;) {
-    if (fresh) {
-      fresh = false;
-      pc_phase = 0;
-      pc_item = 0;
-#pragma unroll 1
-      for (;;) {
-        enter();
-        if (pc_item >= 0 || pc_phase) break;
-        pc_phase = 1;
-        pc_item = 0;
-      }
-#pragma unroll 1
-      for (int i = 0; i < D - 1; ++i) issue();
-    }
-    if (!waited) {
+  for (int i = 0;; ++i) {
+    mbar_wait(&published[i & 1], (i >> 1) & 1, &misc[3], p.err);
+    if (misc[3]) break;
+    const Share& s = *share(i);
+    if (threadIdx.x == 0) misc[2] = i + 1;
+    if (s.phase == 2) break;
+    if (s.phase == 1 && !waited) {
       waited = true;
       wait_a();
+      if (misc[3]) break;
     }
-    if (!in_a && (next_b >= G || misc[3])) break;
-    run_share(in_a ? 0 : 1);
-    if (threadIdx.x == 0) misc[2] = atomicAdd(&a.counters[in_a ? 0 : 1], 1);
-    if (in_a || !aligned) __threadfence();
-    __syncthreads();
-    const int next = misc[2];
-    if (in_a) {
+    run_share(s);
+    if (s.phase == 0 || !aligned) __threadfence();
+    consumer_sync();
+    if (s.phase == 0) {
       if (threadIdx.x == 0) atomicAdd(&a.counters[2], 1);
-    } else if (share(1).n > 0) {
+    } else if (s.n > 0) {
       // tiles that this share touches: an aligned share holds all of a tile's
       // experts; else the CTA that brings the tile's count to A combines it
-      const int ub = share(1).u0, ue = ub + share(1).n, last_tile = (ue - 1) / A;
+      const int ub = s.u0, ue = ub + s.n, last_tile = (ue - 1) / A;
       for (int tile = ub / A; tile <= last_tile; ++tile) {
         if (aligned) {
           combine(tile);
         } else {
           if (threadIdx.x == 0) {
-            const int mine = min(ue, (tile + 1) * A) - max(ub, tile * A);
-            misc[5] = atomicAdd(&a.counters[kCounters + tile], mine) + mine == A;
+            const int part_n = min(ue, (tile + 1) * A) - max(ub, tile * A);
+            misc[5] = atomicAdd(&a.counters[kCounters + tile], part_n) + part_n == A;
             __threadfence();
           }
-          __syncthreads();
+          consumer_sync();
           if (misc[5]) combine(tile);
-          __syncthreads();
+          consumer_sync();
         }
       }
     }
-    if (next < G) {
-      // another share of this phase is unclaimed (some CTAs have not started):
-      // drop what is in flight and start the stream again
-      drain();
-      __syncthreads();  // before misc[2], the rings and the part rows are written again
-      if (threadIdx.x == 0) {
-        if (!in_a) set_share(0, G);
-        set_share(in_a ? 0 : 1, next);
-      }
-      __syncthreads();
-      fresh = true;
-    } else if (in_a) {
-      in_a = waited = false;
-    } else {
-      break;
-    }
   }
-  drain();
+}
+
+// z matrices of y rows of x bytes, boxes of 128 bytes x by rows x bz.
+cudaError_t make_map_3d(CUtensorMap* m, const void* base, uint64_t x, uint64_t y, uint64_t z,
+                        uint32_t by, uint32_t bz) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {x, y, z}, strides[2] = {x, x * y};
+  const cuuint32_t box[3] = {(cuuint32_t)CKB, by, bz}, es[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides,
+                         box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 struct Layout {
@@ -939,21 +991,18 @@ cudaError_t launch_t(const LayerArgs& a, int num_sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // Whole tiles of H per CTA in phase B spare the counting of a tile's experts
   // across CTAs (about 1.5 us) but leave the last round of tiles uneven: taken
-  // when that costs at most kAlignChunks chunks of 2 KB per CTA (about 46 ns
+  // when that costs at most kAlignChunks chunks of 4 KB per CTA (about 92 ns
   // each at the measured HBM rate).
-  constexpr int64_t kAlignChunks = 32;
-  const int64_t tiles = a.p.H / 16, A = std::min<int64_t>(a.p.E, a.p.T * a.p.k);
+  constexpr int64_t kAlignChunks = 16;
+  const int64_t tiles = a.p.H / 32, A = std::min<int64_t>(a.p.E, a.p.T * a.p.k);
   const int64_t whole = (tiles + num_sms - 1) / num_sms * A;
   const int64_t even = (tiles * A + num_sms - 1) / num_sms;
   const int aligned = (whole - even) * ((a.p.I + 255) / 256) <= kAlignChunks;
-  CUtensorMap gu, dn;  // packed matrices, boxes of 8 rows x 128 bytes
-  e = make_map_2d(&gu, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.p.gu, (uint64_t)a.p.H / 2,
-                  (uint64_t)a.p.E * 2 * (uint64_t)a.p.I, (uint64_t)a.p.H / 2, CKB, 8,
-                  CU_TENSOR_MAP_SWIZZLE_128B);
+  CUtensorMap gu, dn;  // boxes of 16 gate and 16 up rows, and of 32 down rows
+  const uint64_t kb = (uint64_t)a.p.H / 2, ib = (uint64_t)a.p.I / 2;
+  e = make_map_3d(&gu, a.p.gu, kb, (uint64_t)a.p.I, (uint64_t)a.p.E * 2, 16, 2);
   if (e != cudaSuccess) return e;
-  e = make_map_2d(&dn, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.p.dn, (uint64_t)a.p.I / 2,
-                  (uint64_t)a.p.E * (uint64_t)a.p.H, (uint64_t)a.p.I / 2, CKB, 8,
-                  CU_TENSOR_MAP_SWIZZLE_128B);
+  e = make_map_3d(&dn, a.p.dn, ib, (uint64_t)a.p.E * (uint64_t)a.p.H, 1, 32, 1);
   if (e != cudaSuccess) return e;
   return launch_kernel<k>(num_sms, kThreads, Smem::bytes, s, true, a, aligned, gu, dn);
 }
