@@ -101,6 +101,16 @@ struct Device {
   }
 };
 
+// A tensor over part of another's memory, from 4-byte element `first` on: much
+// cheaper to make than an allocation or a view.
+at::Tensor part(const at::Tensor& whole, at::ScalarType type, int64_t first, at::IntArrayRef sizes) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+      c10::Storage(whole.storage()), whole.key_set(), at::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_storage_offset(first);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+  return t;
+}
+
 template <typename T = void>
 T* at_(const at::Tensor& t) {
   return static_cast<T*>(t.data_ptr());
@@ -152,17 +162,18 @@ PyObject* route(PyObject* const* a) {
     value_error(d.where + ": k=" + str(k) + " must be in 1 .. min(E=" + str(E) + ", 32)");
   if (T * k > INT32_MAX) value_error(d.where + ": T * k must be below 2^31");
   d.add("logits", l);
-  const at::Tensor ids = d.empty({T, k}, at::kInt), w = d.empty({T, k}, at::kFloat),
-                   off = d.empty({E + 1}, at::kInt), r2t = d.empty({T * k}, at::kInt),
-                   ros = d.empty({T, k}, at::kInt), sor = d.empty({T * k}, at::kInt);
-  const int64_t bytes = gmoe_route_workspace(T, (int32_t)E);
-  at::Tensor ws;
-  if (bytes) ws = d.empty({bytes}, at::kByte);
+  // the results and the workspace in one allocation
+  const int64_t n = T * k, bytes = gmoe_route_workspace(T, (int32_t)E);
+  const at::Tensor all = d.empty({5 * n + E + 1 + bytes / 4}, at::kInt);
+  const at::Tensor ids = part(all, at::kInt, 0, {T, k}), w = part(all, at::kFloat, n, {T, k}),
+                   r2t = part(all, at::kInt, 2 * n, {n}), ros = part(all, at::kInt, 3 * n, {T, k}),
+                   sor = part(all, at::kInt, 4 * n, {n}), off = part(all, at::kInt, 5 * n, {E + 1});
+  int32_t* ws = at_<int32_t>(all) + 5 * n + E + 1;
   const bool renorm = truth(a[2]);
   call(d, [&](void* s) {
     return gmoe_route(l.data_ptr(), type, T, (int32_t)E, (int32_t)k, renorm, at_<int32_t>(ids),
                       at_<float>(w), at_<int32_t>(off), at_<int32_t>(r2t), at_<int32_t>(ros),
-                      at_<int32_t>(sor), bytes ? ws.data_ptr() : nullptr, bytes, s);
+                      at_<int32_t>(sor), bytes ? ws : nullptr, bytes, s);
   });
   return Py_BuildValue("NNNNNN", wrap(ids), wrap(w), wrap(off), wrap(r2t), wrap(ros), wrap(sor));
 }

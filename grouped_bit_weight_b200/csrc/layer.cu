@@ -54,7 +54,7 @@ constexpr int kMaxE = 1024;
 constexpr int kMaxP = 512;
 constexpr int kRows = 8;           // most rows of a group: rows of one expert that share a decode
 constexpr int CKB = 128;           // bytes per weight row and stage: 256 k
-constexpr int D = 3;               // stages per warp
+constexpr int D = 2;               // stages per warp
 constexpr int kStage = 32 * CKB;   // 4 KB: 32 weight rows
 
 // Shared memory by address in the shared window (dynamic shared memory starts
@@ -63,7 +63,7 @@ constexpr int kStage = 32 * CKB;   // 4 KB: 32 weight rows
 // The other half of each 256 bytes holds partial sums (kParts rows of 32
 // floats).  The warps' rings lie on both sides of it.
 constexpr int kParts = 256;
-constexpr int kLowWarps = 4;
+constexpr int kLowWarps = 7;
 struct Smem {
   static constexpr int base = 1024;
   static constexpr int ids = base;               // [kMaxP] int

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(256) combine_kernel(
           const int32_t r = slot_row(rows, t * k + s0 + j, P, err);
           if (r >= 0) {
             w[j] = weights ? __ldg(weights + t * k + s0 + j) : 1.0f;
-            if (w[j] != 0.0f) v[j] = __ldg(reinterpret_cast<const uint4*>(y + r * H + c));
+            if (w[j] != 0.0f) v[j] = __ldcs(reinterpret_cast<const uint4*>(y + r * H + c));
           }
         }
       }
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(256) combine_kernel(
     o.y = pack_bf16x2(a[2], a[3]);
     o.z = pack_bf16x2(a[4], a[5]);
     o.w = pack_bf16x2(a[6], a[7]);
-    *reinterpret_cast<uint4*>(out + t * H + c) = o;
+    __stcs(reinterpret_cast<uint4*>(out + t * H + c), o);
   }
 }
 
