@@ -784,6 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
       Raw raw = {0, 0, 0, 0};
       const uint16_t* src = nullptr;
       const uint8_t* sp = nullptr;
+      bool ready = false;  // x holds the first columns of the item
 #pragma unroll 1
       for (;;) {
         int ai, tile;
@@ -801,15 +802,17 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
           src = column(phase, r0, cnt, 0) + c * 256;
           sp = scale_ptr(phase, ai, tile, c);
           load_scales(sp, next, far, t4 < nbk - c * 4, raw);
-          if (!wide) {
-            load_x(src, x[0][0], x[0][1]);
-            if (nbk - c * 4 > 1) load_x(src + 64, x[1][0], x[1][1]);
-          }
         }
+        const bool two = phase && cnt > 4;
+        if (!two && !ready) {
+          load_x(src, x[0][0], x[0][1]);
+          if (nbk - c * 4 > 1) load_x(src + 64, x[1][0], x[1][1]);
+        }
+        ready = !two;
         float acc[2][2][4];  // [column tile][half]
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[0][0][j] = acc[0][1][j] = acc[1][0][j] = acc[1][1][j] = 0.0f;
-        if (!wide) {
+        if (!two) {
 #pragma unroll 1
           for (; c < c1; ++c, src += 256, sp += kScChunk) {
             const bool last = c + 1 == c1;
@@ -817,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
                      last ? nsp : sp + kScChunk, next, far, last ? nnb : nbk - c * 4 - 4, acc[0]);
           }
         } else {
-          const uint16_t* src1 = column(1, r0, cnt, cnt > 4 ? 1 : 0) + c * 256;
+          const uint16_t* src1 = column(1, r0, cnt, 1) + c * 256;
           uint4 y[2][2][2];
           load_x(src, y[0][0][0], y[0][0][1]);
           load_x(src1, y[0][1][0], y[0][1][1]);
@@ -831,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
         if (u < s.whole || s.lgS == 0) {
           finish(phase, acc[0][0], cnt, r0, tile, 0, 0);
           finish(phase, acc[0][1], cnt, r0, tile, 0, 1);
-          if (wide && cnt > 4) {
+          if (two) {
             finish(1, acc[1][0], cnt, r0, tile, 1, 0);
             finish(1, acc[1][1], cnt, r0, tile, 1, 1);
           }
@@ -842,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
           for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int j = 0; j < 4; ++j) to[(m * 4 + j) * 64] = acc[0][m][j];
-          if (wide)
+          if (two)
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
