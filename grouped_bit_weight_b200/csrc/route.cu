@@ -47,65 +47,79 @@ __device__ __forceinline__ int block_exclusive(int v, int* part) {
   }
   if (lane == 31) part[warp] = incl;
   __syncthreads();
-  int below = 0;
-  for (int i = 0; i < warp; ++i) below += part[i];
-  return below + incl - v;
+  return __reduce_add_sync(0xffffffffu, lane < warp ? part[lane] : 0) + incl - v;
 }
 
-// Places slots [slot0, slot0 + n) of this CTA: base[e] is the row of the
-// CTA's first slot of expert e.  Each warp owns a contiguous run of slots
-// and walks it 32 at a time, so equal experts keep their slot order.
-__device__ __forceinline__ void place(const RouteProblem& p, int64_t slot0, int n, const int* base,
-                                      int* whist) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = p.E;
-  const int nw = min(kWarps, (n + 31) / 32);
-  const int seg = nw ? (n + nw - 1) / nw : 0;
-  const int i0 = min(n, warp * seg), i1 = warp < nw ? min(n, i0 + seg) : i0;
-  for (int i = threadIdx.x; i < nw * E; i += kThreads) whist[i] = 0;
-  __syncthreads();
-  for (int i = i0 + lane; i < i1; i += 32) atomicAdd(&whist[warp * E + p.ids[slot0 + i]], 1);
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kThreads) {
-    int run = base[e];
-    for (int w = 0; w < nw; ++w) {
-      const int c = whist[w * E + e];
-      whist[w * E + e] = run;
-      run += c;
+// The slots [slot0, slot0 + n) of a CTA: each warp owns a contiguous run
+// [i0, i1) of them and walks it 32 at a time, so equal experts keep their slot
+// order.  whist[w * E + e] counts warp w's slots of expert e, then is the row of
+// its next one.
+struct Slots {
+  int64_t slot0;
+  int nw, i0, i1;
+  __device__ __forceinline__ Slots(int64_t s, int n) : slot0(s) {
+    const int warp = threadIdx.x >> 5;
+    nw = min(kWarps, (n + 31) / 32);
+    const int seg = nw ? (n + nw - 1) / nw : 0;
+    i0 = min(n, warp * seg);
+    i1 = warp < nw ? min(n, i0 + seg) : i0;
+  }
+  // `id`: expert of slot i0 + lane (the only one of most lanes)
+  __device__ __forceinline__ void count(const RouteProblem& p, int id, int* whist) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = i0 + lane; i < i1; i += 32) {
+      atomicAdd(&whist[warp * p.E + id], 1);
+      if (i + 32 < i1) id = p.ids[slot0 + i + 32];
     }
   }
-  __syncthreads();
-  for (int i = i0; i < i1; i += 32) {
-    const bool on = i + lane < i1;
-    const int64_t slot = slot0 + i + lane;
-    const int id = on ? p.ids[slot] : -1 - lane;
-    const unsigned same = __match_any_sync(0xffffffffu, id);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    const int at = on ? whist[warp * E + id] + rank : 0;
-    __syncwarp();
-    if (on) {
-      if (rank == 0) whist[warp * E + id] += __popc(same);
-      p.row_of_slot[slot] = at;
-      p.row_to_token[at] = (int32_t)((uint32_t)slot / (uint32_t)p.k);
-      p.slot_of_row[at] = (int32_t)slot;
+  // Thread e: the rows of expert e from `run` on, warp after warp.
+  __device__ __forceinline__ void scan(int E, int run, int* whist) const {
+    for (int w0 = 0; w0 < nw; w0 += 8) {
+      int c[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = w0 + j < nw ? whist[(w0 + j) * E + threadIdx.x] : 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (w0 + j < nw) whist[(w0 + j) * E + threadIdx.x] = run;
+        run += c[j];
+      }
     }
-    __syncwarp();
   }
-}
+  __device__ __forceinline__ void place(const RouteProblem& p, int id, int* whist) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = p.E;
+    for (int i = i0; i < i1; i += 32) {
+      const bool on = i + lane < i1;
+      const int64_t slot = slot0 + i + lane;
+      const unsigned same = __match_any_sync(0xffffffffu, on ? id : -1 - lane);
+      const int rank = __popc(same & ((1u << lane) - 1u));
+      const int at = on ? whist[warp * E + id] + rank : 0;
+      __syncwarp();
+      if (on) {
+        if (rank == 0) whist[warp * E + id] += __popc(same);
+        p.row_of_slot[slot] = at;
+        p.row_to_token[at] = (int32_t)((uint32_t)slot / (uint32_t)p.k);
+        p.slot_of_row[at] = (int32_t)slot;
+        if (i + 32 + lane < i1) id = p.ids[slot + 32];
+      }
+      __syncwarp();
+    }
+  }
+};
 
 // Chooses the experts of tokens [b * per, (b + 1) * per) and counts them;
 // kSingle (one CTA): sorts and places them too.
 template <typename TL, int NPL, bool kSingle>
 __global__ void __launch_bounds__(kThreads) route_choose(const RouteProblem p, const int per) {
   extern __shared__ int sm[];
-  int* count = sm;        // [E] slots of each expert in this CTA, then base
-  int* part = sm + p.E;   // [kWarps]
-  int* whist = part + kWarps;
+  // kSingle: part [kWarps], whist [kWarps][E]; else count [E]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = p.E, k = p.k;
   if (!kSingle) grid_launch_dependents();
-  for (int e = threadIdx.x; e < E; e += kThreads) count[e] = 0;
-  __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * per;
   const int n = (int)max((int64_t)0, min((int64_t)per, p.T - t0));
+  int* const hist = kSingle ? sm + kWarps : sm;
+  const Slots slots(t0 * k, n * k);
+  for (int i = threadIdx.x; i < (kSingle ? slots.nw * E : E); i += kThreads) hist[i] = 0;
+  if (!kSingle) __syncthreads();
   for (int i = warp; i < n; i += kWarps) {
     const int64_t t = t0 + i;
     int id = 0;
@@ -114,41 +128,50 @@ __global__ void __launch_bounds__(kThreads) route_choose(const RouteProblem p, c
     if (lane < k) {
       p.ids[t * k + lane] = id;
       p.weights[t * k + lane] = w;
-      atomicAdd(&count[id], 1);
+      if (!kSingle) atomicAdd(&hist[id], 1);
     }
   }
   __syncthreads();
+  const int e = threadIdx.x;  // E <= kThreads
   if (kSingle) {
-    const int e = threadIdx.x;  // E <= kThreads
-    const int c = e < E ? count[e] : 0;
-    const int at = block_exclusive(c, part);
+    const int id = slots.i0 + lane < slots.i1 ? p.ids[slots.slot0 + slots.i0 + lane] : 0;
+    slots.count(p, id, hist);
+    __syncthreads();
+    int c = 0;
+    if (e < E)
+      for (int w = 0; w < slots.nw; ++w) c += hist[w * E + e];
+    const int at = block_exclusive(c, sm);
     if (e < E) {
-      count[e] = at;
       p.offsets[e] = at;
       if (e == E - 1) p.offsets[E] = at + c;
+      slots.scan(E, at, hist);
     }
     __syncthreads();
-    place(p, t0 * k, n * k, count, whist);
-  } else {
-    for (int e = threadIdx.x; e < E; e += kThreads)
-      p.hist[(int64_t)blockIdx.x * E + e] = count[e];
+    slots.place(p, id, hist);
+  } else if (e < E) {
+    p.hist[(int64_t)blockIdx.x * E + e] = hist[e];
   }
 }
 
 // Second kernel: rows of this CTA's slots from all CTAs' counts.
 __global__ void __launch_bounds__(kThreads) route_place(const RouteProblem p, const int per) {
   extern __shared__ int sm[];
-  int* base = sm;                // [E]
-  int* part = base + p.E;        // [kWarps]
+  int* part = sm;                // [kWarps]
   int* red = part + kWarps;      // [2][kThreads]
   int* whist = red + 2 * kThreads;
-  const int E = p.E;
+  const int E = p.E, lane = threadIdx.x & 31;
   int lg = 5;  // threads of one part: a power of two >= E
   while ((1 << lg) < E) ++lg;
   const int parts = kThreads >> lg, me = threadIdx.x >> lg, e = threadIdx.x & ((1 << lg) - 1);
+  const int64_t t0 = (int64_t)blockIdx.x * per;
+  const int n = (int)max((int64_t)0, min((int64_t)per, p.T - t0));
+  const Slots slots(t0 * p.k, n * p.k);
+  for (int i = threadIdx.x; i < slots.nw * E; i += kThreads) whist[i] = 0;
   grid_dependency_wait();
+  const int id = slots.i0 + lane < slots.i1 ? p.ids[slots.slot0 + slots.i0 + lane] : 0;
   int total = 0, before = 0;
   if (e < E) {
+#pragma unroll 8
     for (int b = me; b < (int)gridDim.x; b += parts) {
       const int c = p.hist[(int64_t)b * E + e];
       total += c;
@@ -158,25 +181,25 @@ __global__ void __launch_bounds__(kThreads) route_place(const RouteProblem p, co
   red[threadIdx.x] = total;
   red[kThreads + threadIdx.x] = before;
   __syncthreads();
+  slots.count(p, id, whist);
   total = before = 0;
   if (threadIdx.x < (unsigned)E) {
+#pragma unroll 8
     for (int i = 0; i < parts; ++i) {
       total += red[(i << lg) + threadIdx.x];
       before += red[kThreads + (i << lg) + threadIdx.x];
     }
   }
-  const int at = block_exclusive(total, part);
+  const int at = block_exclusive(total, part);  // its barrier completes whist
   if (threadIdx.x < (unsigned)E) {
-    base[threadIdx.x] = at + before;
     if (blockIdx.x == 0) {
       p.offsets[threadIdx.x] = at;
       if ((int)threadIdx.x == E - 1) p.offsets[E] = at + total;
     }
+    slots.scan(E, at + before, whist);
   }
   __syncthreads();
-  const int64_t t0 = (int64_t)blockIdx.x * per;
-  const int64_t n = max((int64_t)0, min((int64_t)per, p.T - t0)) * p.k;
-  place(p, t0 * p.k, (int)n, base, whist);
+  slots.place(p, id, whist);
 }
 
 // One warp per token: dlogits row built in shared memory, written once.
@@ -333,9 +356,9 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(
 }
 
 size_t choose_smem(int E, bool single) {
-  return 4 * ((size_t)E + kWarps + (single ? (size_t)kWarps * E : 0));
+  return 4 * (single ? kWarps + (size_t)kWarps * E : (size_t)E);
 }
-size_t place_smem(int E) { return 4 * ((size_t)E + kWarps + 2 * kThreads + (size_t)kWarps * E); }
+size_t place_smem(int E) { return 4 * (kWarps + 2 * kThreads + (size_t)kWarps * E); }
 
 template <typename TL, int NPL>
 cudaError_t route_t(const RouteProblem& p, int num_sms, cudaStream_t s) {
