@@ -162,13 +162,15 @@ PyObject* route(PyObject* const* a) {
     value_error(d.where + ": k=" + str(k) + " must be in 1 .. min(E=" + str(E) + ", 32)");
   if (T * k > INT32_MAX) value_error(d.where + ": T * k must be below 2^31");
   d.add("logits", l);
-  // the results and the workspace in one allocation
+  // the integer results and the workspace in one allocation; the weights in
+  // their own (torch.save refuses one storage under two types)
   const int64_t n = T * k, bytes = gmoe_route_workspace(T, (int32_t)E);
-  const at::Tensor all = d.empty({5 * n + E + 1 + bytes / 4}, at::kInt);
-  const at::Tensor ids = part(all, at::kInt, 0, {T, k}), w = part(all, at::kFloat, n, {T, k}),
-                   r2t = part(all, at::kInt, 2 * n, {n}), ros = part(all, at::kInt, 3 * n, {T, k}),
-                   sor = part(all, at::kInt, 4 * n, {n}), off = part(all, at::kInt, 5 * n, {E + 1});
-  int32_t* ws = at_<int32_t>(all) + 5 * n + E + 1;
+  const at::Tensor all = d.empty({4 * n + E + 1 + bytes / 4}, at::kInt);
+  const at::Tensor w = d.empty({T, k}, at::kFloat);
+  const at::Tensor ids = part(all, at::kInt, 0, {T, k}), r2t = part(all, at::kInt, n, {n}),
+                   ros = part(all, at::kInt, 2 * n, {T, k}), sor = part(all, at::kInt, 3 * n, {n}),
+                   off = part(all, at::kInt, 4 * n, {E + 1});
+  int32_t* ws = at_<int32_t>(all) + 4 * n + E + 1;
   const bool renorm = truth(a[2]);
   call(d, [&](void* s) {
     return gmoe_route(l.data_ptr(), type, T, (int32_t)E, (int32_t)k, renorm, at_<int32_t>(ids),
