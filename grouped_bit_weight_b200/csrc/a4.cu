@@ -21,8 +21,7 @@
 //   warps 4-11  the scale bytes of 128 weight rows and up to 384 routed rows,
 //               loaded two stages ahead and written to TMEM (a set per stage)
 //   warp 1      tcgen05.mma.kind::mxf4.block_scale, 64 k each
-//   warps 12-19 epilogue: tcgen05.ld -> bf16 -> turned over in shared memory ->
-//               64-byte row segments
+//   warps 12-19 epilogue: tcgen05.ld -> bf16 -> 64-byte row segments
 // A tile holds up to 384 routed rows, fed by the same weights: up to 256 are
 // one MMA, more are two; tiles of up to 192 alternate between two accumulator
 // halves, so that an epilogue overlaps the next tile's MMAs.
@@ -154,12 +153,9 @@ constexpr int kSfBytes = 4096;                     // 8 scale bytes of 128 + 384
 constexpr int kStageBytes = kABytes + 2 * kBHalfBytes + kSfBytes;
 static_assert(kStageBytes % 1024 == 0 && kBHalfBytes % 1024 == 0, "swizzle atoms stay aligned");
 constexpr int kEpiWarps = 8;
-constexpr int kEpiRow = 64 + 16;                  // 32 bf16 and a pad
-constexpr int kEpiBytes = 16 * kEpiRow;           // 16 routed rows x 32 weight rows
 
 struct Smem {
-  static constexpr int epi = ST * kStageBytes;
-  static constexpr int bars = epi + kEpiWarps * kEpiBytes;
+  static constexpr int bars = ST * kStageBytes;
   static constexpr int nbars = 2 * ST + 4 + 1;
   static constexpr int misc = bars + nbars * 8;
   static constexpr int tables = misc + 16;
@@ -280,6 +276,13 @@ __device__ __forceinline__ void tmem_store_16(uint32_t taddr, const uint32_t (&r
       : "memory");
 }
 
+// One lane of the warp, the same for every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t v;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(v));
+  return v != 0;
+}
+
 // Barrier of the four warps of a scale group.
 __device__ __forceinline__ void group_sync(int group) {
   asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
@@ -334,7 +337,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
   int32_t* off_s = reinterpret_cast<int32_t*>(smem + Smem::tables);
   int32_t* ts_s = off_s + (pb.E + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int32_t E = pb.E;
   const int64_t N = pb.N;
   const int32_t KB = (int32_t)(pb.K / 2);         // bytes of codes per row
@@ -399,25 +402,29 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
     // ---------------- MMA issuer ----------------
     // One thread issues everything, so its instructions count: descriptors are
     // built once and advance by constants, a whole stage is unrolled.
-    if (lane == 0) {
-      uint32_t g = 0, s = 0, ph = 0;
+    {
+      const bool leader = elect_one();
+      uint32_t s = 0, ph = 0;
       bool ok = true;
       AccSched acc;
+      auto all = [](bool v) { return __all_sync(0xffffffffu, v) != 0; };
       const uint64_t adesc0 = make_sdesc_sw128(smem_u32(smem), 16, 1024);
       const uint64_t bdesc0 = make_sdesc_sw128(smem_u32(smem + kABytes), 16, 1024);
       for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
-        const Tile d = tile_info(t, off_s, ts_s, E, at_e);
+        Tile d = tile_info(t, off_s, ts_s, E, at_e);
+        d.nv = __shfl_sync(0xffffffffu, d.nv, 0);
+        d.nh = __shfl_sync(0xffffffffu, d.nh, 0);
         const bool both = d.nv > BH, two = d.nv > BN;
         const uint32_t h0 = both ? 0u : acc.h;
         const uint32_t n0 = (uint32_t)(d.nh + 15) & ~15u, n1 = (uint32_t)(d.nv - d.nh + 15) & ~15u;
         const uint32_t i0 = idesc_mxf4(n0, 0), i1 = idesc_mxf4(n1, 0);
         constexpr uint32_t kUpper = (2u << 4) | (2u << 29);  // the scale words' upper halves
         const uint32_t d0 = tmem + h0 * BH, d1 = tmem + BH;
-        if (!(ok = mbar_wait(&acc_empty[h0], acc.phase(h0) ^ 1u, abort, pb.err))) break;
-        if (both && !two && !(ok = mbar_wait(&acc_empty[1], acc.phase(1) ^ 1u, abort, pb.err))) break;
-        for (int ks = 0; ks < NS; ++ks, ++g) {
-          if (!(ok = mbar_wait(&full[s], ph, abort, pb.err))) break;
-          if (two && ks == 0 && !(ok = mbar_wait(&acc_empty[1], acc.phase(1) ^ 1u, abort, pb.err))) break;
+        if (!(ok = all(mbar_wait(&acc_empty[h0], acc.phase(h0) ^ 1u, abort, pb.err)))) break;
+        if (both && !two && !(ok = all(mbar_wait(&acc_empty[1], acc.phase(1) ^ 1u, abort, pb.err)))) break;
+        for (int ks = 0; ks < NS; ++ks) {
+          if (!(ok = all(mbar_wait(&full[s], ph, abort, pb.err)))) break;
+          if (two && ks == 0 && !(ok = all(mbar_wait(&acc_empty[1], acc.phase(1) ^ 1u, abort, pb.err)))) break;
           tc_fence_after();
           const uint64_t so = (uint64_t)((s * kStageBytes) >> 4);
           const uint64_t ad = adesc0 + so, bd = bdesc0 + so;
@@ -436,23 +443,30 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
             }
           };
           const int nk = (KB - ks * BKB + 31) / 32;  // 64-k steps left
-          if (nk >= 4) {
-            atom(0, true);
-            atom(1, true);
-          } else {
-            atom(0, nk > 1);
-            if (nk > 2) atom(1, false);
+          if (leader) {
+            if (nk >= 4) {
+              atom(0, true);
+              atom(1, true);
+            } else {
+              atom(0, nk > 1);
+              if (nk > 2) atom(1, false);
+            }
+            tc_commit(&empty[s]);
           }
-          tc_commit(&empty[s]);
           if (++s == ST) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
-        tc_commit(&acc_full[h0]);
-        if (both) tc_commit(&acc_full[1]);
+        if (leader) {
+          tc_commit(&acc_full[h0]);
+          if (both) tc_commit(&acc_full[1]);
+        }
         acc.next(both);
       }
-      tc_commit(mma_done);
-      mbar_drain(mma_done, 0);
+      if (leader) {
+        tc_commit(mma_done);
+        mbar_drain(mma_done, 0);
+      }
+      __syncwarp();
     }
   } else if (warp >= 4 && warp < 12) {
     // ---------------- scales ----------------
@@ -567,20 +581,19 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
   } else if (warp >= 12) {
     // ---------------- epilogue ----------------
     // warp quarter q reads weight rows 32 q .. of the tile (TMEM lanes); the two
-    // warps of a quarter take alternate 16-row pieces of the routed rows, turn
-    // them over in shared memory and store 64-byte row segments
+    // warps of a quarter take alternate 32-row pieces of the routed rows.  Lanes
+    // 2 i and 2 i + 1 trade halves, so that each stores words of two weight rows:
+    // the even lane those of the even routed rows, 64 bytes a row and warp.
     const uint32_t q = (uint32_t)warp & 3u;
-    const int mine = (warp - 12) >> 2;
-    uint8_t* turn = smem + Smem::epi + (warp - 12) * kEpiBytes;
-    uint16_t* put = reinterpret_cast<uint16_t*>(turn) + lane;
-    const uint8_t* got = turn + (lane >> 2) * kEpiRow + (lane & 3) * 16;
+    const int mine = (warp - 12) >> 2, odd = lane & 1;
+    const uint32_t keep_sel = odd ? 0x7632u : 0x5410u, send_sel = odd ? 0x5410u : 0x7632u;
+    const uint32_t lo_sel = odd ? 0x1054u : 0x5410u, hi_sel = odd ? 0x3276u : 0x7632u;
     AccSched acc;
     bool ok = true;
     for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
       const Tile d = tile_info(t, off_s, ts_s, E, at_e);
       const bool both = d.nv > BH, two = d.nv > BN;
-      // this lane's 8 weight rows of a stored segment
-      const int64_t n = d.n0 + (int64_t)(q * 32 + (lane & 3) * 8);
+      const int64_t n = d.n0 + (int64_t)(q * 32 + (lane & 30));
       for (int part = 0; part < (two ? 2 : 1); ++part) {
         const uint32_t h = both ? (uint32_t)part : acc.h;
         ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[h], acc.phase(h), abort, pb.err));
@@ -589,27 +602,23 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
         if (!ok) break;
         tc_fence_after();
         const int rows = part ? d.nv - d.nh : d.nh;
-        uint16_t* dst = pb.out + (int64_t)(d.p0 + (part ? d.nh : 0) + (lane >> 2)) * N + n;
+        uint16_t* dst = pb.out + (int64_t)(d.p0 + (part ? d.nh : 0) + odd) * N + n;
         const uint32_t taddr = tmem + ((q * 32u) << 16) + h * BH;
 #pragma unroll 1
-        for (int c = mine * 16; c < rows; c += 32) {
-          uint32_t r[16];
-          tmem_load_32x32b_x16(taddr + c, r);
+        for (int c = mine * 32; c < rows; c += 64) {
+          uint32_t r[32];
+          tmem_load_32x32b_x32(taddr + c, r);
+          uint16_t* to = dst + (int64_t)c * N;
+          const int left = n < N ? rows - c - odd : 0;
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const uint32_t v = pack_bf16x2(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
-            put[j * (kEpiRow / 2)] = (uint16_t)v;
-            put[(j + 1) * (kEpiRow / 2)] = (uint16_t)(v >> 16);
+          for (int j = 0; j < 32; j += 4) {
+            const uint32_t a = pack_bf16x2(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+            const uint32_t b = pack_bf16x2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
+            const uint32_t keep = prmt(a, b, keep_sel);
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, prmt(a, b, send_sel), 1);
+            if (j < left) *reinterpret_cast<uint32_t*>(to + j * N) = prmt(keep, got, lo_sel);
+            if (j + 2 < left) *reinterpret_cast<uint32_t*>(to + (j + 2) * N) = prmt(keep, got, hi_sel);
           }
-          __syncwarp();
-          if (n < N) {
-#pragma unroll
-            for (int j = 0; j < 16; j += 8)
-              if (c + j + (lane >> 2) < rows)
-                *reinterpret_cast<uint4*>(dst + (int64_t)(c + j) * N) =
-                    *reinterpret_cast<const uint4*>(got + j * kEpiRow);
-          }
-          __syncwarp();
         }
         tc_fence_before();
         __syncwarp();
