@@ -373,29 +373,37 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
 
   if (warp == 0) {
     // ---------------- codes: weights and routed rows ----------------
-    if (lane == 0) {
-      uint32_t g = 0;
+    {
+      const bool leader = elect_one();
+      uint32_t g = 0, s = 0, ph = 1;
       bool ok = true;
       for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
-        const Tile d = tile_info(t, off_s, ts_s, E, at_e);
+        Tile d = tile_info(t, off_s, ts_s, E, at_e);
+        d.nv = __shfl_sync(0xffffffffu, d.nv, 0);
+        d.nh = __shfl_sync(0xffffffffu, d.nh, 0);
+        d.p0 = __shfl_sync(0xffffffffu, d.p0, 0);
+        const int32_t wrow = __shfl_sync(0xffffffffu, (int32_t)((int64_t)d.e * N + d.n0), 0);
         const int b0 = (d.nh + BOX - 1) / BOX, b1 = (d.nv - d.nh + BOX - 1) / BOX;
         const uint32_t bytes = kABytes + (uint32_t)(b0 + b1) * (BOX * BKB);
         for (int ks = 0; ks < NS; ++ks, ++g) {
-          const uint32_t s = g % ST;
-          if (!(ok = mbar_wait(&empty[s], ((g / ST) & 1u) ^ 1u, abort, pb.err))) break;
-          uint8_t* st = smem + s * kStageBytes;
-          mbar_arrive_expect_tx(&full[s], bytes);
-          tma_load_2d(st, &tmw, ks * BKB, (int32_t)((int64_t)d.e * N + d.n0), &full[s]);
-          auto rows = [&](uint8_t* dst, int p0, int n) __attribute__((always_inline)) {
-            for (; n >= 2; n -= 2, dst += 2 * BOX * BKB, p0 += 2 * BOX)
-              tma_load_2d(dst, &tmx2, ks * BKB, p0, &full[s]);
-            if (n) tma_load_2d(dst, &tmx, ks * BKB, p0, &full[s]);
-          };
-          rows(st + kABytes, d.p0, b0);
-          if (b1) rows(st + kABytes + kBHalfBytes, d.p0 + d.nh, b1);
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ph, abort, pb.err));
+          if (!ok) break;
+          if (leader) {
+            uint8_t* st = smem + s * kStageBytes;
+            mbar_arrive_expect_tx(&full[s], bytes);
+            tma_load_2d(st, &tmw, ks * BKB, wrow, &full[s]);
+            auto rows = [&](uint8_t* dst, int p0, int n) __attribute__((always_inline)) {
+              for (; n >= 2; n -= 2, dst += 2 * BOX * BKB, p0 += 2 * BOX)
+                tma_load_2d(dst, &tmx2, ks * BKB, p0, &full[s]);
+              if (n) tma_load_2d(dst, &tmx, ks * BKB, p0, &full[s]);
+            };
+            rows(st + kABytes, d.p0, b0);
+            if (b1) rows(st + kABytes + kBHalfBytes, d.p0 + d.nh, b1);
+          }
+          if (++s == ST) { s = 0; ph ^= 1u; }
         }
       }
-      if (*abort)
+      if (leader && *abort)
         for (uint32_t i = (g > ST ? g - ST : 0); i < g; ++i) mbar_drain(&full[i % ST], (i / ST) & 1u);
     }
   } else if (warp == 1) {
