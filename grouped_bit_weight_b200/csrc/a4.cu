@@ -171,7 +171,6 @@ struct A4Problem {
   const int32_t* offsets;  // [E + 1]
   uint16_t* out;           // [P, N] bf16
   int* err;
-  int wvec;                // widest aligned load of a weight row's scales: 1, 2, 4 or 8 bytes
 };
 
 // nv routed rows.  Up to BN of them are one MMA (N = nv): up to BH in one
@@ -288,37 +287,40 @@ __device__ __forceinline__ void group_sync(int group) {
   asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
-// Eight scale bytes at `p`, of which the first `nvalid` exist; the others
-// read as 127 (2^0: their codes are zeros).  vec divides the address and
-// nvalid.
-__device__ __forceinline__ uint2 load_scales(const uint8_t* p, int nvalid, int vec) {
-  uint32_t w[2] = {0x7F7F7F7Fu, 0x7F7F7F7Fu};
-  if (vec == 8) {
-    if (nvalid > 0) return __ldg(reinterpret_cast<const uint2*>(p));
-  } else if (vec == 4) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (4 * i < nvalid) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
-  } else if (vec == 2 && nvalid >= 8) {
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-    const uint32_t a = __ldg(q), b = __ldg(q + 1), c = __ldg(q + 2), d = __ldg(q + 3);
-    return make_uint2(prmt(a, b, 0x5410u), prmt(c, d, 0x5410u));
-  } else if (vec == 2) {
-    uint32_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      h[i] = 2 * i < nvalid ? (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + i) : 0x7F7Fu;
-    w[0] = h[0] | (h[1] << 16);
-    w[1] = h[2] | (h[3] << 16);
-  } else {
-    uint32_t b[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = i < nvalid ? (uint32_t)__ldg(p + i) : 0x7Fu;
-    w[0] = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
-    w[1] = b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24);
+// Eight scale bytes of a weight row, of which the first `valid` exist: rows have
+// any pitch, so these are the one or two aligned 8-byte words around them (bytes,
+// where a word reaches past the matrix [base, end)).  get() shifts them into
+// place when they are needed: done at once, it would wait for the loads.
+struct RowScales {
+  uint64_t lo, hi;
+  int shift, valid;
+  __device__ __forceinline__ void load(const uint8_t* p, int n, const uint8_t* base,
+                                       const uint8_t* end) {
+    const int o = (int)(reinterpret_cast<uintptr_t>(p) & 7u);
+    const uint8_t* q = p - o;
+    const bool two = o + min(n, 8) > 8;
+    valid = n;
+    shift = 8 * o;
+    if (q >= base && q + (two ? 16 : 8) <= end) {
+      lo = __ldg(reinterpret_cast<const uint64_t*>(q));
+      if (two) hi = __ldg(reinterpret_cast<const uint64_t*>(q) + 1);
+    } else {
+      shift = 0;
+      lo = 0;
+      for (int i = 0; i < min(n, 8); ++i) lo |= (uint64_t)__ldg(p + i) << (8 * i);
+    }
   }
-  return make_uint2(w[0], w[1]);
-}
+  // Bytes that do not exist read as 127 (2^0: their codes are zeros).
+  __device__ __forceinline__ uint2 get() const {
+    uint64_t v = lo;
+    if (shift) v = (lo >> shift) | (hi << (64 - shift));
+    if (valid < 8) {
+      const uint64_t m = valid > 0 ? ~0ull << (8 * valid) : ~0ull;
+      v = (v & ~m) | (0x7F7F7F7F7F7F7F7Full & m);
+    }
+    return make_uint2((uint32_t)v, (uint32_t)(v >> 32));
+  }
+};
 
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
@@ -487,6 +489,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
     // held up the MMAs behind it: 45 of 220 us at 8192 rows x 5760 x 2880.)
     const int group = (warp - 4) >> 2, i = ((warp - 4) & 3) * 32 + lane;
     const uint2 ones = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    const uint8_t* wend = pb.ws + (int64_t)E * N * KS;
     const uint8_t* wp = nullptr;                    // the weight row's scales, or null
     const uint32_t* xp[3] = {nullptr, nullptr, nullptr};  // the routed rows' first words, or null
     int at[3] = {0, 0, 0};                          // their places in the scale area, or -1
@@ -512,7 +515,8 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
       }
     };
     // the scales of the group's next stage, and where they go
-    uint2 w = ones, x[3] = {ones, ones, ones};
+    RowScales w = {0, 0, 0, 0};
+    uint2 x[3] = {ones, ones, ones};
     int to[3] = {0, 0, 0};
     bool two = false, on = false;
     auto step = [&]() __attribute__((always_inline)) {  // to the next stage
@@ -526,7 +530,8 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
       on = t < ntiles;
       if (!on) return;
       two = wide;
-      w = wp ? load_scales(wp + 8 * ks, KS - 8 * ks, pb.wvec) : ones;
+      if (wp) w.load(wp + 8 * ks, KS - 8 * ks, pb.ws, wend);
+      else w.valid = 0;
       const int64_t off = (int64_t)(2 * ks) * pb.P;
       const bool second = 2 * ks + 1 < KA;
 #pragma unroll
@@ -550,7 +555,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
       tc_fence_after();
       // 8 bytes a row: 128 weight rows, then the routed rows
       uint2* sf = reinterpret_cast<uint2*>(smem + s * kStageBytes + kABytes + 2 * kBHalfBytes);
-      sf[i] = w;
+      sf[i] = w.get();
       uint2* sb = sf + BM;
 #pragma unroll
       for (int q = 0; q < 3; ++q)
@@ -644,13 +649,6 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-// The widest of 8, 4, 2, 1 bytes that a row of `pitch` scale bytes at `base`
-// is aligned to in every row.
-int scale_vec(const void* base, int64_t pitch) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(base) | (uintptr_t)pitch | 8u;
-  return (int)(a & (~a + 1u));
-}
-
 }  // namespace
 
 cudaError_t launch_quantize_rows(const uint16_t* x, int64_t T, int64_t K, const int32_t* r2t,
@@ -683,8 +681,7 @@ cudaError_t launch_gemm_a4(const uint8_t* xq, const uint8_t* xs, int64_t P, int6
   e = make_map_2d(&tmx2, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, (uint64_t)K / 2, (uint64_t)P,
                   (uint64_t)K / 2, BKB, 2 * BOX, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
-  const A4Problem pb{reinterpret_cast<const uint32_t*>(xs), ws, P, K, N, E, offsets, out, err,
-                     scale_vec(ws, K / 32)};
+  const A4Problem pb{reinterpret_cast<const uint32_t*>(xs), ws, P, K, N, E, offsets, out, err};
   constexpr size_t most = 1024 + Smem::tables + 8 * (1024 + 1);
   e = opt_in_smem<gemm_a4_kernel>(most);
   if (e != cudaSuccess) return e;
