@@ -257,6 +257,18 @@ struct Share {
 __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
 }
+// The same; whether any of them says `v` (they leave together after a wait that
+// ran out).
+__device__ __forceinline__ bool consumer_any(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n bar.red.or.pred q, 1, %1, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "n"(kConsumers), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
 
 template <Fmt F, int NPL>
 __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, const int aligned,
@@ -883,8 +895,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
     }
   };
 
-  // Waits until every share of phase A is done.
-  auto wait_a = [&]() __attribute__((always_inline)) {
+  // Waits until every share of phase A is done; false after a wait that ran out.
+  auto wait_a = [&]() __attribute__((always_inline)) -> bool {
     if (threadIdx.x == 0) {
       const uint64_t t0 = globaltimer_ns();
       while (ld_acquire(&a.counters[2]) < G) {
@@ -896,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
       }
       __threadfence();
     }
-    consumer_sync();
+    return !consumer_any(misc[3] != 0);
   };
   // Combines the slots of output tile `tile` in slot order.
   auto combine = [&](int tile) __attribute__((always_inline)) {
@@ -915,14 +927,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
 #pragma unroll 1
   for (int i = 0;; ++i) {
     mbar_wait(&published[i & 1], (i >> 1) & 1, &misc[3], p.err);
-    if (misc[3]) break;
+    if (consumer_any(misc[3] != 0)) break;
     const Share& s = *share(i);
     if (threadIdx.x == 0) misc[2] = i + 1;
     if (s.phase == 2) break;
     if (s.phase == 1 && !waited) {
       waited = true;
-      wait_a();
-      if (misc[3]) break;
+      if (!wait_a()) break;
     }
     run_share(s);
     if (s.phase == 0 || !aligned) __threadfence();
