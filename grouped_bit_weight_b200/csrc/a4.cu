@@ -16,15 +16,15 @@
 // weight rows, MMA N the routed rows of one expert, so few rows give a narrow
 // N instead of a padded M):
 //   warp 0      TMA: packed weights [128 x 128 bytes = 256 k] and the rows'
-//               codes (boxes of 64 rows) into a 3-stage ring, 128B swizzle --
+//               codes (boxes of 64 rows) into a 4-stage ring, 128B swizzle --
 //               the packed bytes are the MMA's operands as they are
-//   warps 4-11  the scale bytes of 128 weight rows and up to 384 routed rows,
+//   warps 4-11  the scale bytes of 128 weight rows and up to 256 routed rows,
 //               loaded two stages ahead and written to TMEM (a set per stage)
 //   warp 1      tcgen05.mma.kind::mxf4.block_scale, 64 k each
 //   warps 12-19 epilogue: tcgen05.ld -> bf16 -> 64-byte row segments
-// A tile holds up to 384 routed rows, fed by the same weights: up to 256 are
-// one MMA, more are two; tiles of up to 192 alternate between two accumulator
-// halves, so that an epilogue overlaps the next tile's MMAs.
+// A tile holds up to 256 routed rows.  Tiles of up to 192 alternate between two
+// accumulator halves, so that an epilogue overlaps the next tile's MMAs; larger
+// ones take both.
 // Tiles (expert, weight tile, row tile) run with row tiles innermost: an
 // expert's weights come from HBM once.
 #include "common.cuh"
@@ -136,22 +136,21 @@ __global__ void __launch_bounds__(32 * kQRows) quantize_rows_kernel(
 
 constexpr int BM = 128;       // weight rows per tile (MMA M)
 constexpr int BH = 192;       // TMEM columns of an accumulator half
-constexpr int BT = 2 * BH;    // routed rows per tile
-constexpr int BN = 256;       // routed rows of one MMA at most (MMA N)
+constexpr int BT = 256;       // routed rows per tile (MMA N)
 constexpr int BKB = 128;      // bytes of codes per row and stage: 256 k
 constexpr int BOX = 64;       // routed rows per TMA box, and twice that
-constexpr int ST = 3;         // ring stages
+constexpr int ST = 4;         // ring stages
 constexpr int kThreads = 640;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSfCol = BT;      // scale columns: a set per ring stage
-constexpr uint32_t kSfSet = 8 + 2 * 16;
+constexpr uint32_t kSfCol = 2 * BH;  // scale columns: a set per ring stage
+constexpr uint32_t kSfSet = 8 + 16;
 static_assert(kSfCol + ST * kSfSet <= kTmemCols, "accumulators and scales fit TMEM");
 
 constexpr int kABytes = BM * BKB;                 // 16 KB
-constexpr int kBHalfBytes = BH * BKB;             // 24 KB
-constexpr int kSfBytes = 4096;                     // 8 scale bytes of 128 + 384 rows
-constexpr int kStageBytes = kABytes + 2 * kBHalfBytes + kSfBytes;
-static_assert(kStageBytes % 1024 == 0 && kBHalfBytes % 1024 == 0, "swizzle atoms stay aligned");
+constexpr int kBBytes = BT * BKB;                 // 32 KB
+constexpr int kSfBytes = 8 * (BM + BT);           // 3 KB: 8 scale bytes a row
+constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
+static_assert(kStageBytes % 1024 == 0, "swizzle atoms stay aligned");
 constexpr int kEpiWarps = 8;
 
 struct Smem {
@@ -173,14 +172,14 @@ struct A4Problem {
   int* err;
 };
 
-// nv routed rows.  Up to BN of them are one MMA (N = nv): up to BH in one
-// accumulator half, more across both.  More than BN are two MMAs, the first nh
-// rows in the first half.
 struct Tile {
-  int32_t e, n0, p0, nv, nh;
+  int32_t e, n0, p0, nv;  // expert, first weight row, first routed row, routed rows
 };
 
-__device__ __forceinline__ int32_t row_tiles(int32_t cnt) { return (cnt + BT - 1) / BT; }
+// Up to BT rows are one tile; more are cut so that the tiles alternate halves.
+__device__ __forceinline__ int32_t row_tiles(int32_t cnt) {
+  return cnt <= BT ? (cnt + BT - 1) / BT : (cnt + BH - 1) / BH;
+}
 
 // Tile t, for a caller whose tiles only grow: e is the expert of its last one
 // (0 at first).  The next is usually a few experts on.
@@ -211,7 +210,6 @@ __device__ __forceinline__ Tile tile_info(int64_t t, const int32_t* off, const i
   d.n0 = nt * BM;
   d.p0 = off[e] + r * per;
   d.nv = min(per, cnt - r * per);
-  d.nh = d.nv <= BN ? d.nv : ((d.nv + 31) / 32) * 16;
   return d;
 }
 
@@ -282,9 +280,17 @@ __device__ __forceinline__ bool elect_one() {
   return v != 0;
 }
 
-// Barrier of the four warps of a scale group.
-__device__ __forceinline__ void group_sync(int group) {
-  asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+// Barrier of the four warps of a scale group; whether all of them say `ok` (so
+// that after a wait that ran out they leave together).
+__device__ __forceinline__ bool group_sync(int group, bool ok) {
+  uint32_t v;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n bar.red.and.pred q, %1, 128, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(v)
+      : "r"(1 + group), "r"((uint32_t)ok)
+      : "memory");
+  return v != 0;
 }
 
 // Eight scale bytes of a weight row, of which the first `valid` exist: rows have
@@ -365,7 +371,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
   }
   grid_dependency_wait();
   load_offsets_clamped(pb.offsets, E, pb.P, off_s, pb.err);
-  tile_prefix(off_s, E, BT, ntn, ts_s);
+  tile_prefix_of(off_s, E, ntn, ts_s, row_tiles);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -382,11 +388,10 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
       for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
         Tile d = tile_info(t, off_s, ts_s, E, at_e);
         d.nv = __shfl_sync(0xffffffffu, d.nv, 0);
-        d.nh = __shfl_sync(0xffffffffu, d.nh, 0);
         d.p0 = __shfl_sync(0xffffffffu, d.p0, 0);
         const int32_t wrow = __shfl_sync(0xffffffffu, (int32_t)((int64_t)d.e * N + d.n0), 0);
-        const int b0 = (d.nh + BOX - 1) / BOX, b1 = (d.nv - d.nh + BOX - 1) / BOX;
-        const uint32_t bytes = kABytes + (uint32_t)(b0 + b1) * (BOX * BKB);
+        const int boxes = (d.nv + BOX - 1) / BOX;
+        const uint32_t bytes = kABytes + (uint32_t)boxes * (BOX * BKB);
         for (int ks = 0; ks < NS; ++ks, ++g) {
           ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ph, abort, pb.err));
           if (!ok) break;
@@ -394,13 +399,11 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
             uint8_t* st = smem + s * kStageBytes;
             mbar_arrive_expect_tx(&full[s], bytes);
             tma_load_2d(st, &tmw, ks * BKB, wrow, &full[s]);
-            auto rows = [&](uint8_t* dst, int p0, int n) __attribute__((always_inline)) {
-              for (; n >= 2; n -= 2, dst += 2 * BOX * BKB, p0 += 2 * BOX)
-                tma_load_2d(dst, &tmx2, ks * BKB, p0, &full[s]);
-              if (n) tma_load_2d(dst, &tmx, ks * BKB, p0, &full[s]);
-            };
-            rows(st + kABytes, d.p0, b0);
-            if (b1) rows(st + kABytes + kBHalfBytes, d.p0 + d.nh, b1);
+            uint8_t* dst = st + kABytes;
+            int p0 = d.p0, n = boxes;
+            for (; n >= 2; n -= 2, dst += 2 * BOX * BKB, p0 += 2 * BOX)
+              tma_load_2d(dst, &tmx2, ks * BKB, p0, &full[s]);
+            if (n) tma_load_2d(dst, &tmx, ks * BKB, p0, &full[s]);
           }
           if (++s == ST) { s = 0; ph ^= 1u; }
         }
@@ -423,34 +426,24 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
       for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
         Tile d = tile_info(t, off_s, ts_s, E, at_e);
         d.nv = __shfl_sync(0xffffffffu, d.nv, 0);
-        d.nh = __shfl_sync(0xffffffffu, d.nh, 0);
-        const bool both = d.nv > BH, two = d.nv > BN;
+        const bool both = d.nv > BH;
         const uint32_t h0 = both ? 0u : acc.h;
-        const uint32_t n0 = (uint32_t)(d.nh + 15) & ~15u, n1 = (uint32_t)(d.nv - d.nh + 15) & ~15u;
-        const uint32_t i0 = idesc_mxf4(n0, 0), i1 = idesc_mxf4(n1, 0);
+        const uint32_t id = idesc_mxf4((uint32_t)(d.nv + 15) & ~15u, 0);
         constexpr uint32_t kUpper = (2u << 4) | (2u << 29);  // the scale words' upper halves
-        const uint32_t d0 = tmem + h0 * BH, d1 = tmem + BH;
+        const uint32_t d0 = tmem + h0 * BH;
         if (!(ok = all(mbar_wait(&acc_empty[h0], acc.phase(h0) ^ 1u, abort, pb.err)))) break;
-        if (both && !two && !(ok = all(mbar_wait(&acc_empty[1], acc.phase(1) ^ 1u, abort, pb.err)))) break;
+        if (both && !(ok = all(mbar_wait(&acc_empty[1], acc.phase(1) ^ 1u, abort, pb.err)))) break;
         for (int ks = 0; ks < NS; ++ks) {
           if (!(ok = all(mbar_wait(&full[s], ph, abort, pb.err)))) break;
-          if (two && ks == 0 && !(ok = all(mbar_wait(&acc_empty[1], acc.phase(1) ^ 1u, abort, pb.err)))) break;
           tc_fence_after();
           const uint64_t so = (uint64_t)((s * kStageBytes) >> 4);
           const uint64_t ad = adesc0 + so, bd = bdesc0 + so;
-          const uint64_t bd1 = bd + (uint64_t)(kBHalfBytes >> 4);
           const uint32_t sf = tmem + kSfCol + s * kSfSet;
           // the two 64-k steps of 128-k scale atom a
           auto atom = [&](int a, bool second) __attribute__((always_inline)) {
-            tc_mma_mxf4(d0, ad + 4 * a, bd + 4 * a, i0, sf + a * 4, sf + 8 + a * 8, a > 0 || ks > 0);
+            tc_mma_mxf4(d0, ad + 4 * a, bd + 4 * a, id, sf + a * 4, sf + 8 + a * 8, a > 0 || ks > 0);
             if (second)
-              tc_mma_mxf4(d0, ad + 4 * a + 2, bd + 4 * a + 2, i0 | kUpper, sf + a * 4, sf + 8 + a * 8, 1u);
-            if (two) {
-              tc_mma_mxf4(d1, ad + 4 * a, bd1 + 4 * a, i1, sf + a * 4, sf + 24 + a * 8, a > 0 || ks > 0);
-              if (second)
-                tc_mma_mxf4(d1, ad + 4 * a + 2, bd1 + 4 * a + 2, i1 | kUpper, sf + a * 4,
-                            sf + 24 + a * 8, 1u);
-            }
+              tc_mma_mxf4(d0, ad + 4 * a + 2, bd + 4 * a + 2, id | kUpper, sf + a * 4, sf + 8 + a * 8, 1u);
           };
           const int nk = (KB - ks * BKB + 31) / 32;  // 64-k steps left
           if (leader) {
@@ -482,7 +475,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
     // ---------------- scales ----------------
     // two groups of four warps take alternate stages: what bounds them is the
     // instructions of one stage.  Thread i of a group loads the scales of weight
-    // row i and routed rows i, i + 128, i + 256 of the tile, two stages ahead;
+    // row i and routed rows i, i + 128 of the tile, two stages ahead;
     // through shared memory every warp gets them all, since TMEM wants row r in
     // lane r % 32, column r / 32 of each of the four 32-lane quarters, and a warp
     // writes its own quarter.  (tcgen05.cp does the same from shared memory, but
@@ -491,34 +484,20 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
     const uint2 ones = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
     const uint8_t* wend = pb.ws + (int64_t)E * N * KS;
     const uint8_t* wp = nullptr;                    // the weight row's scales, or null
-    const uint32_t* xp[3] = {nullptr, nullptr, nullptr};  // the routed rows' first words, or null
-    int at[3] = {0, 0, 0};                          // their places in the scale area, or -1
-    bool wide = false;
+    const uint32_t* xp[2] = {nullptr, nullptr};     // the routed rows' first words, or null
     const int KA = (KS + 3) / 4;                    // words of a routed row
     int64_t t = blockIdx.x;                         // stage to load: tile and step
     int ks = 0;
     auto open = [&]() __attribute__((always_inline)) {
       const Tile d = tile_info(t, off_s, ts_s, E, at_e);
-      wide = d.nv > BN;
       wp = d.n0 + i < N ? pb.ws + ((int64_t)d.e * N + d.n0 + i) * KS : nullptr;
 #pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        int j = i + 128 * q, h = 0;
-        bool on = j < d.nv;
-        if (wide) {  // two MMAs: rows nh .. belong to the second half
-          h = j >= BH;
-          if (h) j -= BH;
-          on = j < (h ? d.nv - d.nh : d.nh);
-        }
-        xp[q] = on ? pb.xs + d.p0 + (h ? d.nh : 0) + j : nullptr;
-        at[q] = j < BN ? h * BH + j : -1;
-      }
+      for (int q = 0; q < 2; ++q) xp[q] = i + 128 * q < d.nv ? pb.xs + d.p0 + i + 128 * q : nullptr;
     };
-    // the scales of the group's next stage, and where they go
+    // the scales of the group's next stage
     RowScales w = {0, 0, 0, 0};
-    uint2 x[3] = {ones, ones, ones};
-    int to[3] = {0, 0, 0};
-    bool two = false, on = false;
+    uint2 x[2] = {ones, ones};
+    bool on = false;
     auto step = [&]() __attribute__((always_inline)) {  // to the next stage
       if (++ks == NS) {
         ks = 0;
@@ -529,14 +508,12 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
     auto load = [&]() __attribute__((always_inline)) {
       on = t < ntiles;
       if (!on) return;
-      two = wide;
       if (wp) w.load(wp + 8 * ks, KS - 8 * ks, pb.ws, wend);
       else w.valid = 0;
       const int64_t off = (int64_t)(2 * ks) * pb.P;
       const bool second = 2 * ks + 1 < KA;
 #pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        to[q] = at[q];
+      for (int q = 0; q < 2; ++q) {
         x[q] = ones;
         if (xp[q]) {
           x[q].x = __ldg(xp[q] + off);
@@ -551,18 +528,16 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
     if (group) step();
     load();
     while (on) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, abort, pb.err))) break;
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, abort, pb.err));
       tc_fence_after();
       // 8 bytes a row: 128 weight rows, then the routed rows
-      uint2* sf = reinterpret_cast<uint2*>(smem + s * kStageBytes + kABytes + 2 * kBHalfBytes);
-      sf[i] = w.get();
+      uint2* sf = reinterpret_cast<uint2*>(smem + s * kStageBytes + kABytes + kBBytes);
       uint2* sb = sf + BM;
+      sf[i] = w.get();
 #pragma unroll
-      for (int q = 0; q < 3; ++q)
-        if (to[q] >= 0) sb[to[q]] = x[q];
-      const bool split = two;
+      for (int q = 0; q < 2; ++q) sb[i + 128 * q] = x[q];
       load();
-      group_sync(group);
+      if (!group_sync(group, ok)) break;
       const uint32_t sc = tmem + (((uint32_t)warp & 3u) << 21) + kSfCol + s * kSfSet;
       {
         uint32_t r[8];
@@ -574,16 +549,15 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
         }
         tmem_store_8(sc, r);
       }
-      for (int h = 0; h < (split ? 2 : 1); ++h) {
+      {
         uint32_t r[16];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          // of two MMAs each has at most 192 rows: columns 6 and 7 go unused
-          const uint2 u = !split ? sb[c * 32 + lane] : c < 6 ? sb[h * BH + c * 32 + lane] : ones;
+          const uint2 u = sb[c * 32 + lane];
           r[c] = u.x;
           r[8 + c] = u.y;
         }
-        tmem_store_16(sc + 8 + h * 16, r);
+        tmem_store_16(sc + 8, r);
       }
       tc_fence_before();
       __syncwarp();
@@ -605,40 +579,37 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
     bool ok = true;
     for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
       const Tile d = tile_info(t, off_s, ts_s, E, at_e);
-      const bool both = d.nv > BH, two = d.nv > BN;
+      const bool both = d.nv > BH;
+      const uint32_t h = both ? 0u : acc.h;
+      ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[h], acc.phase(h), abort, pb.err));
+      if (ok && both)
+        ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[1], acc.phase(1), abort, pb.err));
+      if (!ok) break;
+      tc_fence_after();
       const int64_t n = d.n0 + (int64_t)(q * 32 + (lane & 30));
-      for (int part = 0; part < (two ? 2 : 1); ++part) {
-        const uint32_t h = both ? (uint32_t)part : acc.h;
-        ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[h], acc.phase(h), abort, pb.err));
-        if (ok && both && !two)
-          ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[1], acc.phase(1), abort, pb.err));
-        if (!ok) break;
-        tc_fence_after();
-        const int rows = part ? d.nv - d.nh : d.nh;
-        uint16_t* dst = pb.out + (int64_t)(d.p0 + (part ? d.nh : 0) + odd) * N + n;
-        const uint32_t taddr = tmem + ((q * 32u) << 16) + h * BH;
+      uint16_t* dst = pb.out + (int64_t)(d.p0 + odd) * N + n;
+      const uint32_t taddr = tmem + ((q * 32u) << 16) + h * BH;
 #pragma unroll 1
-        for (int c = mine * 32; c < rows; c += 64) {
-          uint32_t r[32];
-          tmem_load_32x32b_x32(taddr + c, r);
-          uint16_t* to = dst + (int64_t)c * N;
-          const int left = n < N ? rows - c - odd : 0;
+      for (int c = mine * 32; c < d.nv; c += 64) {
+        uint32_t r[32];
+        tmem_load_32x32b_x32(taddr + c, r);
+        uint16_t* to = dst + (int64_t)c * N;
+        const int left = n < N ? d.nv - c - odd : 0;
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const uint32_t a = pack_bf16x2(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
-            const uint32_t b = pack_bf16x2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
-            const uint32_t keep = prmt(a, b, keep_sel);
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, prmt(a, b, send_sel), 1);
-            if (j < left) *reinterpret_cast<uint32_t*>(to + j * N) = prmt(keep, got, lo_sel);
-            if (j + 2 < left) *reinterpret_cast<uint32_t*>(to + (j + 2) * N) = prmt(keep, got, hi_sel);
-          }
+        for (int j = 0; j < 32; j += 4) {
+          const uint32_t a = pack_bf16x2(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+          const uint32_t b = pack_bf16x2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
+          const uint32_t keep = prmt(a, b, keep_sel);
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, prmt(a, b, send_sel), 1);
+          if (j < left) *reinterpret_cast<uint32_t*>(to + j * N) = prmt(keep, got, lo_sel);
+          if (j + 2 < left) *reinterpret_cast<uint32_t*>(to + (j + 2) * N) = prmt(keep, got, hi_sel);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&acc_empty[h]);
-          if (both && !two) mbar_arrive(&acc_empty[1]);
-        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&acc_empty[h]);
+        if (both) mbar_arrive(&acc_empty[1]);
       }
       acc.next(both);
     }

@@ -476,11 +476,12 @@ __device__ __forceinline__ void grid_launch_dependents() {
 }
 
 // ts[e] = sum over experts e' < e of tiles(e'), ts[E] = total, where
-// tiles(e) = per_tile_n * ceil(count(e) / rows_per_tile).  Warp 0 scans 32
-// experts at a time with shuffles; the block must sync afterwards.
-__device__ __forceinline__ void tile_prefix(const int32_t* off_s, int32_t E,
-                                            int32_t rows_per_tile,
-                                            int32_t per_tile_n, int32_t* ts) {
+// tiles(e) = per_tile_n * row_tiles(count(e)).  Warp 0 scans 32 experts at a
+// time with shuffles; the block must sync afterwards.
+template <typename RowTiles>
+__device__ __forceinline__ void tile_prefix_of(const int32_t* off_s, int32_t E,
+                                               int32_t per_tile_n, int32_t* ts,
+                                               RowTiles row_tiles) {
   if (threadIdx.x >= 32) return;
   const int lane = threadIdx.x;
   int32_t carry = 0;
@@ -489,7 +490,7 @@ __device__ __forceinline__ void tile_prefix(const int32_t* off_s, int32_t E,
     int32_t v = 0;
     if (e < E) {
       const int32_t cnt = off_s[e + 1] - off_s[e];
-      v = per_tile_n * ((cnt + rows_per_tile - 1) / rows_per_tile);
+      v = per_tile_n * row_tiles(cnt);
     }
     int32_t incl = v;
 #pragma unroll
@@ -501,6 +502,15 @@ __device__ __forceinline__ void tile_prefix(const int32_t* off_s, int32_t E,
     carry += __shfl_sync(0xffffffffu, incl, 31);
   }
   if (lane == 0) ts[E] = carry;
+}
+
+// The same with row_tiles(count) = ceil(count / rows_per_tile).
+__device__ __forceinline__ void tile_prefix(const int32_t* off_s, int32_t E,
+                                            int32_t rows_per_tile,
+                                            int32_t per_tile_n, int32_t* ts) {
+  tile_prefix_of(off_s, E, per_tile_n, ts, [=](int32_t cnt) {
+    return (cnt + rows_per_tile - 1) / rows_per_tile;
+  });
 }
 
 // Expert whose row range holds row p (binary search, p in [0, P)).
