@@ -10,7 +10,8 @@
 //             the products of 32-blocks and their two scales are exact in the
 //             tensor core, the sum is fp32, one rounding to bf16
 //
-// Quantise is bound by memory: 4 lanes share a 32-block, 16-byte loads.
+// Quantise is bound by the instructions of its conversion, at about three
+// quarters of the memory rate.
 //
 // Product, one persistent CTA per SM, 20 warps ("swap AB": MMA M is 128
 // weight rows, MMA N the routed rows of one expert, so few rows give a narrow
@@ -60,73 +61,72 @@ __device__ __forceinline__ void unpack8(uint4 q, float (&v)[8]) {
   }
 }
 
-// A warp quantises one row, 8 values a lane; the 4 lanes of a 32-block share
-// its maximum.  The scale bytes of 128 k are one word, word (k / 128) * P + p: a
-// block's eight rows meet in shared memory, so that whole 32-byte sectors are
-// written (single bytes from each warp took 13 us for 8192 x 2880 where this
-// takes GBW_T us).
-constexpr int kQRows = 8;      // warps, and rows at a time, of a block
-constexpr int kQUnits = 512;   // 8-value units of a row between two barriers
+// A warp quantises kUnits * 256 values of a row, 8 a lane and unit; the 4 lanes
+// of a 32-block share its maximum.  The scale bytes of 128 k are one word, word
+// (k / 128) * P + p; a block's warps take neighbouring rows, whose words share a
+// sector.  8192 rows of 2880 take 12.8 us, 4004 SwiGLU rows 13.1 (5 and 4 TB/s
+// in and out); rows by whole warps took 12.1 and 14.3, one unit a warp 16.8 and
+// 14.3, six 12.3 and 13.1, but 2.7 instead of 2.3 us for a few rows.
+constexpr int kQRows = 4;  // warps, and rows, of a block
+template <bool kGLU>
+constexpr int kUnits = kGLU ? 2 : 4;  // loaded before the first is used
 template <bool kGLU>
 __global__ void __launch_bounds__(32 * kQRows) quantize_rows_kernel(
     const uint16_t* __restrict__ x, int64_t T, int K, const int32_t* __restrict__ r2t, int64_t P,
     uint8_t* __restrict__ codes, uint32_t* __restrict__ scales, int* err) {
-  __shared__ uint32_t words[kQUnits / 16][kQRows];
+  constexpr int NB = kUnits<kGLU>;
   grid_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, U = K / 8, KA = (K + 127) / 128;
-  for (int64_t p0 = (int64_t)blockIdx.x * kQRows; p0 < P; p0 += (int64_t)gridDim.x * kQRows) {
-    const int64_t p = p0 + warp;
-    const bool on = p < P;
-    const int64_t t = on ? token_of_row(r2t, (int32_t)p, T, lane == 0 ? err : nullptr) : 0;
-    const uint4* row = reinterpret_cast<const uint4*>(x + t * K * (kGLU ? 2 : 1));
-    uint32_t* out = reinterpret_cast<uint32_t*>(codes) + p * U;
-    for (int base = 0; base < U; base += kQUnits) {
-      const int stop = on ? min(base + kQUnits, (U + 31) & ~31) : base;
-#pragma unroll 4
-      for (int c = base + lane; c < stop; c += 32) {
-        float v[8];
+  const int lane = threadIdx.x & 31, U = K / 8, KA = (K + 127) / 128;
+  const int64_t p = (int64_t)blockIdx.x * kQRows + (threadIdx.x >> 5);
+  if (p >= P) return;
+  const int64_t t = token_of_row(r2t, (int32_t)p, T, lane == 0 ? err : nullptr);
+  const uint4* row = reinterpret_cast<const uint4*>(x + t * K * (kGLU ? 2 : 1));
+  uint32_t* out = reinterpret_cast<uint32_t*>(codes) + p * U;
+  const int c0 = blockIdx.y * (32 * NB) + lane;
+  uint4 g[NB], u[kGLU ? NB : 1];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        if (c < U) {
-          unpack8(__ldg(row + c), v);
-          if (kGLU) {
-            float u[8];
-            unpack8(__ldg(row + U + c), u);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __fdividef(v[j], 1.0f + __expf(-v[j])) * u[j];
-          }
-        }
-        uint32_t m = 0;  // magnitudes order as their bits do, NaN and inf on top
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const uint32_t ex = m >> 23;
-        uint32_t byte = ex > 2u ? ex - 2u : 0u;
-        uint32_t q = 0;
-        if (ex == 255u) {
-          byte = 255u;  // a value that is not finite: the block is NaN
-        } else if (m) {
-          const float inv = __uint_as_float((254u - byte) << 23);  // 2^-X
-#pragma unroll
-          for (int j = 0; j < 4; ++j) q |= e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv) << (8 * j);
-        }
-        if (c < U) out[c] = q;
-        if (c >= U) byte = 127u;  // blocks of a word past the row: 2^0
-        // the four blocks of 16 lanes make a word
-        uint32_t w = byte << (8 * ((lane >> 2) & 3));
-        w |= __shfl_xor_sync(0xffffffffu, w, 4);
-        w |= __shfl_xor_sync(0xffffffffu, w, 8);
-        if ((lane & 15) == 0) words[(c - base) >> 4][warp] = w;
-      }
-      __syncthreads();
-      const int n = min(kQUnits / 16, KA - base / 16);
-      for (int i = threadIdx.x; i < n * kQRows; i += 32 * kQRows) {
-        const int a = i / kQRows, r = i % kQRows;
-        if (p0 + r < P) scales[(int64_t)(base / 16 + a) * P + p0 + r] = words[a][r];
-      }
-      __syncthreads();
+  for (int i = 0; i < NB; ++i) {
+    const int c = c0 + 32 * i;
+    g[i] = make_uint4(0, 0, 0, 0);
+    if (kGLU) u[i] = make_uint4(0, 0, 0, 0);
+    if (c < U) {
+      g[i] = __ldg(row + c);
+      if (kGLU) u[i] = __ldg(row + U + c);
     }
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int c = c0 + 32 * i;
+    float v[8];
+    unpack8(g[i], v);
+    if (kGLU) {
+      float w[8];
+      unpack8(u[i], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __fdividef(v[j], 1.0f + __expf(-v[j])) * w[j];
+    }
+    uint32_t m = 0;  // magnitudes order as their bits do, NaN and inf on top
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const uint32_t ex = m >> 23;
+    uint32_t byte = ex > 2u ? ex - 2u : 0u;
+    uint32_t q = 0;
+    if (ex == 255u) {
+      byte = 255u;  // a value that is not finite: the block is NaN
+    } else if (m) {
+      const float inv = __uint_as_float((254u - byte) << 23);  // 2^-X
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q |= e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv) << (8 * j);
+    }
+    if (c < U) out[c] = q;
+    if (c >= U) byte = 127u;  // blocks of a word past the row: 2^0
+    // the four blocks of 16 lanes make a word
+    uint32_t w = byte << (8 * ((lane >> 2) & 3));
+    w |= __shfl_xor_sync(0xffffffffu, w, 4);
+    w |= __shfl_xor_sync(0xffffffffu, w, 8);
+    if ((lane & 15) == 0 && c < KA * 16) scales[(int64_t)(c >> 4) * P + p] = w;
   }
 }
 
@@ -624,15 +624,16 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
 
 cudaError_t launch_quantize_rows(const uint16_t* x, int64_t T, int64_t K, const int32_t* r2t,
                                  int64_t P, bool glu, uint8_t* codes, uint8_t* scales, int* err,
-                                 int num_sms, cudaStream_t s) {
+                                 cudaStream_t s) {
   if (P == 0) return cudaSuccess;
-  const int64_t need = (P + kQRows - 1) / kQRows, most = 64 * (int64_t)num_sms;
-  const int grid = (int)(need < most ? need : most);
   uint32_t* words = reinterpret_cast<uint32_t*>(scales);
-  return glu ? launch_kernel<quantize_rows_kernel<true>>(grid, 32 * kQRows, 0, s, false, x, T, (int)K,
-                                                         r2t, P, codes, words, err)
-             : launch_kernel<quantize_rows_kernel<false>>(grid, 32 * kQRows, 0, s, false, x, T, (int)K,
-                                                          r2t, P, codes, words, err);
+  auto grid = [&](int64_t units) {
+    return dim3((unsigned)((P + kQRows - 1) / kQRows), (unsigned)((K + 256 * units - 1) / (256 * units)));
+  };
+  return glu ? launch_kernel<quantize_rows_kernel<true>>(grid(kUnits<true>), 32 * kQRows, 0, s, false, x,
+                                                         T, (int)K, r2t, P, codes, words, err)
+             : launch_kernel<quantize_rows_kernel<false>>(grid(kUnits<false>), 32 * kQRows, 0, s, false, x,
+                                                          T, (int)K, r2t, P, codes, words, err);
 }
 
 cudaError_t launch_gemm_a4(const uint8_t* xq, const uint8_t* xs, int64_t P, int64_t K,

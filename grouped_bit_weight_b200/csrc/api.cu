@@ -527,7 +527,8 @@ gbw_status gmxfp4_quantize_rows(const uint16_t* x, int64_t T, int64_t K,
                                 uint8_t* codes, uint8_t* scales, void* stream) {
   if (T < 0 || K <= 0 || P < 0) return fail(GBW_ERR_SHAPE, "need T >= 0, K > 0, P >= 0");
   if (K % 32) return fail(GBW_ERR_SHAPE, "MXFP4 needs K % 32 == 0");
-  if (K > (int64_t)1 << 30 || P > INT32_MAX || T > INT32_MAX)
+  if (K > (int64_t)1 << 24) return fail(GBW_ERR_SHAPE, "K must be at most 2^24");
+  if (P > INT32_MAX || T > INT32_MAX)
     return fail(GBW_ERR_SHAPE, "sizes exceed the 32-bit row indices");
   if (!row_to_token && T < P) return fail(GBW_ERR_SHAPE, "row_to_token == NULL needs T >= P");
   if (row_to_token && P > 0 && T < 1) return fail(GBW_ERR_SHAPE, "T must be >= 1");
@@ -540,7 +541,7 @@ gbw_status gmxfp4_quantize_rows(const uint16_t* x, int64_t T, int64_t K,
   gbw_status st = device_state(&err, &sms);
   if (st != GBW_OK) return st;
   const cudaError_t e = launch_quantize_rows(x, T, K, row_to_token, P, swiglu != 0, codes, scales,
-                                             err, sms, static_cast<cudaStream_t>(stream));
+                                             err, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? GBW_OK : launch_error(e);
 }
 

@@ -29,13 +29,13 @@ cudaError_t opt_in_smem(size_t smem) {
 // the stream finishes (programmatic dependent launch): Fn then calls
 // grid_dependency_wait() before it touches what that kernel writes.
 template <auto Fn, typename... Args>
-cudaError_t launch_kernel(int grid, int block, size_t smem, cudaStream_t s, bool dependent,
+cudaError_t launch_kernel(dim3 grid, int block, size_t smem, cudaStream_t s, bool dependent,
                           Args... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -102,7 +102,7 @@ cudaError_t launch_layer(Fmt f, const LayerProblem& p, void* workspace, int num_
 // rows [2K]) to MXFP4, and the grouped product of MXFP4 rows and weights.
 cudaError_t launch_quantize_rows(const uint16_t* x, int64_t T, int64_t K, const int32_t* r2t,
                                  int64_t P, bool glu, uint8_t* codes, uint8_t* scales, int* err,
-                                 int num_sms, cudaStream_t s);
+                                 cudaStream_t s);
 cudaError_t launch_gemm_a4(const uint8_t* xq, const uint8_t* xs, int64_t P, int64_t K,
                            const uint8_t* w, const uint8_t* ws, int32_t E, int64_t N,
                            const int32_t* offsets, uint16_t* out, int* err, int num_sms,

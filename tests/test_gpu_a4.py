@@ -303,7 +303,7 @@ def test_a4_host_validation():
 
     def q(x=p, T=4, K=64, r2t=None, P=4, codes=p, scales=p):
         return L.gmxfp4_quantize_rows(x, T, K, r2t, P, 0, codes, scales, None)
-    assert q(K=48) == SHAPE and q(T=3) == SHAPE and q(P=-1) == SHAPE and q(T=0, r2t=p) == SHAPE
+    assert q(K=48) == SHAPE and q(K=(1 << 24) + 32) == SHAPE and q(T=3) == SHAPE and q(P=-1) == SHAPE and q(T=0, r2t=p) == SHAPE
     assert q(x=None) == NULL and q(scales=None) == NULL
     assert q(x=C.c_void_p(24)) == ALIGN and q(codes=C.c_void_p(18)) == ALIGN
 

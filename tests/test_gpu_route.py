@@ -328,3 +328,11 @@ def test_route_and_combine_host_validation():
     assert L.gmoe_combine_bwd(p, p, 8, 64, p, p, None, 4, 2, p, p, None) == NULL
     assert L.gmoe_combine_bwd(p, p, 8, 64, p, p, p, 4, 2, C.c_void_p(24), p, None) == ALIGN
     assert L.gmoe_route_bwd(None, 0, 4, 8, 2, 0, p, p, p, p, None) == NULL
+
+
+@pytest.mark.gpu
+def test_a_routing_can_be_saved(tmp_path):
+    r = gbw.gmoe_route(torch.randn((200, 16), generator=torch.Generator().manual_seed(0)).to(DEV), 4)
+    torch.save(tuple(r), tmp_path / "r.pt")
+    for a, b in zip(r, torch.load(tmp_path / "r.pt")):
+        assert torch.equal(a, b)
