@@ -52,6 +52,13 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
   return d;
 }
 
+// The two values of a byte of codes.
+__device__ __forceinline__ float2 e2m1_values(uint32_t byte) {
+  uint32_t h;
+  asm("{\n .reg .b8 t;\n cvt.u8.u32 t, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n" : "=r"(h) : "r"(byte));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
 __device__ __forceinline__ void unpack8(uint4 q, float (&v)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -130,6 +137,76 @@ __global__ void __launch_bounds__(32 * kQRows) quantize_rows_kernel(
   }
 }
 
+// Sixteen bits in four-bit pieces: v = sum over j < 8 of piece j, each an MXFP4
+// row of its own.  Piece j quantises what pieces 0 .. j - 1 left, exactly
+// known in fp32; a piece leaves at most a quarter of its block's maximum (1 of
+// [4, 6], less than 2 of [6, 8)), so eight leave 2^-16 of it.
+constexpr int kPieces = 8;
+
+// A warp takes 256 values of a row, as above.  kGLU: fp32 rows [2K], silu(gate)
+// * up; else bf16 rows gathered through r2t.  Codes [P * 8, K / 2] and scale
+// words [ceil(K / 128)][P * 8]: row p's pieces are rows 8 p ..
+template <bool kGLU>
+__global__ void __launch_bounds__(32 * kQRows) quantize_pieces_kernel(
+    const void* __restrict__ x, int64_t T, int K, const int32_t* __restrict__ r2t, int64_t P,
+    uint8_t* __restrict__ codes, uint32_t* __restrict__ scales, int* err) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31, U = K / 8;
+  const int64_t p = (int64_t)blockIdx.x * kQRows + (threadIdx.x >> 5);
+  if (p >= P) return;
+  const int c = blockIdx.y * 32 + lane;
+  float v[8] = {};
+  if (kGLU) {
+    if (c < U) {
+      const float4* g = reinterpret_cast<const float4*>(static_cast<const float*>(x) + p * 2 * K) + 2 * c;
+      const float4 a = __ldcg(g), b = __ldcg(g + 1), d = __ldcg(g + K / 4), e = __ldcg(g + K / 4 + 1);
+      const float gate[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      const float up[8] = {d.x, d.y, d.z, d.w, e.x, e.y, e.z, e.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __fdividef(gate[j], 1.0f + __expf(-gate[j])) * up[j];
+    }
+  } else {
+    const int64_t t = token_of_row(r2t, (int32_t)p, T, lane == 0 ? err : nullptr);
+    if (c < U) unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + t * K) + c), v);
+  }
+  uint32_t* out = reinterpret_cast<uint32_t*>(codes) + p * kPieces * U + c;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const uint32_t ex = m >> 23;
+    uint32_t byte = ex > 2u ? ex - 2u : 0u;
+    uint32_t q = 0;
+    if (ex == 255u) {
+      byte = 255u;  // a value that is not finite: the block is NaN, by its first piece
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    } else if (m) {
+      const float inv = __uint_as_float((254u - byte) << 23);
+      const float back = byte ? __uint_as_float(byte << 23) : __uint_as_float(0x00400000u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t two = e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv);
+        const float2 was = e2m1_values(two);
+        v[2 * j] = fmaf(-was.x, back, v[2 * j]);
+        v[2 * j + 1] = fmaf(-was.y, back, v[2 * j + 1]);
+        q |= two << (8 * j);
+      }
+    }
+    if (c < U) out[i * U] = q;
+    if (c >= U) byte = 127u;
+    uint32_t w = byte << (8 * ((lane >> 2) & 3));
+    w |= __shfl_xor_sync(0xffffffffu, w, 4);
+    w |= __shfl_xor_sync(0xffffffffu, w, 8);
+    if ((lane & 15) == 0 && c < (K + 127) / 128 * 16)
+      scales[(int64_t)(c >> 4) * (P * kPieces) + p * kPieces + i] = w;
+  }
+}
+
 // ----------------------------------------------------------------------
 // product
 // ----------------------------------------------------------------------
@@ -168,7 +245,7 @@ struct A4Problem {
   int64_t P, K, N;
   int32_t E;
   const int32_t* offsets;  // [E + 1]
-  uint16_t* out;           // [P, N] bf16
+  void* out;               // [P, N] bf16; of rows in pieces [P / 8, N] fp32
   int* err;
 };
 
@@ -328,6 +405,8 @@ struct RowScales {
   }
 };
 
+// R: rows of x that make one of the output, 1 or kPieces.
+template <int R>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
                const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmx2) {
@@ -370,7 +449,11 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
     tma_prefetch_desc(&tmx2);
   }
   grid_dependency_wait();
-  load_offsets_clamped(pb.offsets, E, pb.P, off_s, pb.err);
+  load_offsets_clamped(pb.offsets, E, pb.P / R, off_s, pb.err);
+  if (R > 1) {
+    for (int i = threadIdx.x; i <= E; i += kThreads) off_s[i] *= R;
+    __syncthreads();
+  }
   tile_prefix_of(off_s, E, ntn, ts_s, row_tiles);
   tc_fence_before();
   __syncthreads();
@@ -586,13 +669,24 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
         ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[1], acc.phase(1), abort, pb.err));
       if (!ok) break;
       tc_fence_after();
-      const int64_t n = d.n0 + (int64_t)(q * 32 + (lane & 30));
-      uint16_t* dst = pb.out + (int64_t)(d.p0 + odd) * N + n;
+      const int64_t n = d.n0 + (int64_t)(q * 32 + (R > 1 ? lane : lane & 30));
+      uint16_t* dst = static_cast<uint16_t*>(pb.out) + (int64_t)(d.p0 + odd) * N + n;
+      float* sums = static_cast<float*>(pb.out) + (int64_t)(d.p0 / R) * N + n;
       const uint32_t taddr = tmem + ((q * 32u) << 16) + h * BH;
 #pragma unroll 1
       for (int c = mine * 32; c < d.nv; c += 64) {
         uint32_t r[32];
         tmem_load_32x32b_x32(taddr + c, r);
+        if (R > 1) {  // a row's pieces, the smallest first
+#pragma unroll
+          for (int j = 0; j < 32; j += R) {
+            float v = __uint_as_float(r[j + R - 1]);
+#pragma unroll
+            for (int i = R - 2; i >= 0; --i) v += __uint_as_float(r[j + i]);
+            if (n < N && c + j < d.nv) sums[(int64_t)((c + j) / R) * N] = v;
+          }
+          continue;
+        }
         uint16_t* to = dst + (int64_t)c * N;
         const int left = n < N ? d.nv - c - odd : 0;
 #pragma unroll
@@ -636,9 +730,22 @@ cudaError_t launch_quantize_rows(const uint16_t* x, int64_t T, int64_t K, const 
                                                           T, (int)K, r2t, P, codes, words, err);
 }
 
-cudaError_t launch_gemm_a4(const uint8_t* xq, const uint8_t* xs, int64_t P, int64_t K,
+cudaError_t launch_quantize_pieces(const void* x, int64_t T, int64_t K, const int32_t* r2t, int64_t P,
+                                   bool glu, uint8_t* codes, uint32_t* scales, int* err,
+                                   cudaStream_t s) {
+  const dim3 grid((unsigned)((P + kQRows - 1) / kQRows), (unsigned)((K + 255) / 256));
+  return glu ? launch_kernel<quantize_pieces_kernel<true>>(grid, 32 * kQRows, 0, s, true, x, T, (int)K,
+                                                           r2t, P, codes, scales, err)
+             : launch_kernel<quantize_pieces_kernel<false>>(grid, 32 * kQRows, 0, s, true, x, T, (int)K,
+                                                            r2t, P, codes, scales, err);
+}
+
+namespace {
+
+template <int R>
+cudaError_t launch_gemm_t(const uint8_t* xq, const uint8_t* xs, int64_t P, int64_t K,
                            const uint8_t* w, const uint8_t* ws, int32_t E, int64_t N,
-                           const int32_t* offsets, uint16_t* out, int* err, int num_sms,
+                           const int32_t* offsets, void* out, int* err, int num_sms,
                            cudaStream_t s) {
   if (P == 0) return cudaSuccess;
   CUtensorMap tmw, tmx;
@@ -655,10 +762,27 @@ cudaError_t launch_gemm_a4(const uint8_t* xq, const uint8_t* xs, int64_t P, int6
   if (e != cudaSuccess) return e;
   const A4Problem pb{reinterpret_cast<const uint32_t*>(xs), ws, P, K, N, E, offsets, out, err};
   constexpr size_t most = 1024 + Smem::tables + 8 * (1024 + 1);
-  e = opt_in_smem<gemm_a4_kernel>(most);
+  e = opt_in_smem<gemm_a4_kernel<R>>(most);
   if (e != cudaSuccess) return e;
   const size_t smem = 1024 + Smem::tables + 8 * (size_t)(E + 1);
-  return launch_kernel<gemm_a4_kernel>(num_sms, kThreads, smem, s, true, pb, tmw, tmx, tmx2);
+  return launch_kernel<gemm_a4_kernel<R>>(num_sms, kThreads, smem, s, true, pb, tmw, tmx, tmx2);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_a4(const uint8_t* xq, const uint8_t* xs, int64_t P, int64_t K,
+                           const uint8_t* w, const uint8_t* ws, int32_t E, int64_t N,
+                           const int32_t* offsets, uint16_t* out, int* err, int num_sms,
+                           cudaStream_t s) {
+  return launch_gemm_t<1>(xq, xs, P, K, w, ws, E, N, offsets, out, err, num_sms, s);
+}
+
+cudaError_t launch_gemm_pieces(const uint8_t* xq, const uint32_t* xs, int64_t P, int64_t K,
+                               const uint8_t* w, const uint8_t* ws, int32_t E, int64_t N,
+                               const int32_t* offsets, float* out, int* err, int num_sms,
+                               cudaStream_t s) {
+  return launch_gemm_t<kPieces>(xq, reinterpret_cast<const uint8_t*>(xs), P * kPieces, K, w, ws, E, N,
+                                offsets, out, err, num_sms, s);
 }
 
 }  // namespace gbw

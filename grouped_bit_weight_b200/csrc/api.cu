@@ -377,7 +377,7 @@ gbw_status gmoe_route(const void* logits, int32_t logits_type, int64_t T, int32_
   const RouteProblem p{logits, logits_type == GBW_LOGITS_FP32, T, E, k, renormalize != 0, topk_ids,
                        topk_weights, expert_offsets, row_to_token, row_of_slot, slot_of_row,
                        static_cast<int32_t*>(workspace)};
-  const cudaError_t e = launch_route(p, sms, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_route(p, sms, false, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? GBW_OK : launch_error(e);
 }
 

@@ -66,7 +66,8 @@ struct RouteProblem {
 // rows of its histogram workspace: at most kMaxRouteCtas.
 constexpr int kMaxRouteCtas = 160;
 int route_ctas(int64_t T, int num_sms);
-cudaError_t launch_route(const RouteProblem& p, int num_sms, cudaStream_t s);
+// dependent: started behind the kernel before it, for which it waits
+cudaError_t launch_route(const RouteProblem& p, int num_sms, bool dependent, cudaStream_t s);
 cudaError_t launch_route_bwd(const void* logits, int32_t fp32, int64_t T, int32_t E, int32_t k,
                              int32_t renorm, const int32_t* ids, const float* weights,
                              const float* dweights, void* dlogits, int* err, int num_sms,
@@ -74,6 +75,10 @@ cudaError_t launch_route_bwd(const void* logits, int32_t fp32, int64_t T, int32_
 cudaError_t launch_combine(const uint16_t* y, int64_t P, int64_t H, const int32_t* row_of_slot,
                            const float* weights, int64_t T, int32_t k, uint16_t* out, int* err,
                            int num_sms, cudaStream_t s);
+// fp32 rows, started behind the kernel before it
+cudaError_t launch_combine_f32(const float* y, int64_t P, int64_t H, const int32_t* row_of_slot,
+                               const float* weights, int64_t T, int32_t k, uint16_t* out, int* err,
+                               int num_sms, cudaStream_t s);
 cudaError_t launch_combine_bwd(const uint16_t* dout, const uint16_t* y, int64_t P, int64_t H,
                                const int32_t* row_of_slot, const int32_t* slot_of_row,
                                const float* weights, int64_t T, int32_t k, uint16_t* dy,
@@ -107,5 +112,18 @@ cudaError_t launch_gemm_a4(const uint8_t* xq, const uint8_t* xs, int64_t P, int6
                            const uint8_t* w, const uint8_t* ws, int32_t E, int64_t N,
                            const int32_t* offsets, uint16_t* out, int* err, int num_sms,
                            cudaStream_t s);
+
+// The same for rows in eight 4-bit pieces each (16 bits of a block's maximum):
+// bf16 rows gathered through r2t, or silu(gate) * up of fp32 rows [2K], to codes
+// [P * 8, K / 2] and scale words [ceil(K / 128)][P * 8]; their product with MXFP4
+// weights, summed over the pieces in fp32, [P, N].  Both start behind the kernel
+// before them and wait for it.
+cudaError_t launch_quantize_pieces(const void* x, int64_t T, int64_t K, const int32_t* r2t, int64_t P,
+                                   bool glu, uint8_t* codes, uint32_t* scales, int* err,
+                                   cudaStream_t s);
+cudaError_t launch_gemm_pieces(const uint8_t* xq, const uint32_t* xs, int64_t P, int64_t K,
+                               const uint8_t* w, const uint8_t* ws, int32_t E, int64_t N,
+                               const int32_t* offsets, float* out, int* err, int num_sms,
+                               cudaStream_t s);
 
 }  // namespace gbw

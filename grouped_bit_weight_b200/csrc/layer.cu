@@ -94,7 +94,7 @@ struct LayerArgs {
   uint16_t* hhi;      // [P, I] bf16
   uint16_t* hlo;      // [P, I] bf16
   float* y;           // [P, H]
-  int* counters;      // claimA, claimB, doneA, then one per 16 columns of H
+  int* counters;      // claimA, claimB, doneA, then one per 16 columns of H; or null
 };
 
 constexpr int kCounters = 4;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router(const LayerArgs a) 
   const LayerProblem& p = a.p;
   __shared__ float part[kRouterThreads / 32][kRouterTokens];
   grid_launch_dependents();
-  if (blockIdx.x == 0 && blockIdx.y == 0)
+  if (a.counters && blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = threadIdx.x; i < kCounters + (int)(p.H / 16); i += blockDim.x) a.counters[i] = 0;
   const int e = blockIdx.x, t0 = blockIdx.y * kRouterTokens;
   const int n = min(kRouterTokens, (int)p.T - t0);
@@ -333,8 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
   for (int t = warp; t < T; t += kWarps + 1) {
     int id = 0;
     float w = 0.0f;
-    choose<LogitL2, NPL>(reinterpret_cast<const LogitL2*>(a.logits) + (int64_t)t * E, E, k, p.renorm,
-                         lane, id, w);
+    choose<float, NPL>(a.logits + (int64_t)t * E, E, k, p.renorm, lane, id, w);
     if (lane < k) {
       ids[t * k + lane] = id;
       wts[t * k + lane] = w;
@@ -992,16 +991,18 @@ Layout layout_of(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I) {
   return l;
 }
 
+cudaError_t launch_router(const LayerArgs& a, cudaStream_t s) {
+  const dim3 grid((unsigned)a.p.E, (unsigned)((a.p.T + kRouterTokens - 1) / kRouterTokens));
+  const int threads = (int)std::min<int64_t>(kRouterThreads, (a.p.H / 8 + 31) / 32 * 32);
+  return launch_kernel<moe_router>(grid, threads, 0, s, false, a);
+}
+
 template <Fmt F, int NPL>
 cudaError_t launch_t(const LayerArgs& a, int num_sms, cudaStream_t s) {
   constexpr auto k = moe_experts<F, NPL>;
   cudaError_t e = opt_in_smem<k>(Smem::bytes);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.p.E, (unsigned)((a.p.T + kRouterTokens - 1) / kRouterTokens));
-  cfg.blockDim = dim3((unsigned)std::min<int64_t>(kRouterThreads, (a.p.H / 8 + 31) / 32 * 32));
-  cfg.stream = s;
-  e = cudaLaunchKernelEx(&cfg, moe_router, a);
+  e = launch_router(a, s);
   if (e != cudaSuccess) return e;
   // Whole tiles of H per CTA in phase B spare the counting of a tile's experts
   // across CTAs (about 1.5 us) but leave the last round of tiles uneven: taken
@@ -1026,17 +1027,90 @@ cudaError_t launch_f(const LayerArgs& a, int num_sms, cudaStream_t s) {
   return a.p.E <= 128 ? launch_t<F, 4>(a, num_sms, s) : launch_t<F, kMaxE / 32>(a, num_sms, s);
 }
 
+// ----------------------------------------------------------------------
+// MXFP4, more tokens: the layer in seven launches on the tensor cores' 4-bit path
+// ----------------------------------------------------------------------
+
+struct PiecesLayout {
+  int64_t logits, ids, weights, offsets, r2t, ros, sor, xq, xs, gu, hq, hs, y, total;
+};
+
+PiecesLayout pieces_layout(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I) {
+  const int64_t P = T * k;
+  PiecesLayout l = {};
+  auto put = [&](int64_t& at, int64_t bytes) {
+    at = l.total;
+    l.total += (bytes + 255) & ~(int64_t)255;
+  };
+  put(l.logits, T * E * 4);
+  put(l.ids, P * 4);
+  put(l.weights, P * 4);
+  put(l.offsets, (E + 1) * 4);
+  put(l.r2t, P * 4);
+  put(l.ros, P * 4);
+  put(l.sor, P * 4);
+  put(l.xq, P * 8 * (H / 2));
+  put(l.xs, P * 8 * ((H + 127) / 128) * 4);
+  put(l.gu, P * 2 * I * 4);
+  put(l.hq, P * 8 * (I / 2));
+  put(l.hs, P * 8 * ((I + 127) / 128) * 4);
+  put(l.y, P * H * 4);
+  return l;
+}
+
+cudaError_t launch_pieces(const LayerProblem& p, uint8_t* w, int num_sms, cudaStream_t s) {
+  const PiecesLayout l = pieces_layout(p.T, p.E, p.k, p.H, p.I);
+  const int64_t P = p.T * p.k;
+  auto ints = [&](int64_t at) { return reinterpret_cast<int32_t*>(w + at); };
+  auto floats = [&](int64_t at) { return reinterpret_cast<float*>(w + at); };
+  auto words = [&](int64_t at) { return reinterpret_cast<uint32_t*>(w + at); };
+  const LayerArgs a{p, floats(l.logits), nullptr, nullptr, nullptr, nullptr};
+  RouteProblem r = {};
+  r.logits = floats(l.logits);
+  r.fp32 = 1;
+  r.T = p.T;
+  r.E = p.E;
+  r.k = p.k;
+  r.renorm = p.renorm;
+  r.ids = ints(l.ids);
+  r.weights = floats(l.weights);
+  r.offsets = ints(l.offsets);
+  r.row_to_token = ints(l.r2t);
+  r.row_of_slot = ints(l.ros);
+  r.slot_of_row = ints(l.sor);
+  cudaError_t e = launch_router(a, s);
+  if (e != cudaSuccess) return e;
+  e = launch_route(r, num_sms, true, s);
+  if (e != cudaSuccess) return e;
+  e = launch_quantize_pieces(p.x, p.T, p.H, r.row_to_token, P, false, w + l.xq, words(l.xs), p.err, s);
+  if (e != cudaSuccess) return e;
+  e = launch_gemm_pieces(w + l.xq, words(l.xs), P, p.H, p.gu, static_cast<const uint8_t*>(p.gu_scale),
+                         p.E, 2 * p.I, r.offsets, floats(l.gu), p.err, num_sms, s);
+  if (e != cudaSuccess) return e;
+  e = launch_quantize_pieces(floats(l.gu), P, p.I, nullptr, P, true, w + l.hq, words(l.hs), p.err, s);
+  if (e != cudaSuccess) return e;
+  e = launch_gemm_pieces(w + l.hq, words(l.hs), P, p.I, p.dn, static_cast<const uint8_t*>(p.dn_scale),
+                         p.E, p.H, r.offsets, floats(l.y), p.err, num_sms, s);
+  if (e != cudaSuccess) return e;
+  return launch_combine_f32(floats(l.y), P, p.H, r.row_of_slot, r.weights, p.T, p.k, p.out, p.err,
+                            num_sms, s);
+}
+
+// Tokens from which MXFP4 takes that way.
+constexpr int64_t kPiecesTokens = 4;
+
 }  // namespace
 
 int64_t layer_workspace(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I) {
-  return layout_of(T, E, k, H, I).total;
+  return std::max(layout_of(T, E, k, H, I).total, pieces_layout(T, E, k, H, I).total);
 }
 
 cudaError_t launch_layer(Fmt f, const LayerProblem& p, void* workspace, int num_sms,
                          cudaStream_t s) {
   if (p.T == 0) return cudaSuccess;
-  const Layout l = layout_of(p.T, p.E, p.k, p.H, p.I);
   uint8_t* w = static_cast<uint8_t*>(workspace);
+  if (f == Fmt::MXFP4 && p.T >= kPiecesTokens) return launch_pieces(p, w, num_sms, s);
+  const Layout l = layout_of(p.T, p.E, p.k, p.H, p.I);
   const LayerArgs a{p,
                     reinterpret_cast<float*>(w + l.logits),
                     reinterpret_cast<uint16_t*>(w + l.hhi),

@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(kThreads) route_choose(const RouteProblem p, c
   extern __shared__ int sm[];
   // kSingle: part [kWarps], whist [kWarps][E]; else count [E]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = p.E, k = p.k;
-  if (!kSingle) grid_launch_dependents();
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int64_t t0 = (int64_t)blockIdx.x * per;
   const int n = (int)max((int64_t)0, min((int64_t)per, p.T - t0));
   int* const hist = kSingle ? sm + kWarps : sm;
@@ -265,44 +266,67 @@ __device__ __forceinline__ int32_t slot_row(const int32_t* row_of_slot, int64_t 
   return -1;
 }
 
-__device__ __forceinline__ void fma8(float (&a)[8], float w, uint4 v) {
-  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+// Eight columns of a row, bf16 or fp32, read past L1.
+template <typename TY>
+struct Unit;
+template <>
+struct Unit<uint16_t> {
+  uint4 v;
+  __device__ __forceinline__ void load(const uint16_t* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void add_to(float (&a)[8], float w) const {
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    a[2 * i] = fmaf(w, __uint_as_float(x[i] << 16), a[2 * i]);
-    a[2 * i + 1] = fmaf(w, __uint_as_float(x[i] & 0xFFFF0000u), a[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) {
+      a[2 * i] = fmaf(w, __uint_as_float(x[i] << 16), a[2 * i]);
+      a[2 * i + 1] = fmaf(w, __uint_as_float(x[i] & 0xFFFF0000u), a[2 * i + 1]);
+    }
   }
-}
+};
+template <>
+struct Unit<float> {
+  float4 v[2];
+  __device__ __forceinline__ void load(const float* p) {
+    v[0] = __ldcg(reinterpret_cast<const float4*>(p));
+    v[1] = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void add_to(float (&a)[8], float w) const {
+    const float x[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = fmaf(w, x[i], a[i]);
+  }
+};
 
 // out[t, :] = sum_s w[t, s] * y[row(t, s), :], summed in slot order in fp32.
 // A thread owns 8 columns of one token.  A slot of weight 0 adds nothing,
 // whatever its row holds: the row is not read.
+template <typename TY>
 __global__ void __launch_bounds__(256) combine_kernel(
-    const uint16_t* __restrict__ y, int64_t P, uint32_t units, const int32_t* __restrict__ rows,
+    const TY* __restrict__ y, int64_t P, uint32_t units, const int32_t* __restrict__ rows,
     const float* __restrict__ weights, int64_t n, int k, uint16_t* __restrict__ out, int* err) {
   const int64_t H = (int64_t)units * 8;
+  grid_dependency_wait();
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
        i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t t = i / units;
     const int64_t c = (i - t * units) * 8;
     float a[8] = {};
     for (int s0 = 0; s0 < k; s0 += 4) {
-      uint4 v[4];
+      Unit<TY> v[4];
       float w[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        v[j] = make_uint4(0, 0, 0, 0);
+        v[j] = {};
         w[j] = 0.0f;
         if (s0 + j < k) {
           const int32_t r = slot_row(rows, t * k + s0 + j, P, err);
           if (r >= 0) {
             w[j] = weights ? __ldg(weights + t * k + s0 + j) : 1.0f;
-            if (w[j] != 0.0f) v[j] = __ldcs(reinterpret_cast<const uint4*>(y + r * H + c));
+            if (w[j] != 0.0f) v[j].load(y + r * H + c);
           }
         }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) fma8(a, w[j], v[j]);
+      for (int j = 0; j < 4; ++j) v[j].add_to(a, w[j]);
     }
     uint4 o;
     o.x = pack_bf16x2(a[0], a[1]);
@@ -361,32 +385,32 @@ size_t choose_smem(int E, bool single) {
 size_t place_smem(int E) { return 4 * (kWarps + 2 * kThreads + (size_t)kWarps * E); }
 
 template <typename TL, int NPL>
-cudaError_t route_t(const RouteProblem& p, int num_sms, cudaStream_t s) {
+cudaError_t route_t(const RouteProblem& p, int num_sms, bool dependent, cudaStream_t s) {
   const int ctas = route_ctas(p.T, num_sms);
   const int per = (int)((p.T + ctas - 1) / ctas);
   if (ctas == 1) {
     constexpr auto k = route_choose<TL, NPL, true>;
     cudaError_t e = opt_in_smem<k>(choose_smem(kMaxE, true));
     if (e != cudaSuccess) return e;
-    return launch_kernel<k>(1, kThreads, choose_smem(p.E, true), s, false, p, per);
+    return launch_kernel<k>(1, kThreads, choose_smem(p.E, true), s, dependent, p, per);
   }
   cudaError_t e = opt_in_smem<route_place>(place_smem(kMaxE));
   if (e != cudaSuccess) return e;
   constexpr auto k = route_choose<TL, NPL, false>;
-  e = launch_kernel<k>(ctas, kThreads, choose_smem(p.E, false), s, false, p, per);
+  e = launch_kernel<k>(ctas, kThreads, choose_smem(p.E, false), s, dependent, p, per);
   if (e != cudaSuccess) return e;
   return launch_kernel<route_place>(ctas, kThreads, place_smem(p.E), s, true, p, per);
 }
 
 template <typename TL>
-cudaError_t route_l(const RouteProblem& p, int num_sms, cudaStream_t s) {
+cudaError_t route_l(const RouteProblem& p, int num_sms, bool d, cudaStream_t s) {
   const int npl = (p.E + 31) / 32;
-  if (npl <= 1) return route_t<TL, 1>(p, num_sms, s);
-  if (npl <= 2) return route_t<TL, 2>(p, num_sms, s);
-  if (npl <= 4) return route_t<TL, 4>(p, num_sms, s);
-  if (npl <= 8) return route_t<TL, 8>(p, num_sms, s);
-  if (npl <= 16) return route_t<TL, 16>(p, num_sms, s);
-  return route_t<TL, 32>(p, num_sms, s);
+  if (npl <= 1) return route_t<TL, 1>(p, num_sms, d, s);
+  if (npl <= 2) return route_t<TL, 2>(p, num_sms, d, s);
+  if (npl <= 4) return route_t<TL, 4>(p, num_sms, d, s);
+  if (npl <= 8) return route_t<TL, 8>(p, num_sms, d, s);
+  if (npl <= 16) return route_t<TL, 16>(p, num_sms, d, s);
+  return route_t<TL, 32>(p, num_sms, d, s);
 }
 
 }  // namespace
@@ -398,8 +422,8 @@ int route_ctas(int64_t T, int num_sms) {
   return (int)(n < most ? n : most);
 }
 
-cudaError_t launch_route(const RouteProblem& p, int num_sms, cudaStream_t s) {
-  return p.fp32 ? route_l<float>(p, num_sms, s) : route_l<uint16_t>(p, num_sms, s);
+cudaError_t launch_route(const RouteProblem& p, int num_sms, bool dependent, cudaStream_t s) {
+  return p.fp32 ? route_l<float>(p, num_sms, dependent, s) : route_l<uint16_t>(p, num_sms, dependent, s);
 }
 
 cudaError_t launch_route_bwd(const void* logits, int32_t fp32, int64_t T, int32_t E, int32_t k,
@@ -419,14 +443,29 @@ cudaError_t launch_route_bwd(const void* logits, int32_t fp32, int64_t T, int32_
       dweights, static_cast<uint16_t*>(dlogits), err);
 }
 
-cudaError_t launch_combine(const uint16_t* y, int64_t P, int64_t H, const int32_t* row_of_slot,
-                           const float* weights, int64_t T, int32_t k, uint16_t* out, int* err,
-                           int num_sms, cudaStream_t s) {
+namespace {
+template <typename TY>
+cudaError_t combine_t(const TY* y, int64_t P, int64_t H, const int32_t* row_of_slot,
+                      const float* weights, int64_t T, int32_t k, uint16_t* out, int* err,
+                      int num_sms, bool dependent, cudaStream_t s) {
   const int64_t n = T * (H / 8);
   if (n == 0) return cudaSuccess;
   const int64_t need = (n + 255) / 256, most = 64 * (int64_t)num_sms;
-  return launch_kernel<combine_kernel>((int)(need < most ? need : most), 256, 0, s, false, y, P,
-                                       (uint32_t)(H / 8), row_of_slot, weights, n, (int)k, out, err);
+  return launch_kernel<combine_kernel<TY>>((int)(need < most ? need : most), 256, 0, s, dependent, y, P,
+                                           (uint32_t)(H / 8), row_of_slot, weights, n, (int)k, out, err);
+}
+}  // namespace
+
+cudaError_t launch_combine(const uint16_t* y, int64_t P, int64_t H, const int32_t* row_of_slot,
+                           const float* weights, int64_t T, int32_t k, uint16_t* out, int* err,
+                           int num_sms, cudaStream_t s) {
+  return combine_t(y, P, H, row_of_slot, weights, T, k, out, err, num_sms, false, s);
+}
+
+cudaError_t launch_combine_f32(const float* y, int64_t P, int64_t H, const int32_t* row_of_slot,
+                               const float* weights, int64_t T, int32_t k, uint16_t* out, int* err,
+                               int num_sms, cudaStream_t s) {
+  return combine_t(y, P, H, row_of_slot, weights, T, k, out, err, num_sms, true, s);
 }
 
 cudaError_t launch_combine_bwd(const uint16_t* dout, const uint16_t* y, int64_t P, int64_t H,

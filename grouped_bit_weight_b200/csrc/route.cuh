@@ -10,13 +10,9 @@ __device__ __forceinline__ float bf16_to_f32(uint32_t bits16) {
   return __uint_as_float(bits16 << 16);
 }
 __device__ __forceinline__ float load_logit(const uint16_t* p) { return bf16_to_f32(__ldg(p)); }
-__device__ __forceinline__ float load_logit(const float* p) { return __ldg(p); }
-// A logit that the kernel before may still have been writing when this one
-// started (programmatic dependent launch): read from L2.
-struct LogitL2 {
-  float v;
-};
-__device__ __forceinline__ float load_logit(const LogitL2* p) { return __ldcg(&p->v); }
+// from L2: the kernel before may still have been writing them when this one
+// started (programmatic dependent launch)
+__device__ __forceinline__ float load_logit(const float* p) { return __ldcg(p); }
 
 __device__ __forceinline__ float no_nan(float v) {
   return v != v ? __int_as_float(0xFF800000) : v;
