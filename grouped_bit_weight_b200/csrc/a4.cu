@@ -228,6 +228,7 @@ constexpr int kBBytes = BT * BKB;                 // 32 KB
 constexpr int kSfBytes = 8 * (BM + BT);           // 3 KB: 8 scale bytes a row
 constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
 static_assert(kStageBytes % 1024 == 0, "swizzle atoms stay aligned");
+static_assert(BH <= BT && BT % BOX == 0, "the boxes of a tile fit its stage");
 constexpr int kEpiWarps = 8;
 
 struct Smem {

@@ -101,8 +101,8 @@ struct Device {
   }
 };
 
-// A tensor over part of another's memory, from 4-byte element `first` on: much
-// cheaper to make than an allocation or a view.
+// A tensor over part of another's memory, from its element `first` on (counted in
+// `type`): much cheaper to make than an allocation or a view.
 at::Tensor part(const at::Tensor& whole, at::ScalarType type, int64_t first, at::IntArrayRef sizes) {
   at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
       c10::Storage(whole.storage()), whole.key_set(), at::scalarTypeToTypeMeta(type));
@@ -288,8 +288,10 @@ PyObject* quantize_rows(PyObject* const* a) {
   if (P && !T) value_error(d.where + ": x has no rows");
   d.add("x", x);
   d.add("row_to_token", r2t);
-  const at::Tensor codes = d.empty({P, K / 32, 16}, at::kByte),
-                   scales = d.empty({(K + 127) / 128, P, 4}, at::kByte);
+  const int64_t KA = (K + 127) / 128;
+  const at::Tensor all = d.empty({P * (K / 2 + KA * 4)}, at::kByte);
+  const at::Tensor codes = part(all, at::kByte, 0, {P, K / 32, 16}),
+                   scales = part(all, at::kByte, P * (K / 2), {KA, P, 4});
   call(d, [&](void* s) {
     return gmxfp4_quantize_rows(at_<uint16_t>(x), T, K, at_<int32_t>(r2t), P, glu,
                                 at_<uint8_t>(codes), at_<uint8_t>(scales), s);
