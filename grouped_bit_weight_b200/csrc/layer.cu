@@ -1,37 +1,54 @@
-// layer.cu -- a whole mixture-of-experts layer for a few tokens (T <= 32) in
-// two launches, on NF4 or MXFP4 expert weights.
+// layer.cu -- a whole mixture-of-experts layer for a few tokens (T <= 32) on NF4
+// or MXFP4 expert weights.
 //
 //   l[t, e] = sum_k x[t, k] Wr[e, k] (+ b[e]); ids, w = the k largest and their
 //   softmax weights (route.cuh); per slot (t, s) with e = ids[t, s]:
 //     h = silu(x Wg_e^T) * (x Wu_e^T),  y = h Wd_e^T;   out[t] = sum_s w y
 //
-// Kernel 1 (moe_router): the router logits, one CTA per expert and 8 tokens,
-// fp32 chains of at most H / 256 products; it also zeroes kernel 2's counters.
-// Kernel 2 (moe_experts), one CTA per SM, launched early behind kernel 1
-// (programmatic dependent launch: its codebook table is built meanwhile):
-//   every CTA chooses the experts itself from the logits (no third kernel);
-//   phase A  gate_up + SwiGLU in units of (expert, 8 gate rows + the matching
-//            8 up rows), h written as bf16 high and low parts;
-//   phase B  down in units of (16 rows, expert), y in fp32; the CTA that
-//            finishes a tile's last expert combines the tile's slots in slot
+// Bound: the active experts' packed bytes from HBM.  Two ways:
+//
+// (1) NF4, and MXFP4 on few weights (takes_pieces): two launches.  Kernel 1
+// (moe_router): the router logits, one CTA per expert and 8 tokens, fp32; it also
+// zeroes kernel 2's counters.  Kernel 2 (moe_experts), one CTA per SM, launched
+// early behind kernel 1 (programmatic dependent launch: its codebook table is
+// built meanwhile):
+//   every CTA chooses the experts itself from the logits (no third kernel) and
+//   cuts each expert's rows into groups of at most 8;
+//   phase A  gate_up + SwiGLU in units of (group, 16 gate rows + the matching
+//            16 up rows), h written as bf16 high and low parts;
+//   phase B  down in units of (32 rows, group), y in fp32; the CTA that
+//            finishes a tile's last group combines the tile's slots in slot
 //            order (no sum depends on the order of arrival).
 //   Between the phases a CTA waits until all of phase A is done.  Shares of
 //   both phases are claimed from counters, and a CTA waits only once no share
 //   of phase A is unclaimed, so every share waited for is held by a running
 //   CTA: the wait ends whether or not all CTAs are resident at a time, also
 //   with other kernels on the device.
+// A loading warp fills a ring of two 4 KB stages (32 weight rows x 256 k, one TMA
+// box) for each of 11 multiplying warps -- across the wait between the phases
+// too: the next phase's weights do not depend on it.  A packed byte becomes two
+// bf16 values by one conflict-free table lookup and goes straight into mma.sync
+// m16n8k16 as the A operand (weights are M, tokens N; from a register operand a
+// decoded weight needs no way through shared memory), one scale block at a time;
+// block sums are scaled in fp32.  The low part of h keeps the down projection's
+// input at 16 bits of mantissa, at one more column and no conversion.  A unit's K
+// is split over several warps (joined through shared memory in a fixed order)
+// when a CTA has fewer units than warps.
+// What bounds it is the shared-memory pipe, not HBM: with the table lookups taken
+// out the 32-token case fell from 165 to 137 us, with the loads of x 127, with
+// the weight loads hardly.  Hidden 2880, 32 experts, MXFP4, 1 token: 34 us
+// (1.55 TB/s); hidden 2048, 128 experts, 8 chosen, NF4, 1 / 8 tokens: 22 / 57 us
+// (0.97 / 2.4 TB/s).
 //
-// Bound: the active experts' packed bytes from HBM, and the decode's
-// instructions.  16 warps each own a ring of four 2 KB stages (16 weight rows
-// x 256 k) filled by cp.async three stages ahead -- across the wait between
-// the phases too: the next phase's weights do not depend on it.  A packed byte
-// becomes two bf16 values by one conflict-free table lookup and goes straight
-// into mma.sync m16n8k16 as the A operand (weights are M, tokens N), 64 k of
-// one scale block at a time; block sums are scaled in fp32.  The low part of h
-// keeps the down projection's input at 16 bits of mantissa, at one more mma
-// and no conversion.  A unit's K is split over several warps (joined through
-// shared memory in a fixed order) when a CTA has fewer units than warps.
+// (2) MXFP4 on more weights: no lookups and no mma.sync, the
+// packed weights go to tcgen05 as they are.  x and h become rows of eight 4-bit
+// pieces (a4.cu: 16 bits of each 32-block's maximum) and the block-scaled 4-bit
+// product sums a row's pieces in fp32: logits, routing, pieces of x, gate_up,
+// SwiGLU + pieces of h, down, combine, seven launches behind one another.  32
+// tokens: 107 us (3.9 TB/s; the two products run at 5.2 and 4.6) against 159 of
+// (1).
 #include <algorithm>
+#include <cmath>
 
 #include "common.cuh"
 #include "launch.cuh"
@@ -1028,7 +1045,7 @@ cudaError_t launch_f(const LayerArgs& a, int num_sms, cudaStream_t s) {
 }
 
 // ----------------------------------------------------------------------
-// MXFP4, more tokens: the layer in seven launches on the tensor cores' 4-bit path
+// MXFP4, more weights: the layer in seven launches on the tensor cores' 4-bit path
 // ----------------------------------------------------------------------
 
 struct PiecesLayout {
@@ -1096,8 +1113,19 @@ cudaError_t launch_pieces(const LayerProblem& p, uint8_t* w, int num_sms, cudaSt
                             num_sms, s);
 }
 
-// Tokens from which MXFP4 takes that way.
-constexpr int64_t kPiecesTokens = 4;
+// Whether MXFP4 takes that way: its five launches more cost 4 to 7 us, its
+// products take the weights nearer to the memory rate, so it pays from 128 MB of
+// codes on.  T tokens that choose independently are expected to need
+// E (1 - (1 - k / E)^T) experts.  us, (1) / (2), and those experts' codes:
+//   hidden 2880, 4 of 32 experts   1 token 34 / 38 (50 MB), 2: 47 / 48 (93),
+//     3: 61 / 54 (131), 4: 71 / 62 (164), 8: 101 / 82 (260), 32: 159 / 107 (393)
+//   hidden 2048, intermediate 768, 8 of 128   1: 24 / 30 (19), 8: 57 / 62 (122),
+//     16: 80 / 78 (195), 32: 108 / 96 (264)
+bool takes_pieces(const LayerProblem& p) {
+  const double experts = p.E * (1.0 - std::pow(1.0 - (double)p.k / p.E, (double)p.T));
+  constexpr int64_t most = (int64_t)65535 * 256;  // a launch's grid of 256-value pieces
+  return p.H <= most && p.I <= most && experts * 1.5 * (double)p.H * (double)p.I >= 1.25e8;
+}
 
 }  // namespace
 
@@ -1109,7 +1137,7 @@ cudaError_t launch_layer(Fmt f, const LayerProblem& p, void* workspace, int num_
                          cudaStream_t s) {
   if (p.T == 0) return cudaSuccess;
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  if (f == Fmt::MXFP4 && p.T >= kPiecesTokens) return launch_pieces(p, w, num_sms, s);
+  if (f == Fmt::MXFP4 && takes_pieces(p)) return launch_pieces(p, w, num_sms, s);
   const Layout l = layout_of(p.T, p.E, p.k, p.H, p.I);
   const LayerArgs a{p,
                     reinterpret_cast<float*>(w + l.logits),

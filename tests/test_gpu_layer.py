@@ -265,6 +265,125 @@ def test_layer_without_tokens():
     assert m(torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)).shape == (0, 64)
 
 
+# ---------------------------------------------------------------- many weights
+
+
+def _blocks_max(a):
+    """The largest magnitude of each 32 columns, at every one of them."""
+    m = a.abs().reshape(*a.shape[:-1], -1, 32).amax(-1, keepdim=True)
+    return m.expand(*m.shape[:-1], 32).reshape(a.shape)
+
+
+class Large:
+    """An MXFP4 layer whose active experts hold more than 125 MB, which takes
+    rows in eight 4-bit pieces; its 64-bit values are computed on the GPU."""
+
+    def __init__(self, E, k, H, I, seed, renorm=True):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        u8 = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, dtype=torch.uint8, device=DEV)
+        self.E, self.k, self.H, self.I, self.renorm = E, k, H, I, renorm
+        self.gu, self.gs = u8(0, 256, E, 2 * I, H // 32, 16), u8(117, 122, E, 2 * I, H // 32)
+        self.dn, self.ds = u8(0, 256, E, H, I // 32, 16), u8(117, 122, E, H, I // 32)
+        self.rw = (torch.randn((E, H), generator=g, device=DEV) * 1.5 / H ** 0.5).to(torch.bfloat16)
+        self.rb = torch.zeros(E, device=DEV)
+
+    def __call__(self, x, **kw):
+        return gbw.gmxfp4_moe_layer(x, self.rw, self.gu, self.gs, self.dn, self.ds, k=self.k,
+                                    renormalize=self.renorm, router_bias=self.rb, **kw)
+
+    def weight(self, codes, scales, e):
+        q = torch.stack([codes[e] & 15, codes[e] >> 4], -1).reshape(codes.shape[1], -1, 32).long()
+        v = torch.from_numpy(mp.E2M1).to(DEV)[q & 7] * torch.where(q & 8 > 0, -1.0, 1.0).double()
+        return (v * torch.exp2(scales[e].double() - 127)[..., None]).reshape(codes.shape[1], -1)
+
+    def check(self, x, got):
+        xd = x.double()
+        l = (xd @ self.rw.double().T + self.rb.double()).cpu().numpy()
+        mag = (xd.abs() @ self.rw.double().abs().T).cpu().numpy()
+        ids, w = mp.route(l, self.k, self.renorm)
+        dl = 2.0 ** -24 * (self.H / 256 * 8 + 16) * mag.max(1)
+        s = -np.sort(-l, 1)
+        if self.k < self.E:
+            assert (s[:, self.k - 1] - s[:, self.k] > 2 * dl).all(), "a choice next to a tie"
+        ref, tol = torch.zeros_like(xd), torch.zeros_like(xd)
+        # a row is kept to 2^-16 of the largest of each 32 values m (each piece
+        # leaves a quarter of it); the pieces' magnitudes are at most
+        # m (1 + 1/4 + 1/16 + ..), of whose sum each of the n products and 8 sums
+        # may drop 2^-24
+        keep = lambda n: 2.0 ** -16 + 4 / 3 * (n + 8) * 2.0 ** -24
+        for e in np.unique(ids):
+            t, j = np.nonzero((ids == e) & (w != 0))
+            if not len(t):
+                continue
+            gw, dw = self.weight(self.gu, self.gs, e), self.weight(self.dn, self.ds, e)
+            t = torch.from_numpy(t).to(DEV)
+            a, da = xd[t] @ gw.T, keep(self.H) * (_blocks_max(xd[t]) @ gw.abs().T)
+            (g, u), (dg, du) = a.split(self.I, 1), da.split(self.I, 1)
+            h = torch.nn.functional.silu(g) * u
+            # |silu'| <= 1.1, silu to 8 roundings
+            dh = 1.1 * dg * (u.abs() + du) + torch.nn.functional.silu(g).abs() * du + 8 * 2.0 ** -24 * h.abs()
+            y = h @ dw.T
+            dy = dh @ dw.abs().T + keep(self.I) * (_blocks_max(h.abs() + dh) @ dw.abs().T)
+            we = torch.from_numpy(w[t.cpu().numpy(), j]).to(DEV)[:, None]
+            rel = torch.from_numpy(4 * dl + (16 + self.k) * 2.0 ** -24).to(DEV)[t][:, None]
+            ref.index_add_(0, t, we * y)
+            tol.index_add_(0, t, we * (dy + rel * y.abs()))
+        got, ref, tol = (v.cpu().double().numpy() for v in (got, ref, tol))
+        mp.bf16_close(got, ref, tol)
+        err = np.linalg.norm(got - ref) / max(np.linalg.norm(ref), 1e-30)
+        assert err < 2.0 ** -8 / 3 ** 0.5 * 1.1, err  # one rounding to bf16, evenly spread, and little else
+        assert gbw.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [  # T, E, k, H, I
+    (4, 32, 4, 2880, 2880), (1, 8, 8, 2880, 3648), (5, 16, 4, 2112, 4160), (17, 1024, 16, 704, 576),
+    (32, 10, 2, 4032, 2112), (31, 6, 6, 64, 217024)], ids=str)
+def test_large_layer_matches_plain(shape):
+    T, E, k, H, I = shape
+    m = Large(E, k, H, I, sum(shape), renorm=T % 2 == 0)
+    x = _x(T, H, T)
+    m.check(x, m(x))
+
+
+@pytest.mark.gpu
+def test_large_layer_rows_streams_and_graphs():
+    """All tokens on the same experts; rows of every magnitude, zero, infinite
+    and NaN; any order of the batch; two streams and a replayed graph."""
+    T, E, k, H, I = 32, 12, 3, 2112, 3456
+    m = Large(E, k, H, I, 5)
+    x = _x(T, H, 6)
+    a = m(x)
+    m.check(x, a)
+    perm = torch.randperm(T, generator=torch.Generator().manual_seed(2)).to(DEV)
+    assert torch.equal(m(x), a) and torch.equal(m(x[perm].contiguous()), a[perm])
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for s in (s1, s2):
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for s, v, ref in ((s1, x, a), (s2, x[perm].contiguous(), a[perm])):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append((m(v), ref, v))
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, r) for u, r, _ in got)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o = m(x)
+    m.rb[[1, 4, 9]] = 50.0
+    x.copy_(_x(T, H, 7) * torch.logspace(-6, 1, T, base=10.0).to(DEV)[:, None])
+    x[3] = 0
+    g.replay()
+    m.check(x, o)
+    good = m(x)
+    assert torch.equal(good, o) and (good[3] == 0).all()
+    x[8, 5], x[20, 700] = float("inf"), float("nan")
+    got = m(x)
+    rest = [t for t in range(T) if t not in (8, 20)]
+    assert torch.equal(got[rest], good[rest]) and gbw.device_status() == 0
+
+
 # ---------------------------------------------------------------- refusals
 
 
