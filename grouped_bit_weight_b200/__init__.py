@@ -452,8 +452,8 @@ def gmoe_combine_bwd(dout, y, row_of_slot, slot_of_row, weights, dy=None):
 
 def gnf4_moe_layer(x, router_w, gu_packed, gu_absmax, dn_packed, dn_absmax, k, renormalize=True,
                    router_bias=None, out=None, workspace=None):
-    """A whole mixture-of-experts layer for up to 32 tokens in two launches:
-    router (x [T, H] @ router_w [E, H]^T + router_bias [E] fp32), the k experts
+    """A whole mixture-of-experts layer for up to 32 tokens in two launches (with
+    MXFP4 experts of more than 125 MB seven): router (x [T, H] @ router_w [E, H]^T + router_bias [E] fp32), the k experts
     of each token and their softmax weights as gmoe_route chooses them,
     gate_up [E, 2I, H/2] (gate rows then up rows), SwiGLU, down [E, H, I/2],
     weighted sum -> [T, H] bf16.  workspace: uint8, at least
@@ -472,8 +472,8 @@ def gmxfp4_moe_layer(x, router_w, gu_blocks, gu_scales, dn_blocks, dn_scales, k,
 
 
 def gmxfp4_quantize_rows(x, row_to_token=None, swiglu=False):
-    """(codes [P, K/32, 16] uint8, scales [ceil(K/128), P, 4] uint8 e8m0): bf16
-    rows in MXFP4, gathered through row_to_token [P] int32 when given; byte b of
+    """(codes [P, K/32, 16] uint8, scales [ceil(K/128), P, 4] uint8 e8m0, in one
+    allocation): bf16 rows in MXFP4, gathered through row_to_token [P] int32 when given; byte b of
     scales[a, p] belongs to block 4 a + b of row p (127 past the last).
     x [T, K]; with swiglu x is a gate_up output [T, 2K] and silu(gate) * up is
     packed."""

@@ -71,7 +71,7 @@ constexpr int kMaxE = 1024;
 constexpr int kMaxP = 512;
 constexpr int kRows = 8;           // most rows of a group: rows of one expert that share a decode
 constexpr int CKB = 128;           // bytes per weight row and stage: 256 k
-constexpr int D = 2;               // stages per warp
+constexpr int D = 2;               // stages per warp (3: 58 instead of 57 us for NF4, 8 tokens)
 constexpr int kStage = 32 * CKB;   // 4 KB: 32 weight rows
 
 // Shared memory by address in the shared window (dynamic shared memory starts

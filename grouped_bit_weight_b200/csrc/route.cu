@@ -17,7 +17,10 @@
 // in registers (E / 32 each) and takes the maxima with two warp reductions
 // per choice; up to kSingleTokens tokens are routed and sorted by one CTA in
 // one launch, more by two kernels (choose + count, then place), the second
-// launched early behind the first.
+// launched early behind the first (a plain launch: 1 us more).  8 of 128 experts
+// for 4 tokens: 4.3 us on the device; for 4096: 8.4; 4 of 32 for 16411 tokens
+// with the gradient: 17.8.  On the host a call takes 7 to 15 us, what bounds the
+// small ones.
 #include "common.cuh"
 #include "launch.cuh"
 #include "route.cuh"
@@ -297,8 +300,10 @@ struct Unit<float> {
 };
 
 // out[t, :] = sum_s w[t, s] * y[row(t, s), :], summed in slot order in fp32.
-// A thread owns 8 columns of one token.  A slot of weight 0 adds nothing,
-// whatever its row holds: the row is not read.
+// A thread owns 8 columns of one token; up to four rows' loads are in flight.
+// Each row is read once, so past L1.  A slot of weight 0 adds nothing, whatever
+// its row holds: the row is not read.  Bound by memory: 2048 tokens, 4 rows of
+// 2880 each: 12.1 us, 4.9 TB/s.
 template <typename TY>
 __global__ void __launch_bounds__(256) combine_kernel(
     const TY* __restrict__ y, int64_t P, uint32_t units, const int32_t* __restrict__ rows,
@@ -338,7 +343,9 @@ __global__ void __launch_bounds__(256) combine_kernel(
 }
 
 // One warp per slot: dy[row] = w * dout[t], dw = <y[row], dout[t]>.  Only the
-// slot that slot_of_row names writes a row.
+// slot that slot_of_row names writes a row.  Bound by memory: with the combine,
+// 4096 tokens, 8 rows of 2048 each: 81 us, 5.4 TB/s (streaming hints or four
+// units of a row ahead: 86).
 __global__ void __launch_bounds__(256) combine_bwd_kernel(
     const uint16_t* __restrict__ dout, const uint16_t* __restrict__ y, int64_t P, int32_t units,
     const int32_t* __restrict__ rows, const int32_t* __restrict__ slots,

@@ -289,7 +289,7 @@ GBW_API gbw_status gmoe_combine_bwd(const uint16_t* dout, const uint16_t* y, int
  *   l[t, e] = sum_k x[t, k] router_w[e, k] + router_bias[e], fp32 accumulation;
  *   topk ids and weights as gmoe_route chooses them from l; for each slot with
  *   e = ids[t, s]:
- *     h = silu(x[t] @ Wg_e^T) * (x[t] @ Wu_e^T)   not rounded to bf16
+ *     h = silu(x[t] @ Wg_e^T) * (x[t] @ Wu_e^T)   kept to 16 bits
  *   out[t, :] = bf16( sum_s w[t, s] * (h_s @ Wd_e^T) )
  *   x            [T, H] bf16; out [T, H] bf16
  *   router_w     [E, H] bf16; router_bias [E] fp32 or NULL
@@ -299,7 +299,8 @@ GBW_API gbw_status gmoe_combine_bwd(const uint16_t* dout, const uint16_t* y, int
  *                device memory, overwritten; nothing is kept in it between
  *                calls; calls that may overlap need one each
  * The codebook enters the sums rounded to bf16, as in the bandwidth GEMV.  A
- * slot of weight 0 adds nothing, whatever its expert gives.
+ * slot of weight 0 adds nothing, whatever its expert gives.  A value of a token
+ * that is not finite may make the whole of its output NaN, no other token's.
  * Requires T <= 32 (larger batches: gmoe_route, gnf4_grouped_expert_mlp,
  * gmoe_combine), 1 <= E <= 1024, 1 <= k <= min(E, 16), H % 64 == 0,
  * I % 64 == 0, H * I <= 2^33, 16-byte aligned x, router_w, packed weights,
@@ -313,7 +314,9 @@ GBW_API gbw_status gnf4_moe_layer(const uint16_t* x, int64_t T, int64_t H,
                                   void* workspace, int64_t workspace_bytes, void* stream);
 
 /* The same with MXFP4 experts (blocks [E, 2I, H/32, 16] + scales [E, 2I, H/32],
- * blocks [E, H, I/32, 16] + scales [E, H, I/32], e8m0). */
+ * blocks [E, H, I/32, 16] + scales [E, H, I/32], e8m0).  From 125 MB of codes
+ * of the experts that T tokens are expected to choose, seven launches: x and h
+ * are kept to 2^-16 of the largest of each 32 columns. */
 GBW_API gbw_status gmxfp4_moe_layer(const uint16_t* x, int64_t T, int64_t H,
                                     const uint16_t* router_w, const float* router_bias,
                                     const uint8_t* gu_blocks, const uint8_t* gu_scales,
@@ -338,7 +341,8 @@ GBW_API int64_t gmoe_layer_workspace(int64_t T, int32_t E, int32_t k, int64_t H,
  * saturating, sign kept); an all-zero block gets scale 0 and codes 0, a block
  * with a value that is not finite scale 255 (NaN) and codes 0.  Token indices
  * are clamped to [0, T) and recorded as in gmxfp4_grouped_gemm.
- * Requires K % 32 == 0, 16-byte aligned x, 4-byte aligned codes and scales. */
+ * Requires K % 32 == 0, K <= 2^24, 16-byte aligned x, 4-byte aligned codes and
+ * scales. */
 GBW_API gbw_status gmxfp4_quantize_rows(const uint16_t* x, int64_t T, int64_t K,
                                         const int32_t* row_to_token, int64_t P, int32_t swiglu,
                                         uint8_t* codes, uint8_t* scales, void* stream);
