@@ -30,9 +30,9 @@
 // expert's weights come from HBM once.
 // What bounds it: no one part.  Of 109 us for 8192 ragged rows of 32 experts,
 // 5760 x 2880 (2.5 PFLOP/s; 3.6 TB/s of weights, rows and output), the MMAs alone
-// are 27 (twice as many took that much longer), the bytes 60; taking out the
-// stores, the scale loads or the row loads won 8, 10 and 1 % each.  The rest is
-// waiting along the chain from an empty stage to a full one (scale bytes to
+// are 27 (twice as many took that much longer), the bytes 60.  When it took 134,
+// leaving out the stores, the scale loads or the row loads won 8, 10 and 1 % each.
+// The rest is waiting along the chain from an empty stage to a full one (scale bytes to
 // registers, shared memory, TMEM) and, for tiles over 192 rows, for the
 // epilogue.  4004 rows, 2880 x 2880: 43 us (1.5 PFLOP/s); 16 rows each of
 // 8 experts, 256 x 512: 5 us, latency.
