@@ -162,8 +162,9 @@ template <bool kGLU>
 __global__ void __launch_bounds__(32 * kQRows) quantize_pieces_kernel(
     const void* __restrict__ x, int64_t T, int K, const int32_t* __restrict__ r2t, int64_t P,
     uint8_t* __restrict__ codes, uint32_t* __restrict__ scales, int* err) {
-  grid_launch_dependents();
+  // the product's CTAs fill the SMs: not before this kernel has its own going
   grid_dependency_wait();
+  grid_launch_dependents();
   const int lane = threadIdx.x & 31, U = K / 8;
   const int64_t p = (int64_t)blockIdx.x * kQRows + (threadIdx.x >> 5);
   if (p >= P) return;
@@ -504,6 +505,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
           if (++s == ST) { s = 0; ph ^= 1u; }
         }
       }
+      grid_launch_dependents();  // the next kernel's launch overlaps the last tiles
       if (leader && *abort)
         for (uint32_t i = (g > ST ? g - ST : 0); i < g; ++i) mbar_drain(&full[i % ST], (i / ST) & 1u);
     }
@@ -747,9 +749,13 @@ cudaError_t launch_quantize_pieces(const void* x, int64_t T, int64_t K, const in
                                    bool glu, uint8_t* codes, uint32_t* scales, int* err,
                                    cudaStream_t s) {
   const dim3 grid((unsigned)((P + kQRows - 1) / kQRows), (unsigned)((K + 255) / 256));
+  // The rows of x start behind a router that has a CTA on most SMs: left to
+  // itself, the scheduler packs these CTAs onto the others (9 instead of 4 us for
+  // 128 rows of 2880).  Shared memory that nothing uses allows four an SM.
+  constexpr size_t kSpread = 48 * 1024;
   return glu ? launch_kernel<quantize_pieces_kernel<true>>(grid, 32 * kQRows, 0, s, true, x, T, (int)K,
                                                            r2t, P, codes, scales, err)
-             : launch_kernel<quantize_pieces_kernel<false>>(grid, 32 * kQRows, 0, s, true, x, T, (int)K,
+             : launch_kernel<quantize_pieces_kernel<false>>(grid, 32 * kQRows, kSpread, s, true, x, T, (int)K,
                                                             r2t, P, codes, scales, err);
 }
 

@@ -138,17 +138,19 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router(const LayerArgs a) 
   for (int u = threadIdx.x; u < U; u += blockDim.x) {
     const uint4 wv = __ldg(w + u);
     const uint32_t wx[4] = {wv.x, wv.y, wv.z, wv.w};
+    // all loads before the first use
+    uint4 xv[kRouterTokens];
+#pragma unroll
+    for (int j = 0; j < kRouterTokens; ++j)
+      xv[j] = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)(t0 + min(j, n - 1)) * p.H) + u);
 #pragma unroll
     for (int j = 0; j < kRouterTokens; ++j) {
-      if (j < n) {
-        const uint4 xv = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)(t0 + j) * p.H) + u);
-        const uint32_t xx[4] = {xv.x, xv.y, xv.z, xv.w};
+      const uint32_t xx[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[j] = fmaf(__uint_as_float(wx[i] << 16), __uint_as_float(xx[i] << 16), acc[j]);
-          acc[j] = fmaf(__uint_as_float(wx[i] & 0xFFFF0000u), __uint_as_float(xx[i] & 0xFFFF0000u),
-                        acc[j]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        acc[j] = fmaf(__uint_as_float(wx[i] << 16), __uint_as_float(xx[i] << 16), acc[j]);
+        acc[j] = fmaf(__uint_as_float(wx[i] & 0xFFFF0000u), __uint_as_float(xx[i] & 0xFFFF0000u),
+                      acc[j]);
       }
     }
   }
@@ -1117,10 +1119,10 @@ cudaError_t launch_pieces(const LayerProblem& p, uint8_t* w, int num_sms, cudaSt
 // products take the weights nearer to the memory rate, so it pays from 128 MB of
 // codes on.  T tokens that choose independently are expected to need
 // E (1 - (1 - k / E)^T) experts.  us, (1) / (2), and those experts' codes:
-//   hidden 2880, 4 of 32 experts   1 token 34 / 38 (50 MB), 2: 47 / 48 (93),
-//     3: 61 / 54 (131), 4: 71 / 62 (164), 8: 101 / 82 (260), 32: 159 / 107 (393)
-//   hidden 2048, intermediate 768, 8 of 128   1: 24 / 30 (19), 8: 57 / 62 (122),
-//     16: 80 / 78 (195), 32: 108 / 96 (264)
+//   hidden 2880, 4 of 32 experts   1 token 35 / 38 (50 MB), 2: 47 / 49 (93),
+//     3: 61 / 53 (131), 4: 71 / 61 (164), 8: 99 / 80 (260), 32: 157 / 102 (393)
+//   hidden 2048, intermediate 768, 8 of 128   1: 24 / 29 (19), 8: 55 / 60 (122),
+//     12: 66 / 68 (163), 16: 79 / 75 (195), 32: 107 / 94 (264)
 bool takes_pieces(const LayerProblem& p) {
   const double experts = p.E * (1.0 - std::pow(1.0 - (double)p.k / p.E, (double)p.T));
   constexpr int64_t most = (int64_t)65535 * 256;  // a launch's grid of 256-value pieces
