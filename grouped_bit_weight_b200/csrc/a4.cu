@@ -462,7 +462,10 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
     tma_prefetch_desc(&tmx);
     tma_prefetch_desc(&tmx2);
   }
-  grid_dependency_wait();
+  // Rows in pieces: the kernel before this one lets it launch only after the one
+  // that wrote the offsets is complete, so only what reads the pieces or writes
+  // the output waits; the first weights are on their way by then.
+  if (R == 1) grid_dependency_wait();
   load_offsets_clamped(pb.offsets, E, pb.P / R, off_s, pb.err);
   if (R > 1) {
     for (int i = threadIdx.x; i <= E; i += kThreads) off_s[i] *= R;
@@ -482,6 +485,20 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
       const bool leader = elect_one();
       uint32_t g = 0, s = 0, ph = 1;
       bool ok = true;
+      // stages whose weights are loaded ahead of the wait
+      const uint32_t ahead = R > 1 && blockIdx.x < ntiles ? (uint32_t)min(NS, ST) : 0;
+      if (R > 1) {
+        if (ahead && leader) {
+          int32_t e = 0;
+          const Tile d = tile_info(blockIdx.x, off_s, ts_s, E, e);
+          for (uint32_t i = 0; i < ahead; ++i) {
+            mbar_arrive_expect_tx(&full[i], kABytes + (uint32_t)((d.nv + BOX - 1) / BOX) * (BOX * BKB));
+            tma_load_2d(smem + i * kStageBytes, &tmw, (int)i * BKB, (int32_t)((int64_t)d.e * N + d.n0), &full[i]);
+          }
+        }
+        __syncwarp();
+        grid_dependency_wait();
+      }
       for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
         Tile d = tile_info(t, off_s, ts_s, E, at_e);
         d.nv = __shfl_sync(0xffffffffu, d.nv, 0);
@@ -494,8 +511,10 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
           if (!ok) break;
           if (leader) {
             uint8_t* st = smem + s * kStageBytes;
-            mbar_arrive_expect_tx(&full[s], bytes);
-            tma_load_2d(st, &tmw, ks * BKB, wrow, &full[s]);
+            if (g >= ahead) {
+              mbar_arrive_expect_tx(&full[s], bytes);
+              tma_load_2d(st, &tmw, ks * BKB, wrow, &full[s]);
+            }
             uint8_t* dst = st + kABytes;
             int p0 = d.p0, n = boxes;
             for (; n >= 2; n -= 2, dst += 2 * BOX * BKB, p0 += 2 * BOX)
@@ -507,7 +526,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
       }
       grid_launch_dependents();  // the next kernel's launch overlaps the last tiles
       if (leader && *abort)
-        for (uint32_t i = (g > ST ? g - ST : 0); i < g; ++i) mbar_drain(&full[i % ST], (i / ST) & 1u);
+        for (uint32_t i = (g > ST ? g - ST : 0); i < max(g, ahead); ++i) mbar_drain(&full[i % ST], (i / ST) & 1u);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
@@ -622,6 +641,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
       step();
     };
     uint32_t s = (uint32_t)group, ph = 0;
+    if (R > 1) grid_dependency_wait();
     if (t < ntiles) open();
     if (group) step();
     load();
@@ -675,6 +695,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
     const uint32_t lo_sel = odd ? 0x1054u : 0x5410u, hi_sel = odd ? 0x3276u : 0x7632u;
     AccSched acc;
     bool ok = true;
+    if (R > 1) grid_dependency_wait();
     for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
       const Tile d = tile_info(t, off_s, ts_s, E, at_e);
       const bool both = d.nv > BH;
