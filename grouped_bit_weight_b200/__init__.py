@@ -453,7 +453,7 @@ def gmoe_combine_bwd(dout, y, row_of_slot, slot_of_row, weights, dy=None):
 def gnf4_moe_layer(x, router_w, gu_packed, gu_absmax, dn_packed, dn_absmax, k, renormalize=True,
                    router_bias=None, out=None, workspace=None):
     """A whole mixture-of-experts layer for up to 32 tokens in two launches (with
-    MXFP4 experts of more than 125 MB seven): router (x [T, H] @ router_w [E, H]^T + router_bias [E] fp32), the k experts
+    MXFP4 experts of more than 100 MB seven): router (x [T, H] @ router_w [E, H]^T + router_bias [E] fp32), the k experts
     of each token and their softmax weights as gmoe_route chooses them,
     gate_up [E, 2I, H/2] (gate rows then up rows), SwiGLU, down [E, H, I/2],
     weighted sum -> [T, H] bf16.  workspace: uint8, at least

@@ -37,16 +37,16 @@
 // What bounds it is the shared-memory pipe, not HBM: with the table lookups taken
 // out the 32-token case fell from 165 to 137 us, with the loads of x 127, with
 // the weight loads hardly.  Hidden 2880, 32 experts, MXFP4, 1 token: 34 us
-// (1.55 TB/s); hidden 2048, 128 experts, 8 chosen, NF4, 1 / 8 tokens: 22 / 57 us
-// (0.97 / 2.4 TB/s).
+// (1.55 TB/s); hidden 2048, 128 experts, 8 chosen, NF4, 1 / 8 tokens: 22 / 55 us
+// (0.97 / 2.5 TB/s).
 //
 // (2) MXFP4 on more weights: no lookups and no mma.sync, the
 // packed weights go to tcgen05 as they are.  x and h become rows of eight 4-bit
 // pieces (a4.cu: 16 bits of each 32-block's maximum) and the block-scaled 4-bit
 // product sums a row's pieces in fp32: logits, routing, pieces of x, gate_up,
 // SwiGLU + pieces of h, down, combine, seven launches behind one another.  32
-// tokens: 107 us (3.9 TB/s; the two products run at 5.2 and 4.6) against 159 of
-// (1).
+// tokens: 98 us (4.3 TB/s; the two products take their weights at 5.3 and 4.7)
+// against 157 of (1).
 #include <algorithm>
 #include <cmath>
 
@@ -1115,18 +1115,18 @@ cudaError_t launch_pieces(const LayerProblem& p, uint8_t* w, int num_sms, cudaSt
                             num_sms, s);
 }
 
-// Whether MXFP4 takes that way: its five launches more cost 4 to 7 us, its
-// products take the weights nearer to the memory rate, so it pays from 128 MB of
+// Whether MXFP4 takes that way: its five launches more cost 1 to 3 us, its
+// products take the weights nearer to the memory rate, so it pays from 100 MB of
 // codes on.  T tokens that choose independently are expected to need
 // E (1 - (1 - k / E)^T) experts.  us, (1) / (2), and those experts' codes:
-//   hidden 2880, 4 of 32 experts   1 token 35 / 38 (50 MB), 2: 47 / 49 (93),
-//     3: 61 / 53 (131), 4: 71 / 61 (164), 8: 99 / 80 (260), 32: 157 / 102 (393)
-//   hidden 2048, intermediate 768, 8 of 128   1: 24 / 29 (19), 8: 55 / 60 (122),
-//     12: 66 / 68 (163), 16: 79 / 75 (195), 32: 107 / 94 (264)
+//   hidden 2880, 4 of 32 experts   1 token 35 / 35 (50 MB), 2: 47 / 46 (93),
+//     3: 61 / 50 (131), 4: 70 / 58 (164), 8: 98 / 75 (260), 32: 157 / 98 (393)
+//   hidden 2048, intermediate 768, 8 of 128   1: 24 / 27 (19), 6: 48 / 50 (97),
+//     8: 55 / 55 (122), 12: 66 / 65 (163), 16: 78 / 74 (195), 32: 107 / 91 (264)
 bool takes_pieces(const LayerProblem& p) {
   const double experts = p.E * (1.0 - std::pow(1.0 - (double)p.k / p.E, (double)p.T));
   constexpr int64_t most = (int64_t)65535 * 256;  // a launch's grid of 256-value pieces
-  return p.H <= most && p.I <= most && experts * 1.5 * (double)p.H * (double)p.I >= 1.25e8;
+  return p.H <= most && p.I <= most && experts * 1.5 * (double)p.H * (double)p.I >= 1e8;
 }
 
 }  // namespace

@@ -314,7 +314,7 @@ GBW_API gbw_status gnf4_moe_layer(const uint16_t* x, int64_t T, int64_t H,
                                   void* workspace, int64_t workspace_bytes, void* stream);
 
 /* The same with MXFP4 experts (blocks [E, 2I, H/32, 16] + scales [E, 2I, H/32],
- * blocks [E, H, I/32, 16] + scales [E, H, I/32], e8m0).  From 125 MB of codes
+ * blocks [E, H, I/32, 16] + scales [E, H, I/32], e8m0).  From 100 MB of codes
  * of the experts that T tokens are expected to choose, seven launches: x and h
  * are kept to 2^-16 of the largest of each 32 columns. */
 GBW_API gbw_status gmxfp4_moe_layer(const uint16_t* x, int64_t T, int64_t H,

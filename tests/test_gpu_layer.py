@@ -275,7 +275,7 @@ def _blocks_max(a):
 
 
 class Large:
-    """An MXFP4 layer whose active experts hold more than 125 MB, which takes
+    """An MXFP4 layer whose active experts hold more than 100 MB, which takes
     rows in eight 4-bit pieces; its 64-bit values are computed on the GPU."""
 
     def __init__(self, E, k, H, I, seed, renorm=True):
