@@ -64,6 +64,18 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
   return d;
 }
 
+// Eight values to a word of codes, the first in the lowest nibble.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+  uint32_t d;
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(d)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return d;
+}
+
 // The two values of a byte of codes.
 __device__ __forceinline__ float2 e2m1_values(uint32_t byte) {
   uint32_t h;
@@ -83,9 +95,10 @@ __device__ __forceinline__ void unpack8(uint4 q, float (&v)[8]) {
 // A warp quantises kUnits * 256 values of a row, 8 a lane and unit; the 4 lanes
 // of a 32-block share its maximum.  The scale bytes of 128 k are one word, word
 // (k / 128) * P + p; a block's warps take neighbouring rows, whose words share a
-// sector.  8192 rows of 2880 take 12.8 us, 4004 SwiGLU rows 13.1 (5 and 4 TB/s
-// in and out); rows by whole warps took 12.1 and 14.3, one unit a warp 16.8 and
-// 14.3, six 12.3 and 13.1, but 2.7 instead of 2.3 us for a few rows.
+// sector.  8192 rows of 2880 take 11.4 us, 4004 SwiGLU rows 12.6 (5 and 4 TB/s
+// in and out), bound by about 60 and 130 instructions per unit.  (When they took
+// 12.8 and 13.1: rows by whole warps 12.1 and 14.3, one unit a warp 16.8 and 14.3,
+// six 12.3 and 13.1, but 2.7 instead of 2.3 us for a few rows.)
 constexpr int kQRows = 4;  // warps, and rows, of a block
 template <bool kGLU>
 constexpr int kUnits = kGLU ? 2 : 4;  // loaded before the first is used
@@ -118,15 +131,20 @@ __global__ void __launch_bounds__(32 * kQRows) quantize_rows_kernel(
     const int c = c0 + 32 * i;
     float v[8];
     unpack8(g[i], v);
+    uint32_t m = 0;  // magnitudes order as their bits do, NaN and inf on top
     if (kGLU) {
       float w[8];
       unpack8(u[i], w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fdividef(v[j], 1.0f + __expf(-v[j])) * w[j];
+      for (int j = 0; j < 8; ++j) {
+        v[j] = __fdividef(v[j], 1.0f + __expf(-v[j])) * w[j];
+        m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+      }
+    } else {  // two at a time
+      const uint32_t k2 = 0x7FFF7FFFu;
+      m = __vmaxu2(__vmaxu2(g[i].x & k2, g[i].y & k2), __vmaxu2(g[i].z & k2, g[i].w & k2));
+      m = max(m & 0xFFFF0000u, m << 16);
     }
-    uint32_t m = 0;  // magnitudes order as their bits do, NaN and inf on top
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const uint32_t ex = m >> 23;
@@ -137,7 +155,8 @@ __global__ void __launch_bounds__(32 * kQRows) quantize_rows_kernel(
     } else if (m) {
       const float inv = __uint_as_float((254u - byte) << 23);  // 2^-X
 #pragma unroll
-      for (int j = 0; j < 4; ++j) q |= e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv) << (8 * j);
+      for (int j = 0; j < 8; ++j) v[j] *= inv;
+      q = e2m1x8(v);
     }
     if (c < U) out[c] = q;
     if (c >= U) byte = 127u;  // blocks of a word past the row: 2^0
