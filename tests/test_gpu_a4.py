@@ -143,7 +143,8 @@ def _check_product(counts, N, K, seed, rows_pad=0, xstd=None):
     ([16] * 8, 256, 512), ([0, 0, 40, 0], 264, 352), ([128, 129, 130], 128, 128),
     ([191, 192, 193], 320, 288), ([383, 384, 385], 128, 544), ([601, 2, 0, 77], 192, 320),
     ([1000], 72, 1024), ([33], 1000, 2912), ([250, 256, 262, 20], 640, 2880), ([255, 256, 257, 319, 320], 136, 640),
-    ([3] * 64, 64, 160), ([2, 1] * 20, 2056, 768)])
+    ([3] * 64, 64, 160), ([2, 1] * 20, 2056, 768), ([0, 1] * 500, 64, 64), ([0] * 1023 + [70], 72, 96),
+    ([3000], 136, 128)])
 def test_product_matches_plain(counts, N, K):
     _check_product(counts, N, K, sum(counts) + N + K)
 
@@ -194,6 +195,29 @@ def test_product_nan_scale_marks_its_rows_and_columns_only():
     want[7] = want[30] = True
     want[:20, 9] = True
     assert torch.equal(bad, want)
+
+
+@pytest.mark.gpu
+def test_quantise_and_product_on_two_streams_and_in_inference_mode():
+    E, N, K = 4, 264, 416
+    w, ws, _ = _weights(E, N, K, 3)
+    t = lambda a: torch.from_numpy(a).to(DEV)
+    w, ws, calls = t(w), t(ws), []
+    for i, counts in enumerate(([100, 0, 30, 7], [1, 290, 3, 64])):
+        x, off = _bf16((sum(counts), K), i).to(DEV), t(_offsets(counts))
+        calls.append((x, off, gbw.gmxfp4_grouped_gemm_a4(*gbw.gmxfp4_quantize_rows(x), w, ws, off)))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    with torch.inference_mode():
+        for _ in range(20):
+            for s, (x, off, ref) in zip(streams, calls):
+                with torch.cuda.stream(s):
+                    q = gbw.gmxfp4_quantize_rows(x)
+                    got.append((gbw.gmxfp4_grouped_gemm_a4(*q, w, ws, off), ref))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in got) and gbw.device_status() == 0
 
 
 @pytest.mark.gpu

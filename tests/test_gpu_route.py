@@ -336,3 +336,17 @@ def test_a_routing_can_be_saved(tmp_path):
     torch.save(tuple(r), tmp_path / "r.pt")
     for a, b in zip(r, torch.load(tmp_path / "r.pt")):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_a_routing_can_be_copied_and_changed_in_inference_mode():
+    import copy
+    l = torch.randn((7, 16), generator=torch.Generator().manual_seed(0)).to(DEV)
+    ref = gbw.gmoe_route(l, 4)
+    with torch.inference_mode():
+        r = copy.deepcopy(gbw.gmoe_route(l, 4))
+        for a, b in zip(r, ref):
+            assert torch.equal(a, b)
+        r.topk_ids.add_(1)
+        r.topk_weights.mul_(2.0)
+        assert torch.equal(r.row_to_token, ref.row_to_token) and torch.equal(r.topk_ids, ref.topk_ids + 1)
