@@ -221,6 +221,43 @@ def test_quantise_and_product_on_two_streams_and_in_inference_mode():
 
 
 @pytest.mark.gpu
+def test_product_in_a_graph_behind_every_kind_of_node():
+    """First in the graph; behind a copy, a fill, and two streams that join."""
+    E, N, K = 4, 264, 416
+    w, ws, _ = _weights(E, N, K, 3)
+    t = lambda a: torch.from_numpy(a).to(DEV)
+    w, ws, off = t(w), t(ws), t(_offsets([100, 0, 30, 7]))
+    x = [_bf16((137, K), i).to(DEV) for i in range(2)]
+    q = [gbw.gmxfp4_quantize_rows(v) for v in x]
+    ref = [gbw.gmxfp4_grouped_gemm_a4(*v, w, ws, off) for v in q]
+    codes, scales = (v.clone() for v in q[0])
+    call = lambda out: gbw.gmxfp4_grouped_gemm_a4(codes, scales, w, ws, off, out=out)
+    outs = [torch.empty_like(ref[0]) for _ in range(4)]
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(outs[0])
+        codes.copy_(q[1][0])
+        scales.copy_(q[1][1])
+        call(outs[1])
+        outs[2].zero_()
+        call(outs[2])
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            codes.copy_(q[0][0])
+        scales.copy_(q[0][1])
+        main.wait_stream(side)
+        call(outs[3])
+    for _ in range(3):
+        for o in outs:
+            o.fill_(float("nan"))
+        g.replay()
+        for o, r in zip(outs, (ref[0], ref[1], ref[1], ref[0])):
+            assert torch.equal(o, r)
+    assert gbw.device_status() == 0
+
+
+@pytest.mark.gpu
 def test_product_without_rows_bad_offsets_and_repeats():
     E, N, K = 3, 64, 128
     w, ws, _ = _weights(E, N, K, 3)

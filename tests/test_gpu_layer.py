@@ -384,6 +384,40 @@ def test_large_layer_rows_streams_and_graphs():
     assert torch.equal(got[rest], good[rest]) and gbw.device_status() == 0
 
 
+@pytest.mark.gpu
+def test_layers_in_graphs_behind_copies_and_one_another():
+    """Layers of both kinds one behind the other in a graph, in between copies,
+    fills and a join of two streams, sharing one workspace."""
+    small, nf4, large = Layer("mxfp4", 8, 2, 512, 256, seed=2), Layer("nf4", 16, 4, 512, 128, seed=1), \
+        Large(6, 3, 512, 44032, 3)
+    x = [_x(9, 512, i) for i in range(2)]
+    layers = (large, nf4, large, small, large)
+    need = max(gbw.lib.gmoe_layer_workspace(9, m.E, m.k, m.H, m.I) for m in layers)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    refs = [[m(v) for m in layers] for v in x]
+    buf, side, g = x[0].clone(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    outs = [torch.empty_like(buf) for _ in range(10)]
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        for i in range(2):
+            for j, m in enumerate(layers):
+                m(buf, out=outs[5 * i + j], workspace=ws)
+            if i == 0:
+                ws.fill_(255)
+                side.wait_stream(main)
+                with torch.cuda.stream(side):
+                    buf.copy_(x[1])
+                main.wait_stream(side)
+        buf.copy_(x[0])
+    for _ in range(5):
+        for o in outs:
+            o.fill_(float("nan"))
+        g.replay()
+        for o, r in zip(outs, refs[0] + refs[1]):
+            assert torch.equal(o, r)
+    assert gbw.device_status() == 0
+
+
 # ---------------------------------------------------------------- refusals
 
 
