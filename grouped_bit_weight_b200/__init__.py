@@ -456,7 +456,8 @@ def gnf4_moe_layer(x, router_w, gu_packed, gu_absmax, dn_packed, dn_absmax, k, r
     MXFP4 experts of more than 100 MB seven): router (x [T, H] @ router_w [E, H]^T + router_bias [E] fp32), the k experts
     of each token and their softmax weights as gmoe_route chooses them,
     gate_up [E, 2I, H/2] (gate rows then up rows), SwiGLU, down [E, H, I/2],
-    weighted sum -> [T, H] bf16.  workspace: uint8, at least
+    weighted sum -> [T, H] bf16.  A token all of whose logits are -inf gives
+    zeros; one that holds a NaN gives NaN.  workspace: uint8, at least
     lib.gmoe_layer_workspace(T, E, k, H, I) bytes, 256-byte aligned; calls that
     may overlap need one each (allocated here when not given)."""
     return _host.moe_layer(True, x, router_w, gu_packed, gu_absmax, dn_packed, dn_absmax, k,

@@ -60,6 +60,7 @@ struct RouteProblem {
   int32_t* row_of_slot;   // [P]
   int32_t* slot_of_row;   // [P]
   int32_t* hist;       // workspace [CTAs, E]
+  bool nan_rows = false;  // NaN weights for a token of NaN logits and no number
 };
 
 // CTAs of the routing's first kernel (1: one kernel does it all), and so the

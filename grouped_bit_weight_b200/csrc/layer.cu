@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
   for (int t = warp; t < T; t += kWarps + 1) {
     int id = 0;
     float w = 0.0f;
-    choose<float, NPL>(a.logits + (int64_t)t * E, E, k, p.renorm, lane, id, w);
+    choose<float, NPL>(a.logits + (int64_t)t * E, E, k, p.renorm, true, lane, id, w);
     if (lane < k) {
       ids[t * k + lane] = id;
       wts[t * k + lane] = w;
@@ -1099,6 +1099,7 @@ cudaError_t launch_pieces(const LayerProblem& p, uint8_t* w, int num_sms, cudaSt
   r.row_to_token = ints(l.r2t);
   r.row_of_slot = ints(l.ros);
   r.slot_of_row = ints(l.sor);
+  r.nan_rows = true;
   cudaError_t e = launch_router(a, s);
   if (e != cudaSuccess) return e;
   e = launch_route(r, num_sms, true, s);

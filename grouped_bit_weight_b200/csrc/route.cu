@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(kThreads) route_choose(const RouteProblem p, c
     const int64_t t = t0 + i;
     int id = 0;
     float w = 0.0f;
-    choose<TL, NPL>(reinterpret_cast<const TL*>(p.logits) + t * E, E, k, p.renorm, lane, id, w);
+    choose<TL, NPL>(reinterpret_cast<const TL*>(p.logits) + t * E, E, k, p.renorm, p.nan_rows,
+                    lane, id, w);
     if (lane < k) {
       p.ids[t * k + lane] = id;
       p.weights[t * k + lane] = w;

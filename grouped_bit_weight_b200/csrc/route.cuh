@@ -36,16 +36,22 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// The choice of one token: lane s < k gets the s-th expert and its weight.
+// The choice of one token: lane s < k gets the s-th expert and its weight.  A
+// token without any logit above -inf gets weights of 0; with nan_rows (the whole
+// layer, which shows nothing of its logits) weights of NaN when one of them is NaN.
 template <typename TL, int NPL>
-__device__ __forceinline__ void choose(const TL* row, int E, int k, int renorm, int lane, int& id,
-                                       float& w) {
+__device__ __forceinline__ void choose(const TL* row, int E, int k, int renorm, bool nan_rows,
+                                       int lane, int& id, float& w) {
   uint32_t key[NPL];
+  bool nan = false;
 #pragma unroll
   for (int j = 0; j < NPL; ++j) {
     const int e = j * 32 + lane;
-    key[j] = e < E ? order_key(no_nan(load_logit(row + e))) : 0u;
+    const float l = e < E ? load_logit(row + e) : 0.0f;
+    nan |= l != l;
+    key[j] = e < E ? order_key(no_nan(l)) : 0u;
   }
+  nan = nan_rows && __any_sync(0xffffffffu, nan);
   float all = 0.0f, m = 0.0f, v = 0.0f;
   if (NPL <= 4) {
     // each lane's keys in falling order (equal ones by index), so that a
@@ -119,7 +125,7 @@ __device__ __forceinline__ void choose(const TL* row, int E, int k, int renorm, 
   }
   const float p = lane < k ? share(v, m) : 0.0f;
   const float total = renorm ? warp_sum(p) : all;
-  w = m == __int_as_float(0xFF800000) ? 0.0f : p / total;
+  w = m == __int_as_float(0xFF800000) ? (nan ? __int_as_float(0x7FC00000) : 0.0f) : p / total;
 }
 
 }  // namespace gbw

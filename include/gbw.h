@@ -300,7 +300,9 @@ GBW_API gbw_status gmoe_combine_bwd(const uint16_t* dout, const uint16_t* y, int
  *                calls; calls that may overlap need one each
  * The codebook enters the sums rounded to bf16, as in the bandwidth GEMV.  A
  * slot of weight 0 adds nothing, whatever its expert gives.  A value of a token
- * that is not finite may make the whole of its output NaN, no other token's.
+ * that is not finite may make the whole of its output NaN, no other token's.  A
+ * token without any logit above -inf gets an output of zeros when all its logits
+ * are -inf, and of NaN when one of them is NaN (as a token that holds a NaN has).
  * Requires T <= 32 (larger batches: gmoe_route, gnf4_grouped_expert_mlp,
  * gmoe_combine), 1 <= E <= 1024, 1 <= k <= min(E, 16), H % 64 == 0,
  * I % 64 == 0, H * I <= 2^33, 16-byte aligned x, router_w, packed weights,

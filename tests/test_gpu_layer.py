@@ -418,6 +418,52 @@ def test_layers_in_graphs_behind_copies_and_one_another():
     assert gbw.device_status() == 0
 
 
+def _check_bad_tokens(m, x, nan, inf):
+    """A token that holds a NaN gives NaN throughout, one that holds an infinity
+    nothing finite, a masked one zeros, the others what they gave before."""
+    good = m(x)
+    x[nan, 3] = float("nan")
+    x[inf, 5] = float("inf")
+    got = m(x)
+    rest = [t for t in range(len(x)) if t not in (nan, inf)]
+    assert torch.equal(got[rest], good[rest]) and torch.isfinite(good).all()
+    assert torch.isnan(got[nan]).all() and not torch.isfinite(got[inf]).any()
+    return got
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("fmt", ["nf4", "mxfp4"])
+def test_layer_of_a_token_with_nan_is_nan(fmt, renorm):
+    m = Layer(fmt, 12, 4, 256, 128, seed=9, renorm=renorm)
+    x = _x(5, 256, 1)
+    _check_bad_tokens(m, x, 1, 3)
+    # an expert of NaN logits is masked, as gmoe_route masks it
+    m.kw["router_bias"] = torch.zeros(12, device=DEV)
+    m.kw["router_bias"][7] = float("nan")
+    a = m(x)
+    m.kw["router_bias"][7] = float("-inf")
+    b = m(x)
+    assert torch.equal(a[[0, 2, 4]], b[[0, 2, 4]])
+    # without any expert: zeros, but for the token of NaN
+    m.kw["router_bias"].fill_(float("-inf"))
+    got = m(x)
+    assert (got[[0, 2, 4]] == 0).all() and torch.isnan(got[1]).all()
+    assert gbw.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_large_layer_of_a_token_with_nan_is_nan():
+    m = Large(12, 3, 2112, 3456, 5)
+    x = _x(9, 2112, 6)
+    _check_bad_tokens(m, x, 2, 7)
+    m.rb.fill_(float("-inf"))
+    got = m(x)
+    rest = [t for t in range(9) if t not in (2, 7)]
+    assert (got[rest] == 0).all() and torch.isnan(got[2]).all()
+    assert gbw.device_status() == 0
+
+
 # ---------------------------------------------------------------- refusals
 
 
