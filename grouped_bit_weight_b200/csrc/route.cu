@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(
       if (id < 0 || id >= E) {
         raise_error(err, GBW_DEVERR_ROUTE);
         id = -1;
+        w = 0.0f;  // the slot is left out: it is no part of the sum either
       }
     }
     // a weight of zero passes nothing on, whatever dw holds

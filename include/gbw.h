@@ -253,7 +253,8 @@ GBW_API int64_t gmoe_route_workspace(int64_t T, int32_t E);
  *   logits, topk_ids, topk_weights   as gmoe_route took and gave them (logits
  *            is not read and may be NULL when renormalize != 0)
  *   dweights [T, k] fp32; dlogits [T, E], every element written, in the
- *            logits' type.  A slot of weight 0 passes nothing on. */
+ *            logits' type.  A slot of weight 0 passes nothing on, nor does one
+ *            whose id is outside [0, E) (it raises GBW_DEVERR_ROUTE). */
 GBW_API gbw_status gmoe_route_bwd(const void* logits, int32_t logits_type, int64_t T, int32_t E,
                                   int32_t k, int32_t renormalize, const int32_t* topk_ids,
                                   const float* topk_weights, const float* dweights, void* dlogits,

@@ -229,6 +229,30 @@ def test_route_bwd_reports_bad_ids():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_bwd_leaves_a_slot_with_a_bad_id_out(renorm):
+    """The gradient is that of the same call with the slot's weight zero, and
+    other tokens' rows are those of good ids."""
+    l = _logits(4, 16, "fp32", 1).to(DEV)
+    r = gbw.gmoe_route(l, 3, renormalize=renorm)
+    dw = _logits(4, 3, "fp32", 2).to(DEV)
+    good = gbw.gmoe_route_bwd(l, r.topk_ids, r.topk_weights, dw, renormalize=renorm)
+    assert gbw.device_status() == 0
+    ids, w = r.topk_ids.clone(), r.topk_weights.clone()
+    ids[1, 0], ids[2, 2] = 16, -3
+    got = gbw.gmoe_route_bwd(l, ids, w, dw, renormalize=renorm)
+    assert gbw.device_status() == gbw.DEVERR_ROUTE
+    w[1, 0] = w[2, 2] = 0.0
+    want = gbw.gmoe_route_bwd(l, r.topk_ids, w, dw, renormalize=renorm)
+    assert torch.equal(got, want) and gbw.device_status() == 0
+    assert torch.equal(got[[0, 3]], good[[0, 3]]) and not torch.equal(got[1], good[1])
+    w64, dw64 = w.cpu().double().numpy(), dw.cpu().double().numpy()
+    ref = mp.route_bwd(l.cpu().double().numpy(), r.topk_ids.cpu().numpy(), w64, dw64, renorm)
+    # 3 products and sums, 16 exponentials, each within 2^-21 of a share of at most 1
+    assert (np.abs(got.cpu().double().numpy() - ref) <= 2.0 ** -19 * np.abs(dw64).sum(1, keepdims=True)).all()
+
+
+@pytest.mark.gpu
 def test_route_then_grouped_then_combine_on_a_side_stream_and_in_a_graph():
     """Route -> fused expert pass -> combine: eager on a side stream, then
     captured once and replayed on other inputs, equals the plain chain."""
