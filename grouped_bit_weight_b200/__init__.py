@@ -485,7 +485,8 @@ def gmxfp4_grouped_gemm_a4(x_codes, x_scales, blocks, scales, expert_offsets, ou
     """out[P, N] bf16 = rows @ W_e^T per expert, both in MXFP4: x_codes
     [P, K/32, 16] and x_scales [ceil(K/128), P, 4] from gmxfp4_quantize_rows,
     expert-sorted; blocks [E, N, K/32, 16] (or [E, N, K/2]), scales
-    [E, N, K/32]."""
+    [E, N, K/32].  Rows past expert_offsets[E], which may be less than P, are
+    not written."""
     return _host.grouped_gemm_a4(x_codes, x_scales, blocks, scales, expert_offsets, out)
 
 

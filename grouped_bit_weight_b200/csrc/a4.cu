@@ -438,6 +438,30 @@ struct RowScales {
   }
 };
 
+// The experts' first rows, checked: 0 at first, never falling, at most P.  The
+// last may be below P (rows past it belong to no expert and are not written).
+// Anything else is clamped to a running maximum and recorded.
+__device__ __forceinline__ void load_offsets(const int32_t* offsets, int32_t E, int64_t P,
+                                             int32_t* off_s, int* err) {
+  int bad = 0;
+  for (int32_t e = threadIdx.x; e <= E; e += kThreads) {
+    const int32_t v = __ldg(offsets + e);
+    off_s[e] = v;
+    bad |= v < 0 || v > P || (e == 0 && v != 0) || (e < E && __ldg(offsets + e + 1) < v);
+  }
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) {
+      int32_t last = 0;
+      for (int32_t e = 0; e <= E; ++e) {
+        if (e > 0) last = max(last, (int32_t)min((int64_t)off_s[e], P));
+        off_s[e] = last;
+      }
+      raise_error(err, GBW_DEVERR_OFFSETS);
+    }
+    __syncthreads();
+  }
+}
+
 // R: rows of x that make one of the output, 1 or kPieces.
 template <int R>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -485,7 +509,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
   // that wrote the offsets is complete, so only what reads the pieces or writes
   // the output waits; the first weights are on their way by then.
   if (R == 1) grid_dependency_wait();
-  load_offsets_clamped(pb.offsets, E, pb.P / R, off_s, pb.err);
+  load_offsets(pb.offsets, E, pb.P / R, off_s, pb.err);
   if (R > 1) {
     for (int i = threadIdx.x; i <= E; i += kThreads) off_s[i] *= R;
     __syncthreads();

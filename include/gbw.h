@@ -355,10 +355,11 @@ GBW_API gbw_status gmxfp4_quantize_rows(const uint16_t* x, int64_t T, int64_t K,
  *   x_codes [P, K/2] uint8, x_scales [ceil(K/128), P, 4] uint8: expert-sorted
  *           rows as gmxfp4_quantize_rows writes them
  *   blocks, scales, expert_offsets, out: as in gmxfp4_grouped_gemm (scales
- *           need no alignment here)
+ *           need no alignment here), but expert_offsets[E] may be less than P
  * Requires K % 32 == 0, N % 8 == 0, 1 <= E <= 1024, 16-byte aligned x_codes,
- * blocks and out, 4-byte aligned x_scales.  P == 0 is a no-op.  Rows of out past expert_offsets[E] are
- * not written. */
+ * blocks and out, 4-byte aligned x_scales.  P == 0 is a no-op.  Rows past
+ * expert_offsets[E] (of a buffer padded to a fixed P) belong to no expert: their
+ * codes and scales are not used and their rows of out are not written. */
 GBW_API gbw_status gmxfp4_grouped_gemm_a4(const uint8_t* x_codes, const uint8_t* x_scales,
                                           int64_t P, int64_t K, const uint8_t* blocks,
                                           const uint8_t* scales, int32_t E, int64_t N,

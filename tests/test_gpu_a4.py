@@ -150,6 +150,44 @@ def test_product_matches_plain(counts, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("counts,pad", [
+    ([16], 1), ([0], 5), ([5, 0, 3], 56), ([0, 0, 0], 64), ([17, 31, 0], 300), ([255, 1], 1),
+    ([250, 256], 262), ([383, 2, 0], 1000)], ids=str)
+def test_product_leaves_rows_behind_the_last_expert_as_they_were(counts, pad):
+    """A buffer padded to a fixed number of rows: the last offset is below P, the
+    rows behind it hold NaN scales, and no error is raised."""
+    E, N, K, P = len(counts), 136, 288, sum(counts)
+    w, ws, wv = _weights(E, N, K, P)
+    xq, xs = gbw.gmxfp4_quantize_rows(_bf16((P + pad, K), 1).to(DEV))
+    xs[:, P:, 0] = 255  # NaN
+    xv = _values(_codes(xq), _scales(xs, K))[:P]
+    off = _offsets(counts)
+    t = lambda a: torch.from_numpy(a).to(DEV)
+    out = torch.full((P + pad, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    gbw.gmxfp4_grouped_gemm_a4(xq, xs, t(w), t(ws), t(off), out=out)
+    assert gbw.device_status() == 0
+    assert (out[P:] == 7.0).all()
+    got = out[:P].cpu().double().numpy()
+    for e in range(E):
+        s = slice(off[e], off[e + 1])
+        mp.bf16_close(got[s], xv[s] @ wv[e].T, K * 2.0 ** -24 * (np.abs(xv[s]) @ np.abs(wv[e]).T))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("off", [[1, 20, 30, 40], [0, 20, 10, 40], [0, 60, 70, 80], [0, -5, -5, -1],
+                                 [0, 10, 20, 51], [0, 2 ** 31 - 1, -2 ** 31, 30]], ids=str)
+def test_product_reports_bad_offsets_and_stays_inside_its_rows(off):
+    E, N, K, P = 3, 64, 128, 50
+    w, ws, _ = _weights(E, N, K, 3)
+    t = lambda a: torch.from_numpy(a).to(DEV)
+    xq, xs = gbw.gmxfp4_quantize_rows(_bf16((P, K), 1).to(DEV))
+    buf = torch.full((P + 60, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    gbw.gmxfp4_grouped_gemm_a4(xq, xs, t(w), t(ws), t(np.array(off, np.int32)), out=buf[20:20 + P])
+    assert gbw.device_status() == gbw.DEVERR_OFFSETS
+    assert (buf[:20] == 7.0).all() and (buf[20 + P:] == 7.0).all()
+
+
+@pytest.mark.gpu
 def test_product_scales_over_a_wide_range():
     """Every row has a magnitude of its own, 2^-60 to 2^60."""
     P = 300
