@@ -291,6 +291,28 @@ __device__ __forceinline__ int32_t row_tiles(int32_t cnt) {
   return cnt <= BT ? (cnt + BT - 1) / BT : (cnt + BH - 1) / BH;
 }
 
+// ts[e] = tiles of the experts below e, ts[E] = all: per_tile_n times the row tiles
+// of each.  Warp 0 scans 32 experts at a time; the block must sync afterwards.
+__device__ __forceinline__ void tiles_below(const int32_t* off_s, int32_t E, int32_t per_tile_n,
+                                            int32_t* ts) {
+  if (threadIdx.x >= 32) return;
+  const int lane = threadIdx.x;
+  int32_t carry = 0;
+  for (int32_t base = 0; base < E; base += 32) {
+    const int32_t e = base + lane;
+    const int32_t v = e < E ? per_tile_n * row_tiles(off_s[e + 1] - off_s[e]) : 0;
+    int32_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (e < E) ts[e] = carry + incl - v;
+    carry += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) ts[E] = carry;
+}
+
 // Tile t, for a caller whose tiles only grow: e is the expert of its last one
 // (0 at first).  The next is usually a few experts on.
 __device__ __forceinline__ Tile tile_info(int64_t t, const int32_t* off, const int32_t* ts,
@@ -514,7 +536,7 @@ gemm_a4_kernel(const A4Problem pb, const __grid_constant__ CUtensorMap tmw,
     for (int i = threadIdx.x; i <= E; i += kThreads) off_s[i] *= R;
     __syncthreads();
   }
-  tile_prefix_of(off_s, E, ntn, ts_s, row_tiles);
+  tiles_below(off_s, E, ntn, ts_s);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

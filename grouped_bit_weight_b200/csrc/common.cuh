@@ -130,19 +130,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Whether the phase with `parity` has completed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n"
-      " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Wait budget of every pipeline wait: after this many nanoseconds without
 // progress the wait gives up, raises GBW_DEVERR_TIMEOUT and the kernel
 // unwinds instead of hanging the GPU.
@@ -463,12 +450,11 @@ __device__ __forceinline__ void grid_launch_dependents() {
 }
 
 // ts[e] = sum over experts e' < e of tiles(e'), ts[E] = total, where
-// tiles(e) = per_tile_n * row_tiles(count(e)).  Warp 0 scans 32 experts at a
-// time with shuffles; the block must sync afterwards.
-template <typename RowTiles>
-__device__ __forceinline__ void tile_prefix_of(const int32_t* off_s, int32_t E,
-                                               int32_t per_tile_n, int32_t* ts,
-                                               RowTiles row_tiles) {
+// tiles(e) = per_tile_n * ceil(count(e) / rows_per_tile).  Warp 0 scans 32
+// experts at a time with shuffles; the block must sync afterwards.
+__device__ __forceinline__ void tile_prefix(const int32_t* off_s, int32_t E,
+                                            int32_t rows_per_tile,
+                                            int32_t per_tile_n, int32_t* ts) {
   if (threadIdx.x >= 32) return;
   const int lane = threadIdx.x;
   int32_t carry = 0;
@@ -477,7 +463,7 @@ __device__ __forceinline__ void tile_prefix_of(const int32_t* off_s, int32_t E,
     int32_t v = 0;
     if (e < E) {
       const int32_t cnt = off_s[e + 1] - off_s[e];
-      v = per_tile_n * row_tiles(cnt);
+      v = per_tile_n * ((cnt + rows_per_tile - 1) / rows_per_tile);
     }
     int32_t incl = v;
 #pragma unroll
@@ -489,15 +475,6 @@ __device__ __forceinline__ void tile_prefix_of(const int32_t* off_s, int32_t E,
     carry += __shfl_sync(0xffffffffu, incl, 31);
   }
   if (lane == 0) ts[E] = carry;
-}
-
-// The same with row_tiles(count) = ceil(count / rows_per_tile).
-__device__ __forceinline__ void tile_prefix(const int32_t* off_s, int32_t E,
-                                            int32_t rows_per_tile,
-                                            int32_t per_tile_n, int32_t* ts) {
-  tile_prefix_of(off_s, E, per_tile_n, ts, [=](int32_t cnt) {
-    return (cnt + rows_per_tile - 1) / rows_per_tile;
-  });
 }
 
 // Expert whose row range holds row p (binary search, p in [0, P)).

@@ -39,6 +39,14 @@ def _with_traffic(tmp_path, monkeypatch, entry):
     return src
 
 
+def test_committed_traffic_is_of_the_committed_sources():
+    """The headline's measured bytes: an edit of a source that they were captured
+    with needs a new capture, or has to go where those kernels do not see it."""
+    with open(os.path.join(ROOT, "profiles", "traffic.json")) as f:
+        names = [n for n in json.load(f) if not n.startswith("_")]
+    assert names and all(bench.load_traffic(n) for n in names)
+
+
 def test_traffic_reported_only_while_the_source_hash_matches(tmp_path, monkeypatch):
     digest = hashlib.sha256(b"kernel source v1\n").hexdigest()
     src = _with_traffic(tmp_path, monkeypatch,
