@@ -37,8 +37,27 @@ if not os.path.exists(LIB_PATH):
 
 lib = C.CDLL(LIB_PATH)
 
+
+
+class _NoHost:
+    """In the place of _host.so when it does not load: the other entry points
+    need libgbw.so alone, these say what is missing when they are called."""
+
+    def __init__(self, why: ImportError):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(
+            f"{os.path.join(_HERE, '_host.so')} does not load ({self._why}): build it with "
+            "`python -m grouped_bit_weight_b200.build` (g++, this torch). "
+            "There is no fallback.") from self._why
+
+
 # checks, allocations and calls of the entry points that take microseconds
-from . import _host  # noqa: E402
+try:
+    from . import _host  # noqa: E402
+except ImportError as _e:
+    _host = _NoHost(_e)
 
 MODE_AUTO, MODE_GEMM, MODE_GEMV = 0, 1, 2
 FLAG_OVERLAP_PREV = 0x100
@@ -90,7 +109,8 @@ class GbwError(RuntimeError):
         self.status = status
 
 
-_host.set_error(GbwError)
+if not isinstance(_host, _NoHost):
+    _host.set_error(GbwError)
 
 
 def _check(status: int, where: str) -> None:

@@ -21,6 +21,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgbw.so")
 HOST_SRC = os.path.join(CSRC, "host.cpp")
 HOST = os.path.join(HERE, "_host.so")
+HOST_STAMP = os.path.join(BUILD, "host.txt")  # what _host.so was built against
 HEADER = os.path.join(HERE, "..", "include", "gbw.h")
 
 NVCC = os.environ.get("NVCC", "nvcc")
@@ -58,13 +59,27 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def _host_stamp() -> str:
+    import torch
+    return f"torch {torch.__version__}, cuda {torch.version.cuda}, python {sys.version}"
+
+
+def host_up_to_date() -> bool:
+    """Whether _host.so is newer than its sources and of this torch and Python."""
+    if not os.path.exists(HOST) or not os.path.exists(HOST_STAMP):
+        return False
+    t = os.path.getmtime(HOST)
+    with open(HOST_STAMP) as f:
+        return (f.read() == _host_stamp()
+                and all(os.path.getmtime(d) <= t for d in (HOST_SRC, HEADER, __file__)))
+
+
 def _host(force: bool) -> None:
     """_host.so: against torch's headers, linked to libgbw.so beside it."""
-    deps = [HOST_SRC, HEADER, __file__]
-    if not force and os.path.exists(HOST) and all(
-            os.path.getmtime(d) <= os.path.getmtime(HOST) for d in deps):
+    if not force and host_up_to_date():
         return
     import torch
+    os.makedirs(BUILD, exist_ok=True)
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(NVCC) or NVCC)))
     inc = [os.path.join(root, "include"), os.path.join(root, "include/torch/csrc/api/include"),
@@ -79,6 +94,8 @@ def _host(force: bool) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {HOST_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, HOST)
+    with open(HOST_STAMP, "w") as f:
+        f.write(_host_stamp())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
