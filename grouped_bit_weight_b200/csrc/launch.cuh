@@ -114,11 +114,12 @@ cudaError_t launch_gemm_a4(const uint8_t* xq, const uint8_t* xs, int64_t P, int6
                            const int32_t* offsets, uint16_t* out, int* err, int num_sms,
                            cudaStream_t s);
 
-// The same for rows in eight 4-bit pieces each (16 bits of a block's maximum):
+// The same for rows in kPieces 4-bit pieces each (32 bits of a block's maximum):
 // bf16 rows gathered through r2t, or silu(gate) * up of fp32 rows [2K], to codes
-// [P * 8, K / 2] and scale words [ceil(K / 128)][P * 8]; their product with MXFP4
-// weights, summed over the pieces in fp32, [P, N].  Both start behind the kernel
+// [P * kPieces, K / 2] and scale words [ceil(K / 128)][P * kPieces]; their product
+// with MXFP4 weights, summed over the pieces in fp32, [P, N].  Both start behind the kernel
 // before them and wait for it.
+constexpr int kPieces = 16;
 cudaError_t launch_quantize_pieces(const void* x, int64_t T, int64_t K, const int32_t* r2t, int64_t P,
                                    bool glu, uint8_t* codes, uint32_t* scales, int* err,
                                    cudaStream_t s);

@@ -43,12 +43,11 @@
 // (0.97 / 2.5 TB/s).
 //
 // (2) MXFP4 on more weights: no lookups and no mma.sync, the
-// packed weights go to tcgen05 as they are.  x and h become rows of eight 4-bit
-// pieces (a4.cu: 16 bits of each 32-block's maximum) and the block-scaled 4-bit
+// packed weights go to tcgen05 as they are.  x and h become rows of sixteen 4-bit
+// pieces (a4.cu: 32 bits of each 32-block's maximum) and the block-scaled 4-bit
 // product sums a row's pieces in fp32: logits, routing, pieces of x, gate_up,
 // SwiGLU + pieces of h, down, combine, seven launches behind one another.  32
-// tokens: 98 us (4.3 TB/s; the two products take their weights at 5.3 and 4.7)
-// against 157 of (1).
+// tokens: 104 us (4.0 TB/s) against 154 of (1).
 #include <algorithm>
 #include <cmath>
 
@@ -1083,11 +1082,11 @@ PiecesLayout pieces_layout(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I
   put(l.r2t, P * 4);
   put(l.ros, P * 4);
   put(l.sor, P * 4);
-  put(l.xq, P * 8 * (H / 2));
-  put(l.xs, P * 8 * ((H + 127) / 128) * 4);
+  put(l.xq, P * kPieces * (H / 2));
+  put(l.xs, P * kPieces * ((H + 127) / 128) * 4);
   put(l.gu, P * 2 * I * 4);
-  put(l.hq, P * 8 * (I / 2));
-  put(l.hs, P * 8 * ((I + 127) / 128) * 4);
+  put(l.hq, P * kPieces * (I / 2));
+  put(l.hs, P * kPieces * ((I + 127) / 128) * 4);
   put(l.y, P * H * 4);
   return l;
 }
@@ -1131,14 +1130,18 @@ cudaError_t launch_pieces(const LayerProblem& p, uint8_t* w, int num_sms, cudaSt
                             num_sms, s);
 }
 
-// Whether MXFP4 takes that way: its five launches more cost 1 to 3 us, its
-// products take the weights nearer to the memory rate, so it pays from 100 MB of
-// codes on.  T tokens that choose independently are expected to need
-// E (1 - (1 - k / E)^T) experts.  us, (1) / (2), and those experts' codes:
-//   hidden 2880, 4 of 32 experts   1 token 35 / 35 (50 MB), 2: 47 / 46 (93),
-//     3: 61 / 50 (131), 4: 70 / 58 (164), 8: 98 / 75 (260), 32: 157 / 98 (393)
-//   hidden 2048, intermediate 768, 8 of 128   1: 24 / 27 (19), 6: 48 / 50 (97),
-//     8: 55 / 55 (122), 12: 66 / 65 (163), 16: 78 / 74 (195), 32: 107 / 91 (264)
+// Whether MXFP4 takes that way: its five launches more cost 1 to 7 us, its
+// products take the weights nearer to the memory rate, so it pays from some
+// number of bytes on: 50 to 180 MB of codes, fewer where an expert has more of the
+// tokens.  At 100 MB no measured size loses more than 3 us.  T tokens that choose
+// independently are expected to need E (1 - (1 - k / E)^T) experts.  us, (1) / (2),
+// and those experts' codes:
+//   hidden 2880, 4 of 32 experts   1 token 35 / 36 (50 MB), 2: 47 / 46 (93),
+//     3: 61 / 52 (131), 4: 70 / 60 (165), 8: 99 / 79 (261), 32: 154 / 104 (393)
+//   hidden 2048, intermediate 768, 8 of 128   6: 50 / 54 (97), 8: 57 / 58 (122),
+//     12: 66 / 69 (163), 16: 80 / 78 (194), 32: 108 / 96 (264)
+//   hidden 4096, intermediate 2048, 2 of 8   1: 23 / 30 (25), 4: 47 / 40 (69),
+//     8: 52 / 43 (91), 32: 69 / 48 (101)
 bool takes_pieces(const LayerProblem& p) {
   const double experts = p.E * (1.0 - std::pow(1.0 - (double)p.k / p.E, (double)p.T));
   constexpr int64_t most = (int64_t)65535 * 256;  // a launch's grid of 256-value pieces

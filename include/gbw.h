@@ -319,7 +319,8 @@ GBW_API gbw_status gnf4_moe_layer(const uint16_t* x, int64_t T, int64_t H,
 /* The same with MXFP4 experts (blocks [E, 2I, H/32, 16] + scales [E, 2I, H/32],
  * blocks [E, H, I/32, 16] + scales [E, H, I/32], e8m0).  From 100 MB of codes
  * of the experts that T tokens are expected to choose, seven launches: x and h
- * are kept to 2^-16 of the largest of each 32 columns. */
+ * are kept to 2^-32 of the largest of each 32 columns (so a bf16 x whole, down to
+ * 2^-24 of it). */
 GBW_API gbw_status gmxfp4_moe_layer(const uint16_t* x, int64_t T, int64_t H,
                                     const uint16_t* router_w, const float* router_bias,
                                     const uint8_t* gu_blocks, const uint8_t* gu_scales,

@@ -385,6 +385,27 @@ def test_large_layer_rows_streams_and_graphs():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("ratio", [10, 17, 21])
+@pytest.mark.parametrize("where", ["x", "h"])
+def test_large_layer_with_a_large_value_in_every_block(where, ratio):
+    """Of each 32 values of h one is 2^ratio times the others, of x three are 2^ratio,
+    2^(2 ratio / 3) and 2^(ratio / 3) times them, and their weights are zero: the
+    others make the result, at full precision."""
+    E, H, I = 32, 2880, 2880
+    m = Large(E, 4, H, I, ratio)
+    x = _x(4, H, 4)
+    if where == "x":
+        for i, c in enumerate((4, 6, 8)):
+            x[:, c::32] *= 2.0 ** (ratio * (i + 1) // 3)
+            m.rw[:, c::32] = 0
+            m.gu[..., c // 2] &= 0xF0  # column c of each block: a byte's low nibble
+    else:
+        m.gs[:, I + 6::32] += ratio    # the up rows of columns 6
+        m.dn[..., 3] &= 0xF0
+    m.check(x, m(x))
+
+
+@pytest.mark.gpu
 def test_layers_in_graphs_behind_copies_and_one_another():
     """Layers of both kinds one behind the other in a graph, in between copies,
     fills and a join of two streams, sharing one workspace."""
