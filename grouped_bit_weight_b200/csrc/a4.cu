@@ -43,6 +43,7 @@
 // precision on the same path.
 #include "common.cuh"
 #include "launch.cuh"
+#include "swiglu.cuh"
 
 namespace gbw {
 
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(32 * kQRows) quantize_rows_kernel(
       unpack8(u[i], w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[j] = __fdividef(v[j], 1.0f + __expf(-v[j])) * w[j];
+        v[j] = swiglu(v[j], w[j]);
         m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
       }
     } else {  // two at a time
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(32 * kQRows) quantize_pieces_kernel(
       const float gate[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
       const float up[8] = {d.x, d.y, d.z, d.w, e.x, e.y, e.z, e.w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fdividef(gate[j], 1.0f + __expf(-gate[j])) * up[j];
+      for (int j = 0; j < 8; ++j) v[j] = swiglu(gate[j], up[j]);
     }
   } else {
     const int64_t t = token_of_row(r2t, (int32_t)p, T, lane == 0 ? err : nullptr);

@@ -54,6 +54,7 @@
 #include "common.cuh"
 #include "launch.cuh"
 #include "route.cuh"
+#include "swiglu.cuh"
 
 namespace gbw {
 
@@ -786,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
         if (c < cnt) {
           const int slot = rows[r0 + c];
           const float gate = d[j] * kUnscale, up = d[2 + j] * kUnscale;
-          const float h = __fdividef(gate, 1.0f + __expf(-gate)) * up;
+          const float h = swiglu(gate, up);
           const __nv_bfloat16 hi = __float2bfloat16_rn(h);
           // an infinite high part keeps a zero low part (inf - inf is NaN)
           const float low = h - __bfloat162float(hi);

@@ -108,6 +108,23 @@ def test_quantize_rows_swiglu(T, K):
     assert torch.equal(c2, codes[perm.long().to(DEV)]) and torch.equal(s2, scales[:, perm.long().to(DEV)])
 
 
+@pytest.mark.gpu
+def test_quantize_rows_swiglu_of_gates_far_below_zero():
+    """Blocks of gates down to -91, whose silu is about 1e-37: fp32 and the scale
+    byte hold it.  Error: __expf's bound, 2 + 1.173 * 91 = 109 steps of 2^-23 or
+    2^-16.2, a subnormal e^-91 rounded by 2^-149 or 2^-18.7 of it, 4 roundings."""
+    gates = torch.tensor([-80.0, -86.0, -87.0, -87.5, -88.0, -88.5, -89.0, -90.0, -91.0])
+    x = torch.empty((4 * len(gates), 128))
+    x[:, :64] = gates.repeat(4)[:, None]
+    x[:, 64:] = _bf16((len(x), 64), 7).float() * 10.0 ** torch.arange(4).repeat_interleave(len(gates))[:, None]
+    x = x.to(torch.bfloat16)
+    codes, scales = gbw.gmxfp4_quantize_rows(x.to(DEV), swiglu=True)
+    got = _values(_codes(codes), _scales(scales, 64))
+    h = mp.silu(x[:, :64].double().numpy()) * x[:, 64:].double().numpy()
+    lo, hi = (mp.mxfp4(h * (1 + s * 2.0 ** -15))[2] for s in (-1, 1))
+    assert ((got == lo) | (got == hi)).all() and (got != 0).any(1).all()
+
+
 def _check_product(counts, N, K, seed, rows_pad=0, xstd=None):
     E, P = len(counts), int(sum(counts))
     w, ws, wv = _weights(E, N, K, seed)
