@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
     if (lane < k) {
       ids[t * k + lane] = id;
       wts[t * k + lane] = w;
-      atomicOr(&count[id], 1 << t);
+      atomicOr(&count[id], (int)(1u << t));
     }
   }
   __syncthreads();
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int slot = threadIdx.x + j * kThreads;
-      at[j] = slot < P ? __popc(count[ids[slot]] & ((1 << (slot / k)) - 1)) : 0;
+      at[j] = slot < P ? __popc((unsigned)count[ids[slot]] & ((1u << (slot / k)) - 1u)) : 0;
     }
     int incl = sum;
 #pragma unroll
