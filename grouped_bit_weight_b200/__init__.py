@@ -62,7 +62,6 @@ except ImportError as _e:
 MODE_AUTO, MODE_GEMM, MODE_GEMV = 0, 1, 2
 FLAG_OVERLAP_PREV = 0x100
 DEVERR_OFFSETS, DEVERR_TOKEN, DEVERR_TIMEOUT, DEVERR_ROUTE = 1, 2, 4, 8
-LOGITS_BF16, LOGITS_FP32 = 0, 1
 _STATUS = {0: "GBW_OK", 1: "GBW_ERR_NULL", 2: "GBW_ERR_SHAPE",
            3: "GBW_ERR_ALIGN", 4: "GBW_ERR_ARCH", 5: "GBW_ERR_LAUNCH",
            6: "GBW_ERR_DEVICE"}
