@@ -72,7 +72,9 @@ typedef enum {
 /* Bits of the device error word. */
 #define GBW_DEVERR_OFFSETS 1 /* expert_offsets not 0 <= ... <= P (clamped) */
 #define GBW_DEVERR_TOKEN 2   /* row_to_token[p] outside [0, T) (clamped) */
-#define GBW_DEVERR_TIMEOUT 4 /* a pipeline wait gave up; output incomplete */
+#define GBW_DEVERR_TIMEOUT 4 /* a pipeline wait gave up (or the whole layer's shared
+                                memory does not start where it counts on);
+                                output incomplete */
 #define GBW_DEVERR_ROUTE 8   /* an expert id or a routed row out of range, or
                                 slot_of_row not the inverse of row_of_slot
                                 (the slot is left out) */
