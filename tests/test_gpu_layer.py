@@ -485,6 +485,119 @@ def test_large_layer_of_a_token_with_nan_is_nan():
     assert gbw.device_status() == 0
 
 
+# ---------------------------------------------------------------- rows and batches
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["nf4", "mxfp4"])
+def test_layer_values_of_tiny_and_huge_rows(fmt):
+    """Rows of very different magnitude, each against its own 64-bit value at its
+    own scale; the bias chooses their experts, different ones for equal logits.
+    (Of 1e-20 and 1e-30, h is below what fp32 holds: zeros.)"""
+    m = Layer(fmt, 8, 2, 256, 128, seed=3)
+    m.rb = torch.tensor([0.5, -1.0, 3.0, 0.25, -2.0, 2.5, 0.0, 1.0])
+    m.kw["router_bias"] = m.rb.to(DEV)
+    scale = torch.tensor([1e-12, 1e-4, 0.0, 30.0, 1.0, 1e-30, 1e-8, 1e-15, 1e-20, 3e4, 1e-17])[:, None].to(DEV)
+    x = (_x(len(scale), 256, 4).float() * scale).to(torch.bfloat16)
+    got = m(x)
+    for t in range(len(x)):
+        m.check(x[t:t + 1], got[t:t + 1])
+    assert (got[2] == 0).all() and (got[0].abs() > 1e-30).any() and (got[9].abs() > 1e6).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["nf4", "mxfp4"])
+def test_layer_of_single_tokens_and_parts_of_a_batch(fmt):
+    """A token alone, in a part of the batch and in the whole: the sums may be
+    split otherwise, so each is held to the 64-bit value, and two of them to one
+    another by twice the allowed error and a rounding each."""
+    m = Layer(fmt, 16, 4, 256, 192, seed=6)
+    x = _x(24, 256, 8)
+    whole = m(x)
+    _, tol, _ = m.plain(x)
+    for a, b in ((0, 1), (5, 6), (23, 24), (0, 7), (3, 20), (12, 24), (0, 24)):
+        part = m(x[a:b].contiguous())
+        m.check(x[a:b], part)
+        assert torch.equal(m(x[a:b].contiguous()), part)
+        p, w = part.cpu().double().numpy(), whole[a:b].cpu().double().numpy()
+        assert (np.abs(p - w) <= 2.0 ** -7 * np.maximum(np.abs(p), np.abs(w)) + 2 * tol[a:b]).all()
+
+
+@pytest.mark.gpu
+def test_large_layer_of_single_tokens_and_parts_of_a_batch():
+    """The same with a batch that takes rows in pieces and tokens that do not."""
+    m = Large(32, 4, 2880, 2880, 8)
+    x = _x(32, 2880, 9) * torch.logspace(-6, 1, 32, base=10.0).to(DEV)[:, None].to(torch.bfloat16)
+    whole = m(x)
+    m.check(x, whole)
+    for a, b in ((0, 1), (9, 10), (31, 32), (4, 6), (10, 13), (7, 27)):
+        m.check(x[a:b], m(x[a:b].contiguous()))
+        m.check(x[a:b], whole[a:b])
+
+
+class Wide:
+    """An NF4 layer of many experts; its 64-bit values are computed on the GPU."""
+
+    def __init__(self, E, k, H, I, seed):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        self.E, self.k, self.H, self.I = E, k, H, I
+        codes = lambda *s: torch.randint(0, 256, s, generator=g, dtype=torch.uint8, device=DEV)
+        absmax = lambda std, *s: std * (2 + torch.rand(s, generator=g, device=DEV))
+        self.gu, self.gs = codes(E, 2 * I, H // 2), absmax(H ** -0.5, E, 2 * I, H // 64)
+        self.dn, self.ds = codes(E, H, I // 2), absmax(I ** -0.5, E, H, I // 64)
+        self.rw = (torch.randn((E, H), generator=g, device=DEV) * 1.5 / H ** 0.5).to(torch.bfloat16)
+
+    def __call__(self, x):
+        return gbw.gnf4_moe_layer(x, self.rw, self.gu, self.gs, self.dn, self.ds, k=self.k)
+
+    def weight(self, codes, absmax, e):
+        q = torch.stack([codes[e] >> 4, codes[e] & 15], -1).flatten(1).long()
+        return torch.from_numpy(mp.NF4).to(DEV)[q] * absmax[e].double().repeat_interleave(64, 1)
+
+    def check(self, x, got):
+        xd = x.double()
+        l, mag = xd @ self.rw.double().T, xd.abs() @ self.rw.double().abs().T
+        ids, w = mp.route(l.cpu().numpy(), self.k, True)
+        dl = 2.0 ** -24 * (self.H / 256 * 8 + 16) * mag.max(1).values.cpu().numpy()
+        s = -np.sort(-l.cpu().numpy(), 1)
+        assert (s[:, self.k - 1] - s[:, self.k] > 2 * dl).all(), "a choice next to a tie"
+        ref, tol = torch.zeros_like(xd), torch.zeros_like(xd)
+        # as in Layer.plain: the levels' error, sums of H and I products, h kept to 2^-16
+        e1, e2 = (_levels_error() + 2.0 ** -22 + (n + 8) * 2.0 ** -24 for n in (self.H, self.I))
+        for e in np.unique(ids):
+            t, j = np.nonzero(ids == e)
+            we = torch.from_numpy(w[t, j]).to(DEV)[:, None]
+            t = torch.from_numpy(t).to(DEV)
+            gw, dw = self.weight(self.gu, self.gs, e), self.weight(self.dn, self.ds, e)
+            (g, u), (dg, du) = (v.split(self.I, 1) for v in (xd[t] @ gw.T, e1 * (xd[t].abs() @ gw.abs().T)))
+            silu = torch.nn.functional.silu(g)
+            h = silu * u
+            dh = 1.1 * dg * (u.abs() + du) + silu.abs() * du + 2.0 ** -16 * h.abs()
+            y, dy = h @ dw.T, (dh + e2 * h.abs()) @ dw.abs().T
+            rel = torch.from_numpy(4 * dl + (17 + self.k) * 2.0 ** -24).to(DEV)[t][:, None]
+            ref.index_add_(0, t, we * y)
+            tol.index_add_(0, t, we * (dy + rel * y.abs()))
+        got, ref, tol = (v.cpu().double().numpy() for v in (got, ref, tol))
+        mp.bf16_close(got, ref, tol)
+        # the levels are off by 6.3e-4 of their root mean square, in gate (by silu'
+        # at most 1.1 times), up and down; the output by one rounding, 2^-8 / sqrt(3)
+        # at most; a tenth for the spread
+        err = np.linalg.norm(got - ref) / np.linalg.norm(ref)
+        assert err < 1.1 * ((1.1 ** 2 + 2) * 6.3e-4 ** 2 + 2.0 ** -16 / 3) ** 0.5, err
+        assert gbw.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 2, 8, 32])
+def test_nf4_layer_at_a_decode_shape(T):
+    """128 experts of which 8 are chosen, 2048 x 768, from one token to the most."""
+    m = Wide(128, 8, 2048, 768, T)
+    x = _x(T, 2048, T + 1)
+    got = m(x)
+    m.check(x, got)
+    assert torch.equal(m(x), got)
+
+
 # ---------------------------------------------------------------- refusals
 
 
