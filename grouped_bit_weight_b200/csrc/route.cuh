@@ -43,15 +43,11 @@ template <typename TL, int NPL>
 __device__ __forceinline__ void choose(const TL* row, int E, int k, int renorm, bool nan_rows,
                                        int lane, int& id, float& w) {
   uint32_t key[NPL];
-  bool nan = false;
 #pragma unroll
   for (int j = 0; j < NPL; ++j) {
     const int e = j * 32 + lane;
-    const float l = e < E ? load_logit(row + e) : 0.0f;
-    nan |= l != l;
-    key[j] = e < E ? order_key(no_nan(l)) : 0u;
+    key[j] = e < E ? order_key(no_nan(load_logit(row + e))) : 0u;
   }
-  nan = nan_rows && __any_sync(0xffffffffu, nan);
   float all = 0.0f, m = 0.0f, v = 0.0f;
   if (NPL <= 4) {
     // each lane's keys in falling order (equal ones by index), so that a
@@ -125,7 +121,16 @@ __device__ __forceinline__ void choose(const TL* row, int E, int k, int renorm, 
   }
   const float p = lane < k ? share(v, m) : 0.0f;
   const float total = renorm ? warp_sum(p) : all;
-  w = m == __int_as_float(0xFF800000) ? (nan ? __int_as_float(0x7FC00000) : 0.0f) : p / total;
+  w = p / total;
+  if (m == __int_as_float(0xFF800000)) {  // rare, so read again (a flag kept above: 0.1 to 0.5 us)
+    bool nan = false;
+    if (nan_rows)
+      for (int e = lane; e < E; e += 32) {
+        const float l = load_logit(row + e);
+        nan |= l != l;
+      }
+    w = __any_sync(0xffffffffu, nan) ? __int_as_float(0x7FC00000) : 0.0f;
+  }
 }
 
 }  // namespace gbw
