@@ -61,6 +61,7 @@ struct RouteProblem {
   int32_t* slot_of_row;   // [P]
   int32_t* hist;       // workspace [CTAs, E]
   bool nan_rows = false;  // NaN weights for a token of NaN logits and no number
+                          // (fp32 logits of at most 128 tokens)
 };
 
 // CTAs of the routing's first kernel (1: one kernel does it all), and so the

@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
   for (int t = warp; t < T; t += kWarps + 1) {
     int id = 0;
     float w = 0.0f;
-    choose<float, NPL>(a.logits + (int64_t)t * E, E, k, p.renorm, true, lane, id, w);
+    choose<float, NPL, true>(a.logits + (int64_t)t * E, E, k, p.renorm, lane, id, w);
     if (lane < k) {
       ids[t * k + lane] = id;
       wts[t * k + lane] = w;

@@ -21,6 +21,8 @@
 // for 4 tokens: 4.3 us on the device; for 4096: 8.4; 4 of 32 for 16411 tokens
 // with the gradient: 17.8.  On the host a call takes 7 to 15 us, what bounds the
 // small ones.
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.cuh"
 #include "route.cuh"
@@ -111,7 +113,7 @@ struct Slots {
 
 // Chooses the experts of tokens [b * per, (b + 1) * per) and counts them;
 // kSingle (one CTA): sorts and places them too.
-template <typename TL, int NPL, bool kSingle>
+template <typename TL, int NPL, bool kSingle, bool kNanRows = false>
 __global__ void __launch_bounds__(kThreads) route_choose(const RouteProblem p, const int per) {
   extern __shared__ int sm[];
   // kSingle: part [kWarps], whist [kWarps][E]; else count [E]
@@ -128,8 +130,7 @@ __global__ void __launch_bounds__(kThreads) route_choose(const RouteProblem p, c
     const int64_t t = t0 + i;
     int id = 0;
     float w = 0.0f;
-    choose<TL, NPL>(reinterpret_cast<const TL*>(p.logits) + t * E, E, k, p.renorm, p.nan_rows,
-                    lane, id, w);
+    choose<TL, NPL, kNanRows>(reinterpret_cast<const TL*>(p.logits) + t * E, E, k, p.renorm, lane, id, w);
     if (lane < k) {
       p.ids[t * k + lane] = id;
       p.weights[t * k + lane] = w;
@@ -227,11 +228,10 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(
       if (id < 0 || id >= E) {
         raise_error(err, GBW_DEVERR_ROUTE);
         id = -1;
-        w = 0.0f;  // the slot is left out: it is no part of the sum either
       }
     }
-    // a weight of zero passes nothing on, whatever dw holds
-    const float wdw = w == 0.0f ? 0.0f : w * dw;
+    // a weight of zero passes nothing on, whatever dw holds, nor does a bad id
+    const float wdw = w == 0.0f || id < 0 ? 0.0f : w * dw;
     const float sum = warp_sum(wdw);
     if (renorm) {
       for (int e = lane; e < E; e += 32) row[e] = 0.0f;
@@ -393,15 +393,21 @@ size_t choose_smem(int E, bool single) {
 }
 size_t place_smem(int E) { return 4 * (kWarps + 2 * kThreads + (size_t)kWarps * E); }
 
+template <auto Fn>
+cudaError_t single_t(const RouteProblem& p, int per, bool dependent, cudaStream_t s) {
+  cudaError_t e = opt_in_smem<Fn>(choose_smem(kMaxE, true));
+  if (e != cudaSuccess) return e;
+  return launch_kernel<Fn>(1, kThreads, choose_smem(p.E, true), s, dependent, p, per);
+}
+
 template <typename TL, int NPL>
 cudaError_t route_t(const RouteProblem& p, int num_sms, bool dependent, cudaStream_t s) {
   const int ctas = route_ctas(p.T, num_sms);
   const int per = (int)((p.T + ctas - 1) / ctas);
   if (ctas == 1) {
-    constexpr auto k = route_choose<TL, NPL, true>;
-    cudaError_t e = opt_in_smem<k>(choose_smem(kMaxE, true));
-    if (e != cudaSuccess) return e;
-    return launch_kernel<k>(1, kThreads, choose_smem(p.E, true), s, dependent, p, per);
+    if (std::is_same<TL, float>::value && p.nan_rows)
+      return single_t<route_choose<float, NPL, true, true>>(p, per, dependent, s);
+    return single_t<route_choose<TL, NPL, true>>(p, per, dependent, s);
   }
   cudaError_t e = opt_in_smem<route_place>(place_smem(kMaxE));
   if (e != cudaSuccess) return e;

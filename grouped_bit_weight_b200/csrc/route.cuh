@@ -37,11 +37,11 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // The choice of one token: lane s < k gets the s-th expert and its weight.  A
-// token without any logit above -inf gets weights of 0; with nan_rows (the whole
+// token without any logit above -inf gets weights of 0; with kNanRows (the whole
 // layer, which shows nothing of its logits) weights of NaN when one of them is NaN.
-template <typename TL, int NPL>
-__device__ __forceinline__ void choose(const TL* row, int E, int k, int renorm, bool nan_rows,
-                                       int lane, int& id, float& w) {
+template <typename TL, int NPL, bool kNanRows>
+__device__ __forceinline__ void choose(const TL* row, int E, int k, int renorm, int lane, int& id,
+                                       float& w) {
   uint32_t key[NPL];
 #pragma unroll
   for (int j = 0; j < NPL; ++j) {
@@ -121,15 +121,14 @@ __device__ __forceinline__ void choose(const TL* row, int E, int k, int renorm, 
   }
   const float p = lane < k ? share(v, m) : 0.0f;
   const float total = renorm ? warp_sum(p) : all;
-  w = p / total;
-  if (m == __int_as_float(0xFF800000)) {  // rare, so read again (a flag kept above: 0.1 to 0.5 us)
+  w = m == __int_as_float(0xFF800000) ? 0.0f : p / total;
+  if (kNanRows && m == __int_as_float(0xFF800000)) {  // rare, so read again
     bool nan = false;
-    if (nan_rows)
-      for (int e = lane; e < E; e += 32) {
-        const float l = load_logit(row + e);
-        nan |= l != l;
-      }
-    w = __any_sync(0xffffffffu, nan) ? __int_as_float(0x7FC00000) : 0.0f;
+    for (int e = lane; e < E; e += 32) {
+      const float l = load_logit(row + e);
+      nan |= l != l;
+    }
+    if (__any_sync(0xffffffffu, nan)) w = __int_as_float(0x7FC00000);
   }
 }
 
