@@ -171,13 +171,13 @@ __global__ void __launch_bounds__(32 * kQRows) quantize_rows_kernel(
 }
 
 // A row in four-bit pieces (kPieces = 16), each an MXFP4 row of its own.  Piece j
-// quantises what pieces 0 .. j - 1 left, exactly known in fp32; a piece leaves at
-// most a quarter of its block's maximum (1 of [4, 6], less than 2 of [6, 8)), so
-// sixteen leave 2^-32 of it: less than fp32 sums of the block drop, and nothing of
-// a bf16 value down to 2^-24 of the maximum.  Eight (2^-16) took 3 to 6 % less
-// time for the whole layer (32 tokens of 2880: 98 instead of 104 us), but beside
-// fp32 values 2^17 times as large, or bf16 ones of three sizes up to 2^21, nothing was left of
-// a value: the whole result, where the weights of the large ones are zero.
+// quantises what pieces 0 .. j - 1 left, exactly known in fp32, with a quarter of
+// the scale before: what is below 8 scales leaves less than 2 (1 below 6, else
+// saturated), so sixteen leave 2^-32 of the block's maximum: less than fp32 sums of
+// the block drop, and nothing of a bf16 value down to 2^-24 of the maximum.  With
+// eight (2^-16) nothing was left of a value beside fp32 ones 2^17 times as large:
+// the whole result, where the weights of the large ones are zero.  (Scales from each
+// remainder's own maximum: 103 instead of 99 us for the layer of 32 tokens of 2880.)
 
 // A warp takes 256 values of a row, as above.  kGLU: fp32 rows [2K], silu(gate)
 // * up; else bf16 rows gathered through r2t.  Codes [P * kPieces, K / 2] and
@@ -207,40 +207,43 @@ __global__ void __launch_bounds__(32 * kQRows) quantize_pieces_kernel(
     const int64_t t = token_of_row(r2t, (int32_t)p, T, lane == 0 ? err : nullptr);
     if (c < U) unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + t * K) + c), v);
   }
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const uint32_t ex = m >> 23;
+  uint32_t byte = ex > 2u ? ex - 2u : 0u;
+  // the four blocks of 16 lanes make a word; a block with a value that is not finite
+  // is NaN by its first piece
+  uint32_t w = (c >= U ? 127u : ex == 255u ? 255u : byte) << (8 * ((lane >> 2) & 3));
+  w |= __shfl_xor_sync(0xffffffffu, w, 4);
+  w |= __shfl_xor_sync(0xffffffffu, w, 8);
+  // each of them writes a piece's
+  static_assert(kPieces == 16, "a lane per piece");
+  if ((c >> 4) < (K + 127) / 128)
+    scales[(int64_t)(c >> 4) * (P * kPieces) + p * kPieces + (lane & 15)] =
+        __vsubus4(w, 0x02020202u * (lane & 15));
+  if (c >= U) return;
+  if (ex == 255u)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
   uint32_t* out = reinterpret_cast<uint32_t*>(codes) + p * kPieces * U + c;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t ex = m >> 23;
-    uint32_t byte = ex > 2u ? ex - 2u : 0u;
+    const float inv = __uint_as_float((254u - byte) << 23);
+    const float back = byte ? __uint_as_float(byte << 23) : __uint_as_float(0x00400000u);
     uint32_t q = 0;
-    if (ex == 255u) {
-      byte = 255u;  // a value that is not finite: the block is NaN, by its first piece
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    } else if (m) {
-      const float inv = __uint_as_float((254u - byte) << 23);
-      const float back = byte ? __uint_as_float(byte << 23) : __uint_as_float(0x00400000u);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t two = e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv);
-        const float2 was = e2m1_values(two);
-        v[2 * j] = fmaf(-was.x, back, v[2 * j]);
-        v[2 * j + 1] = fmaf(-was.y, back, v[2 * j + 1]);
-        q |= two << (8 * j);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t two = e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv);
+      const float2 was = e2m1_values(two);
+      v[2 * j] = fmaf(-was.x, back, v[2 * j]);
+      v[2 * j + 1] = fmaf(-was.y, back, v[2 * j + 1]);
+      q |= two << (8 * j);
     }
-    if (c < U) out[i * U] = q;
-    if (c >= U) byte = 127u;
-    uint32_t w = byte << (8 * ((lane >> 2) & 3));
-    w |= __shfl_xor_sync(0xffffffffu, w, 4);
-    w |= __shfl_xor_sync(0xffffffffu, w, 8);
-    if ((lane & 15) == 0 && c < (K + 127) / 128 * 16)
-      scales[(int64_t)(c >> 4) * (P * kPieces) + p * kPieces + i] = w;
+    out[i * U] = q;
+    byte = byte > 2u ? byte - 2u : 0u;
   }
 }
 

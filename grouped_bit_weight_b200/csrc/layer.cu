@@ -47,7 +47,7 @@
 // pieces (a4.cu: 32 bits of each 32-block's maximum) and the block-scaled 4-bit
 // product sums a row's pieces in fp32: logits, routing, pieces of x, gate_up,
 // SwiGLU + pieces of h, down, combine, seven launches behind one another.  32
-// tokens: 104 us (4.0 TB/s) against 154 of (1).
+// tokens: 99 us (4.2 TB/s) against 154 of (1).
 #include <algorithm>
 #include <cmath>
 
@@ -1131,18 +1131,18 @@ cudaError_t launch_pieces(const LayerProblem& p, uint8_t* w, int num_sms, cudaSt
                             num_sms, s);
 }
 
-// Whether MXFP4 takes that way: its five launches more cost 1 to 7 us, its
+// Whether MXFP4 takes that way: its five launches more cost 1 to 4 us, its
 // products take the weights nearer to the memory rate, so it pays from some
-// number of bytes on: 50 to 180 MB of codes, fewer where an expert has more of the
-// tokens.  At 100 MB no measured size loses more than 3 us.  T tokens that choose
-// independently are expected to need E (1 - (1 - k / E)^T) experts.  us, (1) / (2),
-// and those experts' codes:
-//   hidden 2880, 4 of 32 experts   1 token 35 / 36 (50 MB), 2: 47 / 46 (93),
-//     3: 61 / 52 (131), 4: 70 / 60 (165), 8: 99 / 79 (261), 32: 154 / 104 (393)
-//   hidden 2048, intermediate 768, 8 of 128   6: 50 / 54 (97), 8: 57 / 58 (122),
-//     12: 66 / 69 (163), 16: 80 / 78 (194), 32: 108 / 96 (264)
-//   hidden 4096, intermediate 2048, 2 of 8   1: 23 / 30 (25), 4: 47 / 40 (69),
-//     8: 52 / 43 (91), 32: 69 / 48 (101)
+// number of bytes on: 40 to 110 MB of codes, fewer where an expert has more of the
+// tokens; from 100 MB it never measured slower.  T tokens that choose independently
+// are expected to need E (1 - (1 - k / E)^T) experts.  us, (1) / (2), and those
+// experts' codes:
+//   hidden 2880, 4 of 32 experts   1 token 34 / 35 (50 MB), 2: 47 / 46 (93),
+//     3: 61 / 50 (131), 4: 70 / 58 (165), 8: 99 / 76 (261), 32: 154 / 99 (393)
+//   hidden 2048, intermediate 768, 8 of 128   6: 50 / 51 (97), 8: 56 / 56 (122),
+//     12: 66 / 64 (163), 16: 80 / 73 (194), 32: 109 / 92 (264)
+//   hidden 4096, intermediate 2048, 2 of 8   1: 23 / 27 (25), 4: 47 / 39 (69),
+//     8: 51 / 41 (91), 32: 69 / 45 (101)
 bool takes_pieces(const LayerProblem& p) {
   const double experts = p.E * (1.0 - std::pow(1.0 - (double)p.k / p.E, (double)p.T));
   constexpr int64_t most = (int64_t)65535 * 256;  // a launch's grid of 256-value pieces
