@@ -10,8 +10,7 @@
 //             the products of 32-blocks and their two scales are exact in the
 //             tensor core, the sum is fp32, one rounding to bf16
 //
-// Quantise is bound by the instructions of its conversion, at about three
-// quarters of the memory rate.
+// Quantise is bound by the instructions of its conversion.
 //
 // Product, one persistent CTA per SM, 20 warps ("swap AB": MMA M is 128
 // weight rows, MMA N the routed rows of one expert, so few rows give a narrow
@@ -34,8 +33,8 @@
 // leaving out the stores, the scale loads or the row loads won 8, 10 and 1 % each.
 // The rest is waiting along the chain from an empty stage to a full one (scale bytes to
 // registers, shared memory, TMEM) and, for tiles over 192 rows, for the
-// epilogue.  4004 rows, 2880 x 2880: 43 us (1.5 PFLOP/s); 16 rows each of
-// 8 experts, 256 x 512: 5 us, latency.
+// epilogue.  4004 rows, 2880 x 2880: 41 us (1.6 PFLOP/s); 16 rows each of
+// 8 experts, 256 x 512: 4.4 us, latency.
 //
 // Rows in pieces (quantize_pieces_kernel, gemm_a4_kernel<kPieces>) are for the
 // layer of a few tokens: a bf16 or fp32 row becomes sixteen MXFP4 rows that sum to
@@ -97,8 +96,9 @@ __device__ __forceinline__ void unpack8(uint4 q, float (&v)[8]) {
 // A warp quantises kUnits * 256 values of a row, 8 a lane and unit; the 4 lanes
 // of a 32-block share its maximum.  The scale bytes of 128 k are one word, word
 // (k / 128) * P + p; a block's warps take neighbouring rows, whose words share a
-// sector.  8192 rows of 2880 take 11.4 us, 4004 SwiGLU rows 12.6 (5 and 4 TB/s
-// in and out), bound by about 60 and 130 instructions per unit.  (When they took
+// sector.  8192 rows of 2880, gathered from 2048 tokens, take 11.4 us (5 TB/s in and
+// out, most of it L2: 2.1 TB/s of distinct bytes), 4004 SwiGLU rows 12.6 (4 TB/s),
+// bound by about 60 and 140 instructions per unit.  (When they took
 // 12.8 and 13.1: rows by whole warps 12.1 and 14.3, one unit a warp 16.8 and 14.3,
 // six 12.3 and 13.1, but 2.7 instead of 2.3 us for a few rows.)
 constexpr int kQRows = 4;  // warps, and rows, of a block

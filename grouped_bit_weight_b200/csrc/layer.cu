@@ -35,12 +35,12 @@
 // is split over several warps (joined through shared memory in a fixed order)
 // when a CTA has fewer units than warps.
 // What bounds it is the latency of lookups and x loads at 11 warps an SM (168
-// registers a thread; 15 warps spill and took 58 instead of 55 us): over the
+// registers a thread; 15 warps spill and took 58 instead of 55 us for 8 tokens): over the
 // whole NF4 8-token kernel the shared-memory pipe is 44 % busy, issue 37 %, DRAM
 // 31 %.  With the lookups left out the MXFP4 32-token case fell from 165 to 137
-// us, with the loads of x 127, with the weight loads hardly.  Hidden 2880, 32 experts, MXFP4, 1 token: 34 us
-// (1.55 TB/s); hidden 2048, 128 experts, 8 chosen, NF4, 1 / 8 tokens: 22 / 55 us
-// (0.97 / 2.5 TB/s).
+// us, with the loads of x 127, with the weight loads hardly.  Hidden 2880, 32
+// experts, MXFP4, 1 token: 35 us (1.5 TB/s); hidden 2048, 128 experts, 8 chosen,
+// NF4, 1 / 8 / 32 tokens: 22 / 54 / 104 us (0.97 / 2.5 / 2.9 TB/s).
 //
 // (2) MXFP4 on more weights: no lookups and no mma.sync, the
 // packed weights go to tcgen05 as they are.  x and h become rows of sixteen 4-bit
