@@ -38,7 +38,6 @@ if not os.path.exists(LIB_PATH):
 lib = C.CDLL(LIB_PATH)
 
 
-
 class _NoHost:
     """In the place of _host.so when it does not load: the other entry points
     need libgbw.so alone, these say what is missing when they are called."""

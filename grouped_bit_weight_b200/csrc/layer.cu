@@ -176,12 +176,15 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router(const LayerArgs a) 
 // kernel 2
 // ----------------------------------------------------------------------
 
-// The NF4 levels enter the table times this, and the sums are divided by it:
-// of the factors in [1, 2) it is the one whose products with the 16 levels
-// round to bf16 with the least error, 6.3e-4 of their root mean square (1.1e-3
+// The NF4 levels enter the table times this, rounded to bf16, and the sums are
+// divided by it: of the factors in [1, 2) it is the one whose products with the 16
+// levels round with the least error, 6.3e-4 of their root mean square (1.1e-3
 // without it, as in the other NF4 calls, which round the level or the decoded
-// weight to bf16).  The output is then off by 2.0e-3 of its norm, 1.65e-3 of that
-// its own rounding to bf16.  Levels of full precision leave 1.65e-3 and cost time:
+// weight to bf16).  Levels 9 and 11 are rounded down instead, which makes 7.5e-4 of
+// it but takes the levels' mean error from 2.6e-4 to 9e-6: a mean error meets the
+// sum of a row's x, so that with x = 1 + N(0, 1) the output was off by 1.5e-2 of its
+// norm (now 1.8e-3).  With x = N(0, 1) it is off by 2.1e-3, 1.65e-3 of that its own
+// rounding to bf16.  Levels of full precision leave 1.65e-3 and cost time:
 // 2048 x 768, 1 / 8 / 32 tokens take 22 / 54 / 104 us as it is, 27 / 71 / 142 with
 // levels of a high and a low bf16 part (twice the lookups' bytes and mmas), 25 / 60
 // / 114 with fp16 levels (x and h scaled into fp16's range by powers of two, more
@@ -211,7 +214,8 @@ __device__ __forceinline__ uint32_t code_bf16(int q) {
     v = x ? (float)((2 + m) << (x - 1)) * 0.5f : 0.5f * m;
     v = q & 8 ? -v : v;
   }
-  return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  const bool down = F == Fmt::NF4 && (q == 9 || q == 11);
+  return __bfloat16_as_ushort(down ? __float2bfloat16_rd(v) : __float2bfloat16_rn(v));
 }
 
 // D = A (16 x 16, row) * B (16 x 8, col) (+ D), bf16 in, fp32 out.

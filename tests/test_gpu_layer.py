@@ -561,7 +561,11 @@ class Wide:
         dl = 2.0 ** -24 * (self.H / 256 * 8 + 16) * mag.max(1).values.cpu().numpy()
         s = -np.sort(-l.cpu().numpy(), 1)
         assert (s[:, self.k - 1] - s[:, self.k] > 2 * dl).all(), "a choice next to a tie"
-        ref, tol = torch.zeros_like(xd), torch.zeros_like(xd)
+        ref, tol, var = torch.zeros_like(xd), torch.zeros_like(xd), torch.zeros_like(xd)
+        # variance of a weight's error over absmax^2: the levels are off by 7.5e-4 of
+        # their root mean square, by 9e-6 of it in the mean
+        v0 = (7.5e-4 ** 2) * float((mp.NF4 ** 2).mean())
+        sq = lambda v: (v ** 2).reshape(len(v), -1, 64).sum(-1)  # over a block's columns
         # as in Layer.plain: the levels' error, sums of H and I products, h kept to 2^-16
         e1, e2 = (_levels_error() + 2.0 ** -22 + (n + 8) * 2.0 ** -24 for n in (self.H, self.I))
         for e in np.unique(ids):
@@ -574,16 +578,21 @@ class Wide:
             h = silu * u
             dh = 1.1 * dg * (u.abs() + du) + silu.abs() * du + 2.0 ** -16 * h.abs()
             y, dy = h @ dw.T, (dh + e2 * h.abs()) @ dw.abs().T
+            # the codes are random, so the errors of gate, up and down are independent
+            vg, vu = (v0 * (sq(xd[t]) @ (self.gs[e].double() ** 2).T)).split(self.I, 1)
+            s = torch.sigmoid(g)
+            vh = (s * (1 + g * (1 - s))) ** 2 * vg * u ** 2 + silu ** 2 * vu
+            vy = v0 * (sq(h) @ (self.ds[e].double() ** 2).T) + vh @ (dw ** 2).T
+            var.index_add_(0, t, we ** 2 * vy)
             rel = torch.from_numpy(4 * dl + (17 + self.k) * 2.0 ** -24).to(DEV)[t][:, None]
             ref.index_add_(0, t, we * y)
             tol.index_add_(0, t, we * (dy + rel * y.abs()))
         got, ref, tol = (v.cpu().double().numpy() for v in (got, ref, tol))
         mp.bf16_close(got, ref, tol)
-        # the levels are off by 6.3e-4 of their root mean square, in gate (by silu'
-        # at most 1.1 times), up and down; the output by one rounding, 2^-8 / sqrt(3)
-        # at most; a tenth for the spread
+        # and one rounding of the output, 2^-8 / sqrt(3) at most; a tenth for the spread
         err = np.linalg.norm(got - ref) / np.linalg.norm(ref)
-        assert err < 1.1 * ((1.1 ** 2 + 2) * 6.3e-4 ** 2 + 2.0 ** -16 / 3) ** 0.5, err
+        levels = float(var.sum()) / np.linalg.norm(ref) ** 2
+        assert err < 1.1 * (levels + 2.0 ** -16 / 3) ** 0.5, (err, levels)
         assert gbw.device_status() == 0
 
 
@@ -596,6 +605,17 @@ def test_nf4_layer_at_a_decode_shape(T):
     got = m(x)
     m.check(x, got)
     assert torch.equal(m(x), got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mean", [0.25, 1.0, -3.0])
+def test_nf4_layer_of_tokens_with_a_mean(mean):
+    """The levels' errors have hardly a mean that a mean of x could gather: the
+    error stays that of their spread."""
+    m = Wide(16, 4, 2048, 768, 5)
+    m.rw -= m.rw.float().mean(1, keepdim=True).to(torch.bfloat16)
+    x = (_x(8, 2048, 3).float() + mean).to(torch.bfloat16)
+    m.check(x, m(x))
 
 
 # ---------------------------------------------------------------- refusals
