@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router(const LayerArgs a) 
 // norm (now 1.8e-3).  With x = N(0, 1) it is off by 2.1e-3, 1.65e-3 of that its own
 // rounding to bf16.  Levels of full precision leave 1.65e-3 and cost time:
 // 2048 x 768, 1 / 8 / 32 tokens take 22 / 54 / 104 us as it is, 27 / 71 / 142 with
-// levels of a high and a low bf16 part (twice the lookups' bytes and mmas), 25 / 60
-// / 114 with fp16 levels (x and h scaled into fp16's range by powers of two, more
+// levels of a high and a low bf16 part (twice the lookups' bytes and mmas), 24 / 57
+// / 113 with fp16 levels (x and h scaled into fp16's range by powers of two, more
 // registers than there are).
 constexpr float kLevelScale = 1.437f;
 
