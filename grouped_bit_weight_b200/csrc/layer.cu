@@ -496,8 +496,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const LayerArgs a, co
     };
     for (;;) {
       // a lane has loaded its last share, and the others have begun that one:
-      // claim the next (all of phase A before any of phase B)
-      if (kind != 2 && misc[2] >= known && __any_sync(0xffffffffu, !ended && !busy && mine + 1 == known)) {
+      // claim the next (all of phase A before any of phase B).  Every lane votes,
+      // whatever it reads of the others' progress.
+      const bool next_due = misc[2] >= known && !ended && !busy && mine + 1 == known;
+      if (kind != 2 && __any_sync(0xffffffffu, next_due)) {
         int idx = 0;
         if (kind < 0) {
           kind = 0;
